@@ -45,30 +45,30 @@ def _ffn(name, s, m, n, e, k, dtype, act="silu", bias=True):
 def listed():
     return [
         # a small router's training step, where launches and host time are the cost
-        _balance("balance, 256 tokens", 256, 8, 2),
+        _balance("balance 256 tokens", 256, 8, 2),
         # the router of a large training batch
-        _balance("balance, 32768 tokens", 32768, 128, 8),
+        _balance("balance 32768 tokens", 32768, 128, 8),
         # packed sequences of different lengths with padded tokens, a loss for each sequence
-        _balance("balance, packed and masked", 16381, 60, 4, groups=29, masked=True),
+        _balance("balance packed and masked", 16381, 60, 4, groups=29, masked=True),
         # many small experts
-        _balance("balance, 512 experts", 65536, 512, 10),
+        _balance("balance 512 experts", 65536, 512, 10),
         # decoding: one token's up projection, where the weights of its 8 experts are what is read
-        _gemm("decode, one token", 1, 4096, 1536, 128, 8, "bf16", act="silu", gated=True),
+        _gemm("decode one token", 1, 4096, 1536, 128, 8, "bf16", act="silu", gated=True),
         # decoding a batch: the down projection, weighted, over rows that the up projection left
-        _gemm("decode, 24 tokens, down", 24, 1408, 2816, 64, 6, "f16", bias="own", weighted=True, gather=False),
+        _gemm("decode 24 tokens down", 24, 1408, 2816, 64, 6, "f16", bias="own", weighted=True, gather=False),
         # prompts: up projection of 4096 tokens
-        _gemm("prompt, 4096 tokens", 4096, 2816, 1408, 128, 8, "bf16", act="silu", gated=True),
+        _gemm("prompt 4096 tokens", 4096, 2816, 1408, 128, 8, "bf16", act="silu", gated=True),
         # the largest: a training batch's up projection with the values before the activation kept
-        _gemm("training batch, gated", 8192, 4096, 2048, 128, 8, "bf16", act="silu", gated=True, bias="own", save=True),
+        _gemm("training batch gated", 8192, 4096, 2048, 128, 8, "bf16", act="silu", gated=True, bias="own", save=True),
         # capacity-bounded routing with drops, bias, exact gelu and the tokens' own rows added
-        _gemm("capacity, gelu, residual", 16384, 1024, 1024, 64, 4, "f16", act="gelu", bias="f32",
+        _gemm("capacity gelu residual", 16384, 1024, 1024, 64, 4, "f16", act="gelu", bias="f32",
               residual="tokens", capacity=1024, hot=True),
         # odd sizes: ragged row and column tiles, padded segments, more experts than a power of two
-        _gemm("ragged, relu", 777, 264, 200, 129, 5, "bf16", act="relu", bias="f32", weighted=True,
+        _gemm("ragged relu", 777, 264, 200, 129, 5, "bf16", act="relu", bias="f32", weighted=True,
               residual="rows", pad=16),
         # training steps of the whole expert layer: a small one and an ordinary one
-        _ffn("layer step, 1000 tokens", 1000, 520, 264, 16, 2, "bf16", act="gelu_tanh"),
-        _ffn("layer step, 8192 tokens", 8192, 2048, 1408, 64, 6, "bf16", bias=False),
+        _ffn("layer step 1000 tokens", 1000, 520, 264, 16, 2, "bf16", act="gelu_tanh"),
+        _ffn("layer step 8192 tokens", 8192, 2048, 1408, 64, 6, "bf16", bias=False),
     ]
 
 
