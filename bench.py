@@ -58,6 +58,9 @@ ISOLATED_RUNS = 30  # each op of the step alone after a flush
 GEMM_SOURCES = ("gemm.hip", "gemm_bwd.hip", "gemm_common.h")
 # host code only (argument checks, the workspace plan, the C declarations): no kernel
 HOST_SOURCES = ("api.hip", "moe_gate.h")
+# kernels that no step of this benchmark launches: the balance loss and the expert
+# products with an epilogue
+OTHER_SOURCES = ("ops.h", "balance.hip", "expert_act.hip", "expert_act_bwd.hip")
 
 
 _COMMENT = re.compile(rb"//[^\n]*|/\*.*?\*/", re.S)
@@ -73,14 +76,14 @@ def source_code_bytes(text: bytes) -> bytes:
 def kernel_source_digest(variant: str | None = None) -> str:
     """sha256 over the code of the HIP sources (and the build flags) whose kernels a run
     of `variant` launches: every kernel source for the expert_gemm variant, all but the
-    GEMM's otherwise. Host-only files are left out, and so are comments and layout:
-    neither changes a kernel's traffic."""
+    GEMM's otherwise. Host-only files and kernels that no step launches are left out, and
+    so are comments and layout: none changes a measured kernel's traffic."""
     import hashlib
     from combine_moe_gate_amd import _build
     h = hashlib.sha256()
     for path in sorted(_build.SOURCES + _build.HEADERS):
         name = os.path.basename(path)
-        if name in HOST_SOURCES or (variant != "expert_gemm" and name in GEMM_SOURCES):
+        if name in HOST_SOURCES + OTHER_SOURCES or (variant != "expert_gemm" and name in GEMM_SOURCES):
             continue
         with open(path, "rb") as f:
             h.update(source_code_bytes(f.read()))

@@ -13,6 +13,8 @@ function names are those of the C ABI in include/moe_gate.h:
     gx      = moe_dispatch_backward(layout, grad_out)
     gl      = moe_gate_topk_backward(idx, w, gw, e)
     flags, checksum = moe_layout_read(layout)              # synchronises; tests/debug
+    counts, tokens, probs, loss, z = moe_balance_loss(logits, idx, mask, groups)
+    gl      = moe_balance_loss_backward(logits, counts, tokens, k, grad_loss, grad_z, mask, groups)
 
 There is no CPU fallback: without the built library, or without a GPU, every
 call raises.
@@ -104,6 +106,10 @@ _SIGNATURES = {
     "moe_dispatch_backward": (ctypes.c_int, [ctypes.POINTER(LayoutStruct), _P, _I, ctypes.c_int,
                                              _P, _P]),
     "moe_layout_read": (ctypes.c_int, [ctypes.POINTER(LayoutStruct), _P, _P, _P]),
+    "moe_balance_workspace_bytes": (ctypes.c_size_t, [_I, _I, _I]),
+    "moe_balance_loss": (ctypes.c_int, [_P, _P, _P, _P, _I, _I, _I, _I, _P, _P, _P, _P, _P, _P, ctypes.c_size_t,
+                                        _P]),
+    "moe_balance_loss_backward": (ctypes.c_int, [_P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _P, _P]),
     "moe_dispatch_layout_static_scratch": (ctypes.c_int, [_P, _I, _I, _I, _I, ctypes.POINTER(LayoutOptions), _P,
                                                           ctypes.c_size_t, ctypes.POINTER(LayoutStruct), _P]),
 }
@@ -128,7 +134,11 @@ def lib() -> ctypes.CDLL:
             raise RuntimeError(f"{LIB_PATH} implements ABI version {built}, this binding expects "
                                f"{ABI_VERSION}: rebuild it (python -m combine_moe_gate_amd._build)")
         for name, (res, args) in _SIGNATURES.items():
-            fn = getattr(handle, name)
+            try:
+                fn = getattr(handle, name)
+            except AttributeError:  # built before the function was added
+                raise RuntimeError(f"{LIB_PATH} has no {name}: rebuild it "
+                                   "(python -m combine_moe_gate_amd._build)") from None
             fn.restype = res
             fn.argtypes = args
         _lib = handle
@@ -487,6 +497,91 @@ def moe_renormalize_kept_backward(layout: Layout, w: torch.Tensor, grad_out: tor
     return gw
 
 
+def _launch(t: torch.Tensor, fn, *args) -> None:
+    """fn(*args, current stream of t's device), with that device current (a launch goes to
+    the current device's stream); its status checked."""
+    if torch.cuda.current_device() == t.get_device():
+        _check(fn(*args, _stream(t)))
+    else:
+        with torch.cuda.device(t.device):
+            _check(fn(*args, _stream(t)))
+
+
+def _one_device(*tensors) -> None:
+    _require_gpu(*tensors)
+    devices = {t.device for t in tensors if t is not None}
+    if len(devices) > 1:
+        raise ValueError(f"all tensors must be on one device, got {sorted(map(str, devices))}")
+
+
+def _group_count(mask, groups, s: int) -> int:
+    _expect(mask, "mask", (s,), (torch.bool, torch.uint8))
+    _expect(groups, "groups", (None,), torch.int32)
+    if groups is None:
+        return 1
+    if groups.numel() < 2:
+        raise ValueError(f"groups must hold at least two offsets, got {groups.numel()}")
+    return groups.numel() - 1
+
+
+def moe_balance_loss(logits: torch.Tensor, idx: torch.Tensor, mask=None, groups=None, workspace=None, out=None):
+    """Load-balance loss, z loss and per-expert counts of a router.
+
+    logits [s, e] float32 and the routes' expert ids idx [s, k] int32; mask [s] bool or
+    uint8, 0 for padded tokens; groups [g + 1] int32 offsets of packed sequences (without
+    it, one group of all tokens). Returns (counts [g, e] int32, tokens [g] int32, probs
+    [g, e], loss [g], z [g] float32): per group of n unpadded tokens, with p the softmax of
+    the logits over all experts, probs = mean p, loss = e/k sum_x counts_x/n probs_x and z =
+    mean logsumexp^2. out: the five tensors to write to.
+    """
+    _expect(logits, "logits", (None, None), torch.float32)
+    s, e = logits.shape
+    _expect(idx, "idx", (s, None), torch.int32)
+    k = idx.shape[1]
+    g = _group_count(mask, groups, s)
+    _expect(workspace, "workspace", (None,), torch.uint8)
+    if out is not None:
+        if len(out) != 5:
+            raise ValueError(f"out must be (counts, tokens, probs, loss, z), got {len(out)} values")
+        for t, name, shape, dt in zip(out, ("counts", "tokens", "probs", "loss", "z"),
+                                      ((g, e), (g,), (g, e), (g,), (g,)), (torch.int32,) * 2 + (torch.float32,) * 3):
+            if t is None:
+                raise ValueError(f"out: {name} is None")
+            _expect(t, name, shape, dt)
+    _one_device(logits, idx, mask, groups, workspace, *(out or ()))
+    dev = logits.device
+    if out is None:
+        out = (torch.empty((g, e), dtype=torch.int32, device=dev), torch.empty(g, dtype=torch.int32, device=dev),
+               torch.empty((g, e), dtype=torch.float32, device=dev), torch.empty(g, dtype=torch.float32, device=dev),
+               torch.empty(g, dtype=torch.float32, device=dev))
+    if workspace is None:
+        workspace = torch.empty(lib().moe_balance_workspace_bytes(s, e, g), dtype=torch.uint8, device=dev)
+    _launch(logits, lib().moe_balance_loss, _ptr(logits), _ptr(idx), _ptr(mask), _ptr(groups), s, e, k, g,
+            *(_ptr(t) for t in out), _ptr(workspace), workspace.numel())
+    return tuple(out)
+
+
+def moe_balance_loss_backward(logits: torch.Tensor, counts: torch.Tensor, tokens: torch.Tensor, k: int, grad_loss,
+                              grad_z=None, mask=None, groups=None, out=None):
+    """Gradient [s, e] of moe_balance_loss with respect to the logits, for gradients
+    grad_loss and grad_z [g] float32 (either may be None) of its two losses; counts and
+    tokens are what it returned, k the routes per token. Padded tokens, and tokens in no
+    group, get zeros."""
+    _expect(logits, "logits", (None, None), torch.float32)
+    s, e = logits.shape
+    g = _group_count(mask, groups, s)
+    _expect(counts, "counts", (g, e), torch.int32)
+    _expect(tokens, "tokens", (g,), torch.int32)
+    _expect(grad_loss, "grad_loss", (g,), torch.float32)
+    _expect(grad_z, "grad_z", (g,), torch.float32)
+    _expect(out, "out", (s, e), torch.float32)
+    _one_device(logits, counts, tokens, grad_loss, grad_z, mask, groups, out)
+    gl = out if out is not None else torch.empty((s, e), dtype=torch.float32, device=logits.device)
+    _launch(logits, lib().moe_balance_loss_backward, _ptr(logits), _ptr(mask), _ptr(groups), _ptr(counts), _ptr(tokens),
+            _ptr(grad_loss), _ptr(grad_z), s, e, k, g, _ptr(gl))
+    return gl
+
+
 def moe_layout_read(layout: Layout):
     flags = ctypes.c_int32(0)
     checksum = ctypes.c_uint64(0)
@@ -499,6 +594,7 @@ __all__ = [
     "moe_gate_topk", "moe_gate_topk_backward", "moe_dispatch_layout", "moe_dispatch",
     "moe_dispatch_replay", "moe_combine", "moe_combine_backward", "moe_dispatch_backward",
     "moe_layout_read", "moe_dispatch_weighted", "moe_dispatch_weighted_backward",
-    "moe_renormalize_kept", "moe_renormalize_kept_backward", "moe_expert_gemm", "moe_expert_gemm_wgrad", "moe_expert_gemm_dgrad", "workspace_bytes", "Layout",
+    "moe_renormalize_kept", "moe_renormalize_kept_backward", "moe_expert_gemm", "moe_expert_gemm_wgrad", "moe_expert_gemm_dgrad",
+    "moe_balance_loss", "moe_balance_loss_backward", "workspace_bytes", "Layout",
     "LayoutOptions", "MoeError", "lib", "EXPORTS",
 ]

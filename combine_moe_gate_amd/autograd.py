@@ -32,9 +32,10 @@ from __future__ import annotations
 
 import torch
 import torch.utils.checkpoint
+from torch.autograd.function import once_differentiable
 
-from . import (FLAG_REPLAY_MISMATCH, Layout, moe_combine, moe_combine_backward, moe_dispatch,
-               moe_dispatch_backward, moe_dispatch_layout, moe_dispatch_replay,
+from . import (FLAG_REPLAY_MISMATCH, Layout, moe_balance_loss, moe_balance_loss_backward, moe_combine,
+               moe_combine_backward, moe_dispatch, moe_dispatch_backward, moe_dispatch_layout, moe_dispatch_replay,
                moe_dispatch_weighted, moe_dispatch_weighted_backward, moe_expert_gemm,
                moe_expert_gemm_dgrad, moe_expert_gemm_wgrad, moe_gate_topk,
                moe_gate_topk_backward, moe_layout_read, moe_renormalize_kept,
@@ -155,6 +156,27 @@ class _Sum(torch.autograd.Function):
     @staticmethod
     def backward(ctx, g_y):
         return moe_dispatch(ctx.layout, g_y.contiguous()), None
+
+
+class _Balance(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, logits, idx, mask, groups):
+        logits = logits.contiguous()
+        counts, tokens, _, loss, z = moe_balance_loss(logits, idx, mask, groups)
+        ctx.save_for_backward(logits, counts, tokens, mask, groups)
+        ctx.k = idx.shape[1]
+        ctx.mark_non_differentiable(counts)
+        ctx.set_materialize_grads(False)
+        return loss, z, counts
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, g_loss, g_z, _g_counts):
+        logits, counts, tokens, mask, groups = ctx.saved_tensors
+        if g_loss is None and g_z is None:
+            return None, None, None, None
+        g_loss, g_z = (None if g is None else g.float().contiguous() for g in (g_loss, g_z))
+        return moe_balance_loss_backward(logits, counts, tokens, ctx.k, g_loss, g_z, mask, groups), None, None, None
 
 
 class _Renormalize(torch.autograd.Function):
@@ -292,6 +314,15 @@ def route(logits: torch.Tensor, k: int, recorder: LayoutRecorder | None = None):
     return _Gate.apply(logits, k)
 
 
+def balance_loss(logits: torch.Tensor, idx: torch.Tensor, mask: torch.Tensor | None = None,
+                 groups: torch.Tensor | None = None):
+    """(loss [g], z [g], counts [g, e]) of a router's logits and the ids route() chose: the
+    load-balance loss e/k sum_x (counts_x/n) mean_t p_tx and the z loss mean_t logsumexp^2,
+    for each group of packed tokens (without groups, one of all), padded tokens (mask 0)
+    left out. Both losses carry a gradient to the logits; the counts carry none."""
+    return _Balance.apply(logits, idx, mask, groups)
+
+
 def layout(idx: torch.Tensor, e: int, capacity: int = 0, recorder: LayoutRecorder | None = None,
            route_major: bool = False, pad_multiple: int = 1):
     """The dispatch layout (recorded or replayed through `recorder` if given)."""
@@ -354,5 +385,5 @@ def checkpoint(fn, *args, verify: bool = True, **kwargs):
     return out, rec
 
 
-__all__ = ["route", "layout", "dispatch", "dispatch_on", "combine", "renormalize", "expert_linear", "checkpoint",
+__all__ = ["route", "balance_loss", "layout", "dispatch", "dispatch_on", "combine", "renormalize", "expert_linear", "checkpoint",
            "LayoutRecorder"]

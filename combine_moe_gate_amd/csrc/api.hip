@@ -10,6 +10,7 @@
 #include "../../include/moe_gate.h"
 #include "internal.h"
 #include "moe_device.h"
+#include "ops.h"
 
 namespace {
 
@@ -642,6 +643,68 @@ moe_status_t moe_dispatch_backward(const moe_layout_t* layout, const void* grad_
   return hip_status(moe::launch_combine(v, grad_out, nullptr, rc, static_cast<int>(dtype), grad_x,
                                         static_cast<hipStream_t>(stream)),
                     "moe_dispatch_backward");
+}
+
+static moe_status_t check_balance(int32_t s, int32_t e, int32_t k, int32_t g, const int32_t* groups) {
+  MOE_TRY(check_sizes(s, e, k, 0));
+  if (g < 1) return fail(MOE_ERR_INVALID_ARG, "g must be >= 1 (got %d)", g);
+  if (groups == nullptr && g != 1)
+    return fail(MOE_ERR_INVALID_ARG, "g=%d groups need their offsets (groups is NULL)", g);
+  const moe::BalancePlan p = moe::balance_plan(s, e, g);
+  if (static_cast<int64_t>(g) * p.chunks > INT32_MAX || p.slots > INT32_MAX)
+    return fail(MOE_ERR_UNSUPPORTED, "g=%d groups of e=%d experts exceed one launch", g, e);
+  return MOE_OK;
+}
+
+size_t moe_balance_workspace_bytes(int32_t s, int32_t e, int32_t g) {
+  if (s < 0 || e < 1 || e > MOE_MAX_EXPERTS || g < 1 || s > INT32_MAX - 65536) return 0;
+  return moe::balance_plan(s, e, g).bytes;
+}
+
+moe_status_t moe_balance_loss(const float* logits, const int32_t* topk_idx,
+                              const uint8_t* token_mask, const int32_t* groups, int32_t s,
+                              int32_t e, int32_t k, int32_t g, int32_t* counts, int32_t* tokens,
+                              float* probs, float* loss, float* z, void* workspace,
+                              size_t workspace_bytes, void* stream) {
+  MOE_TRY(check_balance(s, e, k, g, groups));
+  MOE_TRY(check_array(logits, s, "logits", false));
+  MOE_TRY(check_array(topk_idx, s, "topk_idx", false));
+  MOE_TRY(check_array(counts, g, "counts", false));
+  MOE_TRY(check_array(tokens, g, "tokens", false));
+  MOE_TRY(check_array(probs, g, "probs", false));
+  MOE_TRY(check_array(loss, g, "loss", false));
+  MOE_TRY(check_array(z, g, "z", false));
+  if (workspace == nullptr) return fail(MOE_ERR_INVALID_ARG, "workspace is NULL");
+  if ((reinterpret_cast<uintptr_t>(workspace) & (kAlign - 1)) != 0)
+    return fail(MOE_ERR_MISALIGNED, "workspace is not %zu-byte aligned", kAlign);
+  const moe::BalancePlan p = moe::balance_plan(s, e, g);
+  if (workspace_bytes < p.bytes)
+    return fail(MOE_ERR_WORKSPACE, "workspace has %zu bytes, the balance loss needs %zu", workspace_bytes, p.bytes);
+  const moe::BalanceArgs a{logits, topk_idx, token_mask, groups, s, e, k, g};
+  return hip_status(moe::launch_balance_loss(a, p, static_cast<char*>(workspace), counts, tokens, probs, loss, z,
+                                             static_cast<hipStream_t>(stream)),
+                    "moe_balance_loss");
+}
+
+moe_status_t moe_balance_loss_backward(const float* logits, const uint8_t* token_mask,
+                                       const int32_t* groups, const int32_t* counts,
+                                       const int32_t* tokens, const float* grad_loss,
+                                       const float* grad_z, int32_t s, int32_t e, int32_t k,
+                                       int32_t g, float* grad_logits, void* stream) {
+  MOE_TRY(check_balance(s, e, k, g, groups));
+  MOE_TRY(check_array(logits, s, "logits", false));
+  MOE_TRY(check_array(counts, s, "counts", false));
+  MOE_TRY(check_array(tokens, s, "tokens", false));
+  MOE_TRY(check_array(grad_logits, s, "grad_logits", false));
+  const char* in = reinterpret_cast<const char*>(logits);
+  const char* out = reinterpret_cast<const char*>(grad_logits);
+  const size_t bytes = static_cast<size_t>(s) * e * 4;
+  if (s > 0 && in < out + bytes && out < in + bytes)
+    return fail(MOE_ERR_INVALID_ARG, "grad_logits may not overlap logits");
+  const moe::BalanceArgs a{logits, nullptr, token_mask, groups, s, e, k, g};
+  return hip_status(moe::launch_balance_loss_backward(a, counts, tokens, grad_loss, grad_z, grad_logits,
+                                                      static_cast<hipStream_t>(stream)),
+                    "moe_balance_loss_backward");
 }
 
 moe_status_t moe_layout_read(const moe_layout_t* layout, int32_t* flags_host,

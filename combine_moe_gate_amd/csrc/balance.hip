@@ -1,0 +1,541 @@
+// The router's load-balance loss, z loss and per-expert counts on gfx950, and their
+// gradient with respect to the logits.
+//
+// For the tokens V_g of group g (a packed sequence, or the whole batch) that are not
+// padding, n = |V_g|, with p_t = softmax(l_t) over all e experts and c_x the number of
+// V_g's valid routes that name expert x:
+//     P_x  = (1 / n) sum_t p_tx
+//     loss = (e / k) sum_x (c_x / n) P_x           (1 where the load is level)
+//     z    = (1 / n) sum_t logsumexp(l_t)^2
+//     d/dl_ti = p_ti [ gL e / (k n^2) (c_i - sum_x p_tx c_x) + gZ (2 / n) logsumexp(l_t) ]
+// The counts carry no gradient (they are whole numbers). As sum_x p_tx = 1, the bracket
+// keeps its value when every c_x is shifted alike: the kernel uses c_x - k n / e, whose
+// differences survive float32 where those of the counts themselves would not.
+//
+// Both directions stream the logits once (the backward forms the softmax again: reading
+// 4 e bytes per token costs what a saved copy would) and are bound by that traffic.
+//
+// A token's row lies across LPT lanes (4, 16 or a whole wave, the fewest that hold e at
+// four to sixteen values a lane), so a lane keeps the same experts for all its tokens and
+// the column sums P stay in its registers over the tile. One softmax needs a maximum and
+// a sum over the LPT lanes, DPP steps without LDS. Tiles are contiguous tokens; a tile
+// adds up its waves' sums in a fixed order and writes one partial row per group it meets,
+// and a second launch adds the partial rows of each group, in float64 and tile order.
+// Nothing depends on an order of arrival: the only atomics are the LDS integer counts.
+#include <type_traits>
+
+#include "moe_device.h"
+#include "ops.h"
+
+namespace moe {
+
+constexpr int kBalBlock = 512;  // threads per workgroup of both directions
+constexpr int kBalWaves = kBalBlock / kWave;
+constexpr int kBalTiles = 512;  // most tiles: two workgroups per CU
+constexpr int kBalMinTile = 32;
+constexpr int kBalChunk = 128;  // experts per workgroup of the second launch
+// Batches of up to this many logits are one tile, finished by the first launch alone.
+constexpr int64_t kBalSingle = 16384;
+
+BalancePlan balance_plan(int32_t s, int32_t e, int32_t g) {
+  BalancePlan p{};
+  if (g == 1 && static_cast<int64_t>(s) * e <= kBalSingle) {
+    p.tile = s > 0 ? s : 1;
+  } else {
+    p.tile = (s + kBalTiles - 1) / kBalTiles;
+    if (p.tile < kBalMinTile) p.tile = kBalMinTile;
+  }
+  p.ntiles = s > 0 ? (s - 1) / p.tile + 1 : 1;
+  p.pitch = (e + 3) / 4 * 4;
+  p.chunks = (e + kBalChunk - 1) / kBalChunk;
+  p.slots = static_cast<int64_t>(p.ntiles) + g - 1;
+  size_t at = 0;
+  auto take = [&](size_t n) {
+    const size_t here = at;
+    at = (at + n + 255) / 256 * 256;
+    return here;
+  };
+  p.off_probs = take(static_cast<size_t>(p.slots) * p.pitch * 4);
+  p.off_counts = take(static_cast<size_t>(p.slots) * p.pitch * 4);
+  p.off_z = take(static_cast<size_t>(p.slots) * 8);
+  p.off_tokens = take(static_cast<size_t>(p.slots) * 4);
+  p.off_dots = take(static_cast<size_t>(g) * p.chunks * 8);
+  p.bytes = at;
+  return p;
+}
+
+// ---------------------------------------------------------------------------------
+// reductions over the LPT lanes that share a token (every lane of the wave active)
+
+template <int CTRL>
+__device__ __forceinline__ float dpp_move(float v) {
+  return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), CTRL, 0xf, 0xf, false));
+}
+
+template <int LPT, class Op>
+__device__ __forceinline__ float lanes_reduce(float v, Op op) {
+  static_assert(LPT == 4 || LPT == 16 || LPT == 64, "a quad, a row or the wave");
+  v = op(v, dpp_move<0xb1>(v));  // quad_perm [1,0,3,2]
+  v = op(v, dpp_move<0x4e>(v));  // quad_perm [2,3,0,1]
+  if constexpr (LPT >= 16) {
+    v = op(v, dpp_move<0x141>(v));  // row_half_mirror
+    v = op(v, dpp_move<0x140>(v));  // row_mirror
+  }
+  if constexpr (LPT == 64) {
+    auto at = [&](int l) { return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), l)); };
+    const float a = at(0), b = at(16), c = at(32), d = at(48);
+    v = op(op(a, b), op(c, d));
+  }
+  return v;
+}
+
+template <int LPT>
+__device__ __forceinline__ float lanes_max(float v) {
+  return lanes_reduce<LPT>(v, [](float a, float b) { return fmaxf(a, b); });
+}
+template <int LPT>
+__device__ __forceinline__ float lanes_sum(float v) {
+  return lanes_reduce<LPT>(v, [](float a, float b) { return a + b; });
+}
+
+// The group that holds token t: the last one that starts at or before it (-1: none does).
+// Offsets that are no rising sequence give some group in range.
+__device__ __forceinline__ int group_at(const int32_t* __restrict__ groups, int g, int t) {
+  int lo = -1, hi = g;  // groups[lo] <= t < groups[hi], with the ends outside
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) / 2;
+    if (groups[mid] <= t) lo = mid;
+    else hi = mid;
+  }
+  return lo;
+}
+
+// Column i of lane r: four neighbouring experts per 16-byte load where rows allow them
+// (VEC), else experts r, r + LPT, ... so that a load's lanes are neighbours.
+template <int LPT, bool VEC>
+__device__ __forceinline__ int column(int r, int i) {
+  return VEC ? 4 * (r + LPT * (i / 4)) + i % 4 : r + LPT * i;
+}
+
+template <int LPT, int NV, bool VEC>
+__device__ __forceinline__ void load_row(const float* __restrict__ row, int e, int r, bool live, float (&v)[NV]) {
+#pragma unroll
+  for (int i = 0; i < NV; i += VEC ? 4 : 1) {
+    const int c = column<LPT, VEC>(r, i);
+    const bool in = live && c < e;
+    if constexpr (VEC) {
+      const chunk_t none = {0xff800000u, 0xff800000u, 0xff800000u, 0xff800000u};  // -inf
+      chunk_t q = none;
+      if (in) q = *reinterpret_cast<const chunk_t*>(row + c);
+#pragma unroll
+      for (int u = 0; u < 4; ++u) v[i + u] = __uint_as_float(q[u]);
+    } else {
+      v[i] = in ? row[c] : -INFINITY;
+    }
+  }
+}
+
+// exp(x) for x <= 0 through the hardware's base-2 exponential: a relative error of about
+// 2^-23 + |x| 2^-24, against probabilities whose sum is kept to float32.
+__device__ __forceinline__ float exp_neg(float x) { return __builtin_amdgcn_exp2f(x * 1.4426950408889634f); }
+
+// Softmax of one row in place: v becomes exp(v - top) and the row's 1 / sum and logsumexp
+// come back (both 0 where every logit is -inf: such a token has no distribution and adds
+// nothing). NaN and +inf logits make both NaN.
+template <int LPT, int NV>
+__device__ __forceinline__ void row_softmax(float (&v)[NV], float* inv, float* lse) {
+  float top = v[0];
+#pragma unroll
+  for (int i = 1; i < NV; ++i) top = fmaxf(top, v[i]);
+  top = lanes_max<LPT>(top);
+  const float base = top == -INFINITY ? 0.0f : top;
+  float sum = 0.0f;
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    v[i] = exp_neg(v[i] - base);
+    sum += v[i];
+  }
+  sum = lanes_sum<LPT>(sum);
+  const bool none = sum == 0.0f;
+  *inv = none ? 0.0f : 1.0f / sum;
+  *lse = none ? 0.0f : base + __logf(sum);
+}
+
+// ---------------------------------------------------------------------------------
+// forward, first launch: one workgroup per tile
+
+// Sum over the workgroup, in lane and wave order; every thread gets it. `red` holds a
+// value per wave.
+template <class T>
+__device__ __forceinline__ T block_sum(T v, T* red) {
+#pragma unroll
+  for (int o = 1; o < kWave; o <<= 1) v += __shfl_xor(v, o, kWave);
+  __syncthreads();
+  if (lane_id() == 0) red[wave_in_block()] = v;
+  __syncthreads();
+  T total = red[0];
+  for (int w = 1; w < static_cast<int>(blockDim.x) / kWave; ++w) total += red[w];
+  return total;
+}
+
+struct BalanceOut {
+  int32_t* counts;  // [g, e]
+  int32_t* tokens;  // [g]
+  float* probs;     // [g, e]
+  float* loss;      // [g]
+  float* z;         // [g]
+};
+
+struct BalancePartials {
+  float* probs;     // [slots, pitch]
+  int32_t* counts;  // [slots, pitch]
+  double* z;        // [slots]
+  int32_t* tokens;  // [slots]
+  double* dots;     // [g, chunks]
+};
+
+template <int LPT, int NV, bool VEC>
+__global__ __launch_bounds__(kBalBlock) void balance_tile_kernel(BalanceArgs a, int tile, int pitch, bool single,
+                                                                 BalancePartials part, BalanceOut out) {
+  constexpr int kGroups = kBalBlock / LPT;  // tokens in work at once
+  constexpr int U = NV >= 16 ? 1 : 2;       // rows loaded ahead of the softmax
+  constexpr int kCols = LPT * NV;
+  __shared__ float sums[kBalWaves][kCols];
+  __shared__ int32_t hist[kCols];
+  __shared__ double red_z[kBalWaves];
+  __shared__ int32_t red_n[kBalWaves];
+  const int tid = threadIdx.x, lane = lane_id(), wv = wave_in_block();
+  const int r = tid % LPT, gid = tid / LPT;
+  const int t0 = blockIdx.x * tile;
+  const int t1 = a.s - t0 > tile ? t0 + tile : a.s;
+
+  int j = 0;
+  if (a.groups != nullptr) {
+    j = group_at(a.groups, a.g, t0);
+    if (j < 0) j = 0;
+  }
+  for (; j < a.g; ++j) {
+    int lo = t0, hi = t1;
+    if (a.groups != nullptr) {
+      const int first = a.groups[j], last = a.groups[j + 1];
+      if (first >= t1) break;
+      lo = first > t0 ? first : t0;
+      hi = last < t1 ? last : t1;
+    }
+    if (lo >= hi && !single) continue;  // uniform; a single tile finishes its group, empty or not
+    for (int c = tid; c < kCols; c += kBalBlock) hist[c] = 0;
+
+    float acc[NV];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) acc[i] = 0.0f;
+    double zacc = 0.0;
+    int count = 0;
+    for (int tb = lo; tb < hi; tb += U * kGroups) {  // the same trips for every lane
+      float v[U][NV];
+      bool live[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int t = tb + u * kGroups + gid;
+        live[u] = t < hi && (a.mask == nullptr || a.mask[t] != 0);
+        load_row<LPT, NV, VEC>(a.logits + static_cast<size_t>(t < hi ? t : lo) * a.e, a.e, r, live[u], v[u]);
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        float inv, lse;
+        row_softmax<LPT, NV>(v[u], &inv, &lse);  // a row that is not live is all -inf: adds nothing
+#pragma unroll
+        for (int i = 0; i < NV; ++i) acc[i] += v[u][i] * inv;
+        if (r == 0) {
+          zacc += static_cast<double>(lse) * static_cast<double>(lse);
+          count += live[u];
+        }
+      }
+    }
+    // the wave's token groups add up column by column, then the waves in order through LDS
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+#pragma unroll
+      for (int o = LPT; o < kWave; o <<= 1) acc[i] += __shfl_xor(acc[i], o, kWave);
+      if (lane < LPT) sums[wv][column<LPT, VEC>(r, i)] = acc[i];
+    }
+    const double zsum = block_sum(zacc, red_z);  // its barriers also order sums and hist
+    const int nsum = block_sum(count, red_n);
+    // the routes: valid ones are counted, a route naming no expert or one that an earlier
+    // route of its token named is not
+    for (int q = tid; q < (hi - lo) * a.k; q += kBalBlock) {
+      const int t = lo + q / a.k, jj = q % a.k;
+      if (a.mask != nullptr && a.mask[t] == 0) continue;
+      const int32_t* route = a.idx + static_cast<size_t>(t) * a.k;
+      const int x = route[jj];
+      bool ok = x >= 0 && x < a.e;
+      for (int p = 0; p < jj; ++p) ok = ok && route[p] != x;
+      if (ok) atomicAdd(&hist[x], 1);
+    }
+    __syncthreads();
+
+    if (!single) {
+      const size_t slot = static_cast<size_t>(blockIdx.x) + j;
+      for (int c = tid; c < pitch; c += kBalBlock) {
+        float sum = 0.0f;
+        for (int w = 0; w < kBalWaves; ++w) sum += sums[w][c];
+        part.probs[slot * pitch + c] = sum;
+        part.counts[slot * pitch + c] = hist[c];
+      }
+      if (tid == 0) {
+        part.z[slot] = zsum;
+        part.tokens[slot] = nsum;
+      }
+    } else {  // the only tile of the only group: finished here
+      const double n = nsum > 0 ? static_cast<double>(nsum) : 1.0;
+      double dot = 0.0;
+      for (int c = tid; c < a.e; c += kBalBlock) {
+        double sum = 0.0;
+        for (int w = 0; w < kBalWaves; ++w) sum += static_cast<double>(sums[w][c]);
+        const double p = sum / n;
+        out.probs[c] = static_cast<float>(p);
+        out.counts[c] = hist[c];
+        dot += static_cast<double>(hist[c]) * p;
+      }
+      dot = block_sum(dot, red_z);
+      if (tid == 0) {
+        out.tokens[0] = nsum;
+        out.z[0] = static_cast<float>(zsum / n);
+        out.loss[0] = static_cast<float>(dot * a.e / (static_cast<double>(a.k) * n));
+      }
+    }
+    __syncthreads();  // sums and hist are read out before the next group writes them
+  }
+}
+
+// Forward, second launch: workgroup (chunk, group) adds the group's partial rows over
+// kBalChunk experts: 32 lanes of four experts by 16 rows at a time, in float64, then the
+// 16 in order. With more than one chunk the chunks' shares of the loss meet in a third.
+__global__ __launch_bounds__(kBalBlock) void balance_reduce_kernel(BalanceArgs a, int tile, int ntiles, int pitch,
+                                                                   int chunks, BalancePartials part, BalanceOut out) {
+  constexpr int kRows = kBalBlock / 32;
+  __shared__ double psum[kRows][kBalChunk];
+  __shared__ int32_t csum[kRows][kBalChunk];
+  __shared__ double red_z[kBalWaves];
+  __shared__ int32_t red_n[kBalWaves];
+  const int tid = threadIdx.x, chunk = blockIdx.x % chunks, j = blockIdx.x / chunks;
+  int lo = 0, hi = a.s;
+  if (a.groups != nullptr) {
+    lo = a.groups[j] > 0 ? a.groups[j] : 0;
+    hi = a.groups[j + 1] < a.s ? a.groups[j + 1] : a.s;
+  }
+  const int64_t s0 = lo < hi ? lo / tile + static_cast<int64_t>(j) : 0;
+  const int ns = lo < hi ? (hi - 1) / tile - lo / tile + 1 : 0;
+
+  int count = 0;
+  double zacc = 0.0;
+  for (int i = tid; i < ns; i += kBalBlock) {
+    count += part.tokens[s0 + i];
+    zacc += part.z[s0 + i];
+  }
+  const int nsum = block_sum(count, red_n);
+  const double zsum = block_sum(zacc, red_z);
+  const double n = nsum > 0 ? static_cast<double>(nsum) : 1.0;
+
+  const int c4 = chunk * kBalChunk + 4 * (tid % 32), row = tid / 32;
+  double p[4] = {0.0, 0.0, 0.0, 0.0};
+  int32_t q[4] = {0, 0, 0, 0};
+  if (c4 < pitch) {
+#pragma unroll 4
+    for (int i = row; i < ns; i += kRows) {
+      const size_t at = static_cast<size_t>(s0 + i) * pitch + c4;
+      const chunk_t v = *reinterpret_cast<const chunk_t*>(part.probs + at);
+      const chunk_t w = *reinterpret_cast<const chunk_t*>(part.counts + at);
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        p[u] += static_cast<double>(__uint_as_float(v[u]));
+        q[u] += static_cast<int32_t>(w[u]);
+      }
+    }
+  }
+#pragma unroll
+  for (int u = 0; u < 4; ++u) {
+    psum[row][4 * (tid % 32) + u] = p[u];
+    csum[row][4 * (tid % 32) + u] = q[u];
+  }
+  __syncthreads();
+  double dot = 0.0;
+  const int c = chunk * kBalChunk + tid;
+  if (tid < kBalChunk && c < a.e) {
+    double sum = 0.0;
+    int32_t cnt = 0;
+    for (int w = 0; w < kRows; ++w) {
+      sum += psum[w][tid];
+      cnt += csum[w][tid];
+    }
+    sum /= n;
+    out.probs[static_cast<size_t>(j) * a.e + c] = static_cast<float>(sum);
+    out.counts[static_cast<size_t>(j) * a.e + c] = cnt;
+    dot = static_cast<double>(cnt) * sum;
+  }
+  dot = block_sum(dot, red_z);
+  if (tid == 0) {
+    if (chunk == 0) {
+      out.tokens[j] = nsum;
+      out.z[j] = static_cast<float>(zsum / n);
+    }
+    if (chunks == 1) out.loss[j] = static_cast<float>(dot * a.e / (static_cast<double>(a.k) * n));
+    else part.dots[static_cast<size_t>(j) * chunks + chunk] = dot;
+  }
+}
+
+__global__ __launch_bounds__(kBlock) void balance_finish_kernel(BalanceArgs a, int chunks, const double* __restrict__ dots,
+                                                                const int32_t* __restrict__ tokens,
+                                                                float* __restrict__ loss) {
+  const int j = blockIdx.x * kBlock + threadIdx.x;
+  if (j >= a.g) return;
+  double dot = 0.0;
+  for (int c = 0; c < chunks; ++c) dot += dots[static_cast<size_t>(j) * chunks + c];
+  const double n = tokens[j] > 0 ? static_cast<double>(tokens[j]) : 1.0;
+  loss[j] = static_cast<float>(dot * a.e / (static_cast<double>(a.k) * n));
+}
+
+// ---------------------------------------------------------------------------------
+// backward: the same lanes per token; a lane keeps its experts' shifted counts, scaled,
+// for as long as its tokens stay in one group
+
+template <int LPT, int NV, bool VEC>
+__global__ __launch_bounds__(kBalBlock) void balance_backward_kernel(
+    BalanceArgs a, int tile, const int32_t* __restrict__ counts, const int32_t* __restrict__ tokens,
+    const float* __restrict__ grad_loss, const float* __restrict__ grad_z, float* __restrict__ grad) {
+  constexpr int kGroups = kBalBlock / LPT;
+  constexpr int U = NV >= 16 ? 1 : 2;
+  const int tid = threadIdx.x;
+  const int r = tid % LPT, gid = tid / LPT;
+  const int t0 = blockIdx.x * tile;
+  const int t1 = a.s - t0 > tile ? t0 + tile : a.s;
+  int j = -1;          // the group whose numbers are held
+  float off[NV], zt = 0.0f;
+#pragma unroll
+  for (int i = 0; i < NV; ++i) off[i] = 0.0f;
+
+  for (int tb = t0; tb < t1; tb += U * kGroups) {
+    float v[U][NV];
+    bool live[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int t = tb + u * kGroups + gid;
+      live[u] = t < t1 && (a.mask == nullptr || a.mask[t] != 0);
+      load_row<LPT, NV, VEC>(a.logits + static_cast<size_t>(t < t1 ? t : t0) * a.e, a.e, r, live[u], v[u]);
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int t = tb + u * kGroups + gid;
+      int here = 0;
+      bool in = live[u];
+      if (a.groups != nullptr) {
+        here = j;
+        const bool kept = j >= 0 && t >= a.groups[j] && t < a.groups[j + 1];
+        if (!kept) here = group_at(a.groups, a.g, t);
+        in = in && here >= 0 && t < a.groups[here + 1 > 0 ? here + 1 : 0];
+      }
+      if (in && here != j) {
+        j = here;
+        const double n = tokens[j] > 0 ? static_cast<double>(tokens[j]) : 1.0;
+        const double mean = static_cast<double>(a.k) * n / a.e;
+        const double scale = static_cast<double>(grad_loss != nullptr ? grad_loss[j] : 0.0f) * a.e /
+                             (static_cast<double>(a.k) * n * n);
+        zt = grad_z != nullptr ? static_cast<float>(static_cast<double>(grad_z[j]) * 2.0 / n) : 0.0f;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+          const int c = column<LPT, VEC>(r, i);
+          off[i] = c < a.e ? static_cast<float>((static_cast<double>(counts[static_cast<size_t>(j) * a.e + c]) - mean) * scale)
+                           : 0.0f;
+        }
+      }
+      float inv, lse;
+      row_softmax<LPT, NV>(v[u], &inv, &lse);
+      float dot = 0.0f;
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        v[u][i] *= inv;
+        dot += v[u][i] * off[i];
+      }
+      dot = lanes_sum<LPT>(dot);
+      const float add = zt * lse - dot;
+      if (t < t1) {
+        float* row = grad + static_cast<size_t>(t) * a.e;
+#pragma unroll
+        for (int i = 0; i < NV; i += VEC ? 4 : 1) {
+          const int c = column<LPT, VEC>(r, i);
+          if constexpr (VEC) {
+            chunk_t q = {0u, 0u, 0u, 0u};
+#pragma unroll
+            for (int w = 0; w < 4; ++w)
+              if (in) q[w] = __float_as_uint(v[u][i + w] * (off[i + w] + add));
+            if (c < a.e) *reinterpret_cast<chunk_t*>(row + c) = q;
+          } else {
+            if (c < a.e) row[c] = in ? v[u][i] * (off[i] + add) : 0.0f;
+          }
+        }
+      }
+    }
+  }
+}
+
+// Calls f with the lanes per token, values per lane and load width that e and the rows'
+// alignment ask for.
+template <int LPT, int NV>
+struct Rows {
+  static constexpr int lpt = LPT, nv = NV;
+};
+template <class F>
+static void with_rows(int e, bool vec, F f) {
+  auto go = [&](auto shape) {
+    if (vec) f(shape, std::true_type{});
+    else f(shape, std::false_type{});
+  };
+  if (e <= 16) go(Rows<4, 4>{});
+  else if (e <= 64) go(Rows<16, 4>{});
+  else if (e <= 128) go(Rows<16, 8>{});
+  else if (e <= 256) go(Rows<64, 4>{});
+  else if (e <= 512) go(Rows<64, 8>{});
+  else go(Rows<64, 16>{});
+}
+
+static bool rows16(const void* p, int e) { return e % 4 == 0 && (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
+hipError_t launch_balance_loss(const BalanceArgs& a, const BalancePlan& p, char* ws, int32_t* counts, int32_t* tokens,
+                               float* probs, float* loss, float* z, hipStream_t stream) {
+  const BalanceOut out{counts, tokens, probs, loss, z};
+  const BalancePartials part{reinterpret_cast<float*>(ws + p.off_probs), reinterpret_cast<int32_t*>(ws + p.off_counts),
+                             reinterpret_cast<double*>(ws + p.off_z), reinterpret_cast<int32_t*>(ws + p.off_tokens),
+                             reinterpret_cast<double*>(ws + p.off_dots)};
+  // groups given by offsets may leave tokens out, so only a whole batch is finished at once
+  const bool single = p.ntiles == 1 && a.g == 1 && a.groups == nullptr;
+  with_rows(a.e, rows16(a.logits, a.e), [&](auto shape, auto vec) {
+    using S = decltype(shape);
+    balance_tile_kernel<S::lpt, S::nv, decltype(vec)::value>
+        <<<p.ntiles, kBalBlock, 0, stream>>>(a, p.tile, p.pitch, single, part, out);
+  });
+  hipError_t err = hipGetLastError();
+  if (err != hipSuccess || single) return err;
+  balance_reduce_kernel<<<static_cast<unsigned>(a.g) * p.chunks, kBalBlock, 0, stream>>>(a, p.tile, p.ntiles, p.pitch,
+                                                                                       p.chunks, part, out);
+  err = hipGetLastError();
+  if (err != hipSuccess || p.chunks == 1) return err;
+  balance_finish_kernel<<<(a.g + kBlock - 1) / kBlock, kBlock, 0, stream>>>(a, p.chunks, part.dots, tokens, loss);
+  return hipGetLastError();
+}
+
+hipError_t launch_balance_loss_backward(const BalanceArgs& a, const int32_t* counts, const int32_t* tokens,
+                                        const float* grad_loss, const float* grad_z, float* grad_logits,
+                                        hipStream_t stream) {
+  if (a.s == 0) return hipSuccess;
+  with_rows(a.e, rows16(a.logits, a.e) && rows16(grad_logits, a.e), [&](auto shape, auto vec) {
+    using S = decltype(shape);
+    constexpr int kAtOnce = kBalBlock / S::lpt * (S::nv >= 16 ? 1 : 2);
+    // whole rounds of tokens, up to 2048 workgroups
+    int tile = (a.s + 2047) / 2048;
+    tile = (tile + kAtOnce - 1) / kAtOnce * kAtOnce;
+    balance_backward_kernel<S::lpt, S::nv, decltype(vec)::value>
+        <<<(a.s - 1) / tile + 1, kBalBlock, 0, stream>>>(a, tile, counts, tokens, grad_loss, grad_z, grad_logits);
+  });
+  return hipGetLastError();
+}
+
+}  // namespace moe

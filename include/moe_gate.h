@@ -6,7 +6,9 @@
  *   (2) the dispatch layout: per-expert counts, token-order slots, capacity drop,
  *   (3) the permute of activation rows into an expert-grouped buffer,
  *   (4) the weighted combine of each token's expert outputs,
- *   (5) the backward passes, and a replay of (3) from a saved layout.
+ *   (5) the backward passes, and a replay of (3) from a saved layout,
+ * and what a layer built on it trains and computes with: the router's balance loss, and the
+ * experts' products (plain, or with bias, activation, route weight and residual applied).
  *
  * Sources, cited by page title and section:
  *   [DS-8195] DeepSpeed PR "MoE dispatch: fix silent Tutel + TP corruption, speed up
@@ -409,6 +411,53 @@ moe_status_t moe_expert_gemm_dgrad(const moe_layout_t* layout, const void* grad_
 moe_status_t moe_expert_gemm_wgrad(const moe_layout_t* layout, const void* a, int32_t gather,
                                    const void* grad_out, int32_t m, int32_t n, moe_dtype_t dtype,
                                    moe_dtype_t grad_w_dtype, void* grad_w, void* stream);
+
+/*
+ * Load-balance loss, z loss and per-expert counts of a router, for each group of tokens
+ * (a packed sequence, or the whole batch). Over the unpadded tokens V of group g, n = |V|,
+ * with p_t = softmax(logits_t) over all e experts:
+ *   counts[g,x] = routes (t, j), t in V, that name expert x (a route naming no expert in
+ *                 [0, e), or one an earlier route of its token named, is not counted: what
+ *                 moe_dispatch_layout counts before the capacity drop)
+ *   probs[g,x]  = (1/n) sum_t p_tx
+ *   loss[g]     = (e/k) sum_x (counts[g,x]/n) probs[g,x]       (1 where the load is level)
+ *   z[g]        = (1/n) sum_t (log sum_x exp(logits_tx))^2
+ *   tokens[g]   = n;  a group without tokens gets zeros.
+ *   logits     [s, e] float32;  topk_idx [s, k] int32
+ *   token_mask [s] bytes, 0 for a padded token (its logits and ids are not read), or NULL
+ *   groups     [g + 1] int32, group i holding tokens [groups[i], groups[i+1]); offsets rise
+ *              from >= 0 to <= s (tokens outside are in no group; offsets that fall give
+ *              unspecified results, never an access out of bounds); NULL (g = 1): all tokens
+ *   counts [g, e] int32, tokens [g] int32, probs [g, e], loss [g], z [g] float32: out
+ *   workspace  device buffer of moe_balance_workspace_bytes(s, e, g) bytes, 256-byte aligned
+ *              (not kept after the call; calls that may overlap in time need one each)
+ * Probabilities and their sums over a tile of tokens are float32, sums over tiles, the
+ * loss and z float64, rounded once. A token whose logits are all -inf has no distribution:
+ * it counts among the tokens, its routes are counted, and it adds 0 to probs and z. NaN or
+ * +inf in an unpadded token's logits makes probs, loss and z of its group NaN, no other's.
+ * One launch for a single group of up to 16384 logits, else two (three for e > 128).
+ */
+size_t moe_balance_workspace_bytes(int32_t s, int32_t e, int32_t g);
+moe_status_t moe_balance_loss(const float* logits, const int32_t* topk_idx,
+                              const uint8_t* token_mask, const int32_t* groups, int32_t s,
+                              int32_t e, int32_t k, int32_t g, int32_t* counts, int32_t* tokens,
+                              float* probs, float* loss, float* z, void* workspace,
+                              size_t workspace_bytes, void* stream);
+
+/*
+ * Gradient of moe_balance_loss with respect to the logits, for gradients grad_loss [g] and
+ * grad_z [g] (float32; NULL: none) of its two losses, given its counts and tokens:
+ *   grad_logits[t,i] = p_ti (grad_loss[g] e/(k n^2) (counts[g,i] - sum_x p_tx counts[g,x])
+ *                            + grad_z[g] (2/n) log sum_x exp(logits_tx))
+ * for a token t of group g; 0 for padded tokens and tokens in no group. [s, e] float32,
+ * every entry written; may not overlap logits. The counts are whole numbers and carry no
+ * gradient.
+ */
+moe_status_t moe_balance_loss_backward(const float* logits, const uint8_t* token_mask,
+                                       const int32_t* groups, const int32_t* counts,
+                                       const int32_t* tokens, const float* grad_loss,
+                                       const float* grad_z, int32_t s, int32_t e, int32_t k,
+                                       int32_t g, float* grad_logits, void* stream);
 
 /*
  * Read the layout's flags word and routing checksum into HOST memory. Synchronises

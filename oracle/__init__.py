@@ -55,3 +55,4 @@ from .moe import (  # noqa: F401
     FLAG_DUPLICATE_EXPERT,
     FLAG_REPLAY_MISMATCH,
 )
+from .router import Balance, balance_loss, balance_loss_backward  # noqa: F401
