@@ -60,7 +60,7 @@ GEMM_SOURCES = ("gemm.hip", "gemm_bwd.hip", "gemm_common.h")
 HOST_SOURCES = ("api.hip", "moe_gate.h")
 # kernels that no step of this benchmark launches: the balance loss and the expert
 # products with an epilogue
-OTHER_SOURCES = ("ops.h", "balance.hip", "expert_act.hip", "expert_act_bwd.hip")
+OTHER_SOURCES = ("ops.h", "balance.hip", "expert_act.h", "expert_act.hip", "expert_act_bwd.hip")
 
 
 _COMMENT = re.compile(rb"//[^\n]*|/\*.*?\*/", re.S)

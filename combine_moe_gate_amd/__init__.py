@@ -13,6 +13,8 @@ function names are those of the C ABI in include/moe_gate.h:
     gx      = moe_dispatch_backward(layout, grad_out)
     gl      = moe_gate_topk_backward(idx, w, gw, e)
     flags, checksum = moe_layout_read(layout)              # synchronises; tests/debug
+    h       = moe_expert_gemm_act(layout, x, weights, bias=b, act="silu", gated=True)
+    gz, gb, gw, gr = moe_expert_act_backward(layout, grad_h, preact, act="silu", gated=True)
     counts, tokens, probs, loss, z = moe_balance_loss(logits, idx, mask, groups)
     gl      = moe_balance_loss_backward(logits, counts, tokens, k, grad_loss, grad_z, mask, groups)
 
@@ -70,6 +72,15 @@ class LayoutOptions(ctypes.Structure):
     _fields_ = [("route_major", ctypes.c_int32), ("pad_multiple", ctypes.c_int32)]
 
 
+class Epilogue(ctypes.Structure):
+    """Mirror of moe_expert_epilogue_t."""
+    _fields_ = [("activation", ctypes.c_int32), ("gated", ctypes.c_int32), ("bias", ctypes.c_void_p),
+                ("bias_dtype", ctypes.c_int32), ("residual_gather", ctypes.c_int32), ("topk_w", ctypes.c_void_p),
+                ("residual", ctypes.c_void_p), ("preact", ctypes.c_void_p)]
+
+
+ACTIVATIONS = {"none": 0, "relu": 1, "gelu": 2, "gelu_tanh": 3, "silu": 4}
+
 _lib = None
 
 _P = ctypes.c_void_p
@@ -106,6 +117,11 @@ _SIGNATURES = {
     "moe_dispatch_backward": (ctypes.c_int, [ctypes.POINTER(LayoutStruct), _P, _I, ctypes.c_int,
                                              _P, _P]),
     "moe_layout_read": (ctypes.c_int, [ctypes.POINTER(LayoutStruct), _P, _P, _P]),
+    "moe_expert_gemm_act": (ctypes.c_int, [ctypes.POINTER(LayoutStruct), _P, _I, _P, _I, _I, ctypes.c_int,
+                                           ctypes.POINTER(Epilogue), _P, _P]),
+    "moe_expert_act_backward_workspace_bytes": (ctypes.c_size_t, [ctypes.POINTER(LayoutStruct), _I, _I]),
+    "moe_expert_act_backward": (ctypes.c_int, [ctypes.POINTER(LayoutStruct), _P, _P, _I, ctypes.c_int, _I, _I, _P, _P,
+                                               ctypes.c_int, _P, _P, _P, _P, ctypes.c_size_t, _P]),
     "moe_balance_workspace_bytes": (ctypes.c_size_t, [_I, _I, _I]),
     "moe_balance_loss": (ctypes.c_int, [_P, _P, _P, _P, _I, _I, _I, _I, _P, _P, _P, _P, _P, _P, ctypes.c_size_t,
                                         _P]),
@@ -477,6 +493,98 @@ def moe_expert_gemm_dgrad(layout: Layout, grad_out: torch.Tensor, weights: torch
     return out
 
 
+def _activation(act: str) -> int:
+    try:
+        return ACTIVATIONS[act]
+    except (KeyError, TypeError):
+        raise ValueError(f"act must be one of {', '.join(ACTIVATIONS)}, got {act!r}") from None
+
+
+_GEMM_DTYPES = (torch.bfloat16, torch.float16)
+
+
+def moe_expert_gemm_act(layout: Layout, a: torch.Tensor, weights: torch.Tensor, gather: bool = True, bias=None,
+                        act: str = "none", gated: bool = False, w=None, residual=None, residual_gather: bool = False,
+                        save_preact: bool = False, out=None, preact=None):
+    """Grouped expert product with an epilogue: for each placed row r of expert x, with
+    z = A(r) @ weights[x]^T + bias[x],
+        out[r] = w_r u + res(r),   u = act(z), or gated: u = act(z[:n]) * z[n:]
+    in float32, rounded once. [rows, n]; rows no route fills are zero.
+
+    a, gather and weights as in moe_expert_gemm; gated weights are [e, 2n, m], the n gate
+    rows first. bias [e, weight rows] float32 or a's dtype; act none, relu, gelu (exact),
+    gelu_tanh or silu; w [s, k] float32 scales a row by its route's weight; residual [rows,
+    n], or token rows [s, n] with residual_gather, is added last. With save_preact (or
+    preact given) returns (out, preact): z rounded, [rows, weight rows], for
+    moe_expert_act_backward.
+    """
+    _expect(a, "a", (layout.s if gather else layout.rows, None), _GEMM_DTYPES)
+    m = a.shape[1]
+    _expect(weights, "weights", (layout.e, None, m), a.dtype)
+    nz = weights.shape[1]
+    if gated and nz % 2:
+        raise ValueError(f"gated weights must have an even number of rows, got {nz}")
+    n = nz // 2 if gated else nz
+    _expect(bias, "bias", (layout.e, nz), (torch.float32, a.dtype))
+    code = _activation(act)
+    _expect(w, "w", (layout.s, layout.k), torch.float32)
+    _expect(residual, "residual", (layout.s if residual_gather else layout.rows, n), a.dtype)
+    _expect(out, "out", (layout.rows, n), a.dtype)
+    _expect(preact, "preact", (layout.rows, nz), a.dtype)
+    _same_device(layout, a, weights, bias, w, residual, out, preact)
+    if out is None:
+        out = torch.empty((layout.rows, n), dtype=a.dtype, device=a.device)
+    if save_preact and preact is None:
+        preact = torch.empty((layout.rows, nz), dtype=a.dtype, device=a.device)
+    ep = Epilogue(code, int(bool(gated)), bias.data_ptr() if bias is not None else None,
+                  _DTYPE_CODE[bias.dtype] if bias is not None else MOE_F32, int(bool(residual_gather)),
+                  w.data_ptr() if w is not None else None, residual.data_ptr() if residual is not None else None,
+                  preact.data_ptr() if preact is not None else None)
+    _launch(a, lib().moe_expert_gemm_act, layout.byref(), _ptr(a), int(bool(gather)), _ptr(weights), m, n,
+            _DTYPE_CODE[a.dtype], ctypes.byref(ep), _ptr(out))
+    return out if preact is None else (out, preact)
+
+
+def moe_expert_act_backward(layout: Layout, grad_out: torch.Tensor, preact=None, act: str = "none", gated: bool = False,
+                            w=None, need_preact: bool = True, bias_dtype=None, need_w: bool = False,
+                            need_residual: bool = False, workspace=None):
+    """Backward of moe_expert_gemm_act's epilogue: (grad_preact, grad_bias, grad_w,
+    grad_residual), None where not asked for.
+
+    grad_out [rows, n]; preact as the forward kept it (not needed for act none, not gated,
+    without need_w). grad_preact [rows, weight rows]; grad_bias [e, weight rows] of
+    bias_dtype (float32 or grad_out's dtype; None: not wanted); grad_w [s, k] float32 (needs
+    w); grad_residual [rows, n], for a residual of buffer rows. The gradients of a and
+    weights are moe_expert_gemm_dgrad and _wgrad of grad_preact.
+    """
+    _expect(grad_out, "grad_out", (layout.rows, None), _GEMM_DTYPES)
+    n, dt = grad_out.shape[1], grad_out.dtype
+    nz = 2 * n if gated else n
+    code = _activation(act)
+    if bias_dtype not in (None, torch.float32, dt):
+        raise ValueError(f"bias_dtype must be float32 or {dt}, got {bias_dtype}")
+    _expect(w, "w", (layout.s, layout.k), torch.float32)
+    if need_w and w is None:
+        raise ValueError("need_w: w is required")
+    if preact is None and (code != 0 or gated or need_w):
+        raise ValueError("preact is required (the values the forward kept)")
+    _expect(preact, "preact", (layout.rows, nz), dt)
+    _expect(workspace, "workspace", (None,), torch.uint8)
+    _same_device(layout, grad_out, preact, w, workspace)
+    dev = grad_out.device
+    gz = torch.empty((layout.rows, nz), dtype=dt, device=dev) if need_preact else None
+    gb = torch.empty((layout.e, nz), dtype=bias_dtype, device=dev) if bias_dtype is not None else None
+    gw = torch.empty((layout.s, layout.k), dtype=torch.float32, device=dev) if need_w else None
+    gr = torch.empty((layout.rows, n), dtype=dt, device=dev) if need_residual else None
+    if workspace is None and (gb is not None or gw is not None):
+        workspace = torch.empty(lib().moe_expert_act_backward_workspace_bytes(layout.byref(), n, int(bool(gated))),
+                                dtype=torch.uint8, device=dev)
+    _launch(grad_out, lib().moe_expert_act_backward, layout.byref(), _ptr(grad_out), _ptr(preact), n, _DTYPE_CODE[dt],
+            code, int(bool(gated)), _ptr(w), _ptr(gz), _DTYPE_CODE[bias_dtype] if gb is not None else MOE_F32, _ptr(gb),
+            _ptr(gw), _ptr(gr), _ptr(workspace), workspace.numel() if workspace is not None else 0)
+    return gz, gb, gw, gr
+
+
 def moe_renormalize_kept(layout: Layout, w: torch.Tensor, out=None):
     _expect(w, "w", (layout.s, layout.k), torch.float32)
     _expect(out, "out", (layout.s, layout.k), torch.float32)
@@ -595,6 +703,7 @@ __all__ = [
     "moe_dispatch_replay", "moe_combine", "moe_combine_backward", "moe_dispatch_backward",
     "moe_layout_read", "moe_dispatch_weighted", "moe_dispatch_weighted_backward",
     "moe_renormalize_kept", "moe_renormalize_kept_backward", "moe_expert_gemm", "moe_expert_gemm_wgrad", "moe_expert_gemm_dgrad",
+    "moe_expert_gemm_act", "moe_expert_act_backward", "ACTIVATIONS",
     "moe_balance_loss", "moe_balance_loss_backward", "workspace_bytes", "Layout",
     "LayoutOptions", "MoeError", "lib", "EXPORTS",
 ]

@@ -17,8 +17,8 @@ ROOT = os.path.dirname(HERE)
 LIB_NAME = "libmoe_gate.so"
 LIB_PATH = os.path.join(HERE, LIB_NAME)
 SOURCES = [os.path.join(HERE, "csrc", f) for f in ("api.hip", "gate.hip", "layout.hip", "rows.hip", "gemm.hip", "gemm_bwd.hip",
-                                                     "balance.hip")]
-HEADERS = [os.path.join(HERE, "csrc", f) for f in ("internal.h", "moe_device.h", "gemm_common.h", "ops.h")] + [
+                                                     "balance.hip", "expert_act.hip", "expert_act_bwd.hip")]
+HEADERS = [os.path.join(HERE, "csrc", f) for f in ("internal.h", "moe_device.h", "gemm_common.h", "ops.h", "expert_act.h")] + [
     os.path.join(ROOT, "include", "moe_gate.h")]
 
 ARCH = "gfx950"

@@ -36,8 +36,8 @@ from torch.autograd.function import once_differentiable
 
 from . import (FLAG_REPLAY_MISMATCH, Layout, moe_balance_loss, moe_balance_loss_backward, moe_combine,
                moe_combine_backward, moe_dispatch, moe_dispatch_backward, moe_dispatch_layout, moe_dispatch_replay,
-               moe_dispatch_weighted, moe_dispatch_weighted_backward, moe_expert_gemm,
-               moe_expert_gemm_dgrad, moe_expert_gemm_wgrad, moe_gate_topk,
+               moe_dispatch_weighted, moe_dispatch_weighted_backward, moe_expert_act_backward,
+               moe_expert_gemm, moe_expert_gemm_act, moe_expert_gemm_dgrad, moe_expert_gemm_wgrad, moe_gate_topk,
                moe_gate_topk_backward, moe_layout_read, moe_renormalize_kept,
                moe_renormalize_kept_backward)
 
@@ -216,6 +216,50 @@ class _ExpertLinear(torch.autograd.Function):
         return g_x, g_w, None
 
 
+class _ExpertAct(torch.autograd.Function):
+    """One projection per expert with its epilogue; a gathered from token rows or a buffer."""
+
+    @staticmethod
+    def forward(ctx, a, weights, bias, w, residual, layout, act, gated, gather, residual_gather):
+        a, weights = a.contiguous(), weights.contiguous()
+        bias, w, residual = (None if t is None else t.contiguous() for t in (bias, w, residual))
+        bent = act != "none" or gated
+        keep = (bent and any(ctx.needs_input_grad[:4])) or (w is not None and ctx.needs_input_grad[3])
+        got = moe_expert_gemm_act(layout, a, weights, gather=gather, bias=bias, act=act, gated=gated, w=w,
+                                  residual=residual, residual_gather=residual_gather, save_preact=keep)
+        out, preact = got if keep else (got, None)
+        ctx.save_for_backward(a, weights, w, preact)
+        ctx.layout, ctx.act, ctx.gated, ctx.bent = layout, act, gated, bent
+        ctx.gather, ctx.residual_gather = gather, residual_gather
+        ctx.bias_dtype = None if bias is None else bias.dtype
+        return out
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, g_out):
+        a, weights, w, preact = ctx.saved_tensors
+        need_a, need_weights, need_bias, need_w, need_res = ctx.needs_input_grad[:5]
+        L, g_out = ctx.layout, g_out.contiguous()
+        g_a = g_weights = g_bias = g_w = g_res = None
+        g_z = g_out  # neither bent nor weighted: the product's own gradient
+        need_z = (need_a or need_weights) and (ctx.bent or w is not None)
+        rows_res = need_res and not ctx.residual_gather
+        if need_z or need_bias or need_w or rows_res:
+            gz, g_bias, g_w, g_res = moe_expert_act_backward(
+                L, g_out, preact, ctx.act, ctx.gated, w, need_preact=need_z,
+                bias_dtype=ctx.bias_dtype if need_bias else None, need_w=need_w, need_residual=rows_res)
+            g_z = gz if need_z else g_out
+        if need_a:
+            g_a = moe_expert_gemm_dgrad(L, g_z, weights)
+            if ctx.gather:
+                g_a = moe_dispatch_backward(L, g_a)
+        if need_weights:
+            g_weights = moe_expert_gemm_wgrad(L, a, g_z, gather=ctx.gather, out_dtype=weights.dtype)
+        if need_res and ctx.residual_gather:
+            g_res = moe_dispatch_backward(L, g_out)
+        return g_a, g_weights, g_bias, g_w, g_res, None, None, None, None, None
+
+
 class LayoutRecorder:
     """Routing and layouts of one checkpointed call, recorded on its forward, replayed on
     its recompute.
@@ -361,11 +405,21 @@ def combine(expert_out: torch.Tensor, w: torch.Tensor | None, layout: Layout):
     return _Combine.apply(expert_out, w, layout)
 
 
-def expert_linear(x: torch.Tensor, weights: torch.Tensor, layout: Layout):
+def expert_linear(x: torch.Tensor, weights: torch.Tensor, layout: Layout, bias: torch.Tensor | None = None,
+                  act: str = "none", gated: bool = False, w: torch.Tensor | None = None,
+                  residual: torch.Tensor | None = None, residual_gather: bool = False, gather: bool = True):
     """Each placed row r of expert x: x[src[r]] @ weights[x]^T, the dispatch fused into the
     grouped GEMM's operand loads (forward, input-row gradient and weight gradient all run
-    on the layout). weights [e, n, m]; returns [rows, n] for combine()."""
-    return _ExpertLinear.apply(x, weights, layout)
+    on the layout). weights [e, n, m]; returns [rows, n] for combine().
+
+    With an epilogue, out[r] = w_r u + res(r) for z = x[src[r]] @ weights[x]^T + bias[x] and
+    u = act(z), or, gated, act(z[:n]) * z[n:] with weights [e, 2n, m]: act none, relu, gelu,
+    gelu_tanh or silu, w [s, k] the route weights, residual a row for each buffer row or,
+    with residual_gather, for each token. gather=False takes x as a buffer [rows, m] (the
+    rows an earlier projection left). Gradients reach x, weights, bias, w and residual."""
+    if gather and bias is None and act == "none" and not gated and w is None and residual is None:
+        return _ExpertLinear.apply(x, weights, layout)
+    return _ExpertAct.apply(x, weights, bias, w, residual, layout, act, gated, gather, residual_gather)
 
 
 def renormalize(w: torch.Tensor, layout: Layout):

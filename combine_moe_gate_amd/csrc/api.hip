@@ -520,6 +520,169 @@ moe_status_t moe_expert_gemm(const moe_layout_t* layout, const void* a, int32_t 
                     "moe_expert_gemm");
 }
 
+// Whether two arrays share a byte.
+static bool overlap(const void* p, size_t np, const void* q, size_t nq) {
+  const char* a = static_cast<const char*>(p);
+  const char* b = static_cast<const char*>(q);
+  return p != nullptr && q != nullptr && np > 0 && nq > 0 && a < b + nq && b < a + np;
+}
+
+static moe_status_t check_act(int32_t activation, int32_t gated, int32_t n) {
+  if (activation < MOE_ACT_NONE || activation > MOE_ACT_SILU)
+    return fail(MOE_ERR_INVALID_ARG, "unknown activation %d", activation);
+  if (gated != 0 && gated != 1) return fail(MOE_ERR_INVALID_ARG, "gated must be 0 or 1 (got %d)", gated);
+  if (gated && n > INT32_MAX / 2) return fail(MOE_ERR_UNSUPPORTED, "n=%d: 2 n exceeds 32 bits", n);
+  return MOE_OK;
+}
+
+static moe_status_t check_bias_dtype(int32_t bias_dtype, moe_dtype_t dtype) {
+  if (bias_dtype != MOE_F32 && bias_dtype != dtype)
+    return fail(MOE_ERR_UNSUPPORTED, "bias_dtype must be float32 or dtype (got %d, dtype %d)", bias_dtype,
+                static_cast<int>(dtype));
+  return MOE_OK;
+}
+
+moe_status_t moe_expert_gemm_act(const moe_layout_t* layout, const void* a, int32_t gather,
+                                 const void* weights, int32_t m, int32_t n, moe_dtype_t dtype,
+                                 const moe_expert_epilogue_t* epilogue, void* out, void* stream) {
+  moe::LayoutView v;
+  MOE_TRY(view_of(layout, &v));
+  if (dtype != MOE_BF16 && dtype != MOE_F16)
+    return fail(MOE_ERR_UNSUPPORTED, "moe_expert_gemm_act supports bf16 and f16 only (got dtype %d)",
+                static_cast<int>(dtype));
+  if (gather != 0 && gather != 1)
+    return fail(MOE_ERR_INVALID_ARG, "gather must be 0 or 1 (got %d)", gather);
+  const moe_expert_epilogue_t none{};
+  const moe_expert_epilogue_t& ep = epilogue != nullptr ? *epilogue : none;
+  int64_t rc_in = 0, rc_out = 0;
+  MOE_TRY(check_rows(m, dtype, &rc_in));
+  MOE_TRY(check_rows(n, dtype, &rc_out));
+  MOE_TRY(check_act(ep.activation, ep.gated, n));
+  if (ep.bias != nullptr) MOE_TRY(check_bias_dtype(ep.bias_dtype, dtype));
+  if (ep.residual_gather != 0 && ep.residual_gather != 1)
+    return fail(MOE_ERR_INVALID_ARG, "residual_gather must be 0 or 1 (got %d)", ep.residual_gather);
+  const int32_t nz = ep.gated ? 2 * n : n;
+  if (moe::expert_act_grid(v, n, ep.gated != 0) > INT32_MAX)
+    return fail(MOE_ERR_UNSUPPORTED, "rows x n too large for one grouped GEMM launch");
+  const int64_t a_rows = gather ? v.s : v.rows, res_rows = ep.residual_gather ? v.s : v.rows;
+  MOE_TRY(check_array(a, v.s > 0 ? a_rows : 0, "a", true));
+  MOE_TRY(check_array(weights, v.s > 0 ? v.e : 0, "weights", true));
+  MOE_TRY(check_array(out, v.rows, "out", true));
+  if (ep.bias != nullptr) MOE_TRY(check_array(ep.bias, 1, "bias", true));
+  if (ep.residual != nullptr) MOE_TRY(check_array(ep.residual, 1, "residual", true));
+  if (ep.preact != nullptr) MOE_TRY(check_array(ep.preact, 1, "preact", true));
+  const size_t eb = elem_bytes(dtype);
+  const size_t a_bytes = a_rows * m * eb, res_bytes = res_rows * n * eb;
+  const size_t out_bytes = v.rows * n * eb, pre_bytes = static_cast<size_t>(v.rows) * nz * eb;
+  if (overlap(out, out_bytes, a, a_bytes) || overlap(out, out_bytes, ep.residual, res_bytes) ||
+      overlap(ep.preact, pre_bytes, a, a_bytes) || overlap(ep.preact, pre_bytes, ep.residual, res_bytes) ||
+      overlap(out, out_bytes, ep.preact, pre_bytes))
+    return fail(MOE_ERR_INVALID_ARG, "out and preact may not overlap each other, a or residual");
+  moe::ExpertAct p{};
+  p.a = a;
+  p.w = weights;
+  p.bias = ep.bias;
+  p.route_w = ep.topk_w;
+  p.residual = ep.residual;
+  p.preact = ep.preact;
+  p.out = out;
+  p.dst = v.dst;
+  p.src = v.src;
+  p.kept = v.kept;
+  p.offsets = v.offsets;
+  p.e = v.e;
+  p.k = v.k;
+  p.m = m;
+  p.n = n;
+  p.nz = nz;
+  p.act = ep.activation;
+  p.rows = v.rows;
+  p.gather = gather != 0;
+  p.gated = ep.gated != 0;
+  p.bias_f32 = ep.bias_dtype == MOE_F32;
+  p.residual_gather = ep.residual_gather != 0;
+  return hip_status(moe::launch_expert_act(v, p, static_cast<int>(dtype), static_cast<hipStream_t>(stream)),
+                    "moe_expert_gemm_act");
+}
+
+size_t moe_expert_act_backward_workspace_bytes(const moe_layout_t* layout, int32_t n, int32_t gated) {
+  const std::string saved = g_last_error;
+  moe::LayoutView v;
+  if (view_of(layout, &v) != MOE_OK || n < 1 || check_act(MOE_ACT_NONE, gated, n) != MOE_OK) {
+    g_last_error = saved;
+    return 0;
+  }
+  return moe::expert_act_backward_plan(v, n, gated != 0).bytes;
+}
+
+moe_status_t moe_expert_act_backward(const moe_layout_t* layout, const void* grad_out,
+                                     const void* preact, int32_t n, moe_dtype_t dtype,
+                                     int32_t activation, int32_t gated, const float* topk_w,
+                                     void* grad_preact, moe_dtype_t bias_dtype, void* grad_bias,
+                                     float* grad_topk_w, void* grad_residual, void* workspace,
+                                     size_t workspace_bytes, void* stream) {
+  moe::LayoutView v;
+  MOE_TRY(view_of(layout, &v));
+  if (dtype != MOE_BF16 && dtype != MOE_F16)
+    return fail(MOE_ERR_UNSUPPORTED, "moe_expert_act_backward supports bf16 and f16 only (got dtype %d)",
+                static_cast<int>(dtype));
+  int64_t rc = 0;
+  MOE_TRY(check_rows(n, dtype, &rc));
+  MOE_TRY(check_act(activation, gated, n));
+  if (grad_bias != nullptr) MOE_TRY(check_bias_dtype(bias_dtype, dtype));
+  if (grad_topk_w != nullptr && topk_w == nullptr && v.s > 0)
+    return fail(MOE_ERR_INVALID_ARG, "grad_topk_w needs topk_w");
+  const bool needs_z = activation != MOE_ACT_NONE || gated != 0 || grad_topk_w != nullptr;
+  const int64_t rows = v.s > 0 ? v.rows : 0;
+  MOE_TRY(check_array(grad_out, rows, "grad_out", true));
+  if (needs_z) MOE_TRY(check_array(preact, rows, "preact", true));
+  if (grad_preact != nullptr) MOE_TRY(check_array(grad_preact, 1, "grad_preact", true));
+  if (grad_residual != nullptr) MOE_TRY(check_array(grad_residual, 1, "grad_residual", true));
+  const moe::ExpertActBackwardPlan plan = moe::expert_act_backward_plan(v, n, gated != 0);
+  const int32_t nz = gated ? 2 * n : n;
+  const int64_t sums = static_cast<int64_t>(v.e) * ((nz + 63) / 64) + static_cast<int64_t>(v.s) * v.k / 256 + 1;
+  if (plan.grid > INT32_MAX - 65536 || sums > INT32_MAX)
+    return fail(MOE_ERR_UNSUPPORTED, "rows x n too large for one launch");
+  if (grad_bias != nullptr || grad_topk_w != nullptr) {
+    if (workspace == nullptr) return fail(MOE_ERR_INVALID_ARG, "workspace is NULL");
+    if ((reinterpret_cast<uintptr_t>(workspace) & (kAlign - 1)) != 0)
+      return fail(MOE_ERR_MISALIGNED, "workspace is not %zu-byte aligned", kAlign);
+    if (workspace_bytes < plan.bytes)
+      return fail(MOE_ERR_WORKSPACE, "workspace has %zu bytes, the epilogue's backward needs %zu", workspace_bytes,
+                  plan.bytes);
+  }
+  const size_t eb = elem_bytes(dtype);
+  const size_t n_bytes = v.rows * n * eb, z_bytes = static_cast<size_t>(v.rows) * nz * eb;
+  if (overlap(grad_preact, z_bytes, grad_out, n_bytes) || overlap(grad_preact, z_bytes, preact, z_bytes) ||
+      overlap(grad_residual, n_bytes, grad_out, n_bytes) || overlap(grad_residual, n_bytes, preact, z_bytes) ||
+      overlap(grad_preact, z_bytes, grad_residual, n_bytes))
+    return fail(MOE_ERR_INVALID_ARG, "grad_preact and grad_residual may not overlap each other, grad_out or preact");
+  moe::ExpertActBackward p{};
+  p.grad_out = grad_out;
+  p.preact = needs_z ? preact : nullptr;
+  p.route_w = topk_w;
+  p.grad_preact = grad_preact;
+  p.grad_bias = grad_bias;
+  p.grad_w = grad_topk_w;
+  p.grad_residual = grad_residual;
+  p.dst = v.dst;
+  p.src = v.src;
+  p.kept = v.kept;
+  p.offsets = v.offsets;
+  p.s = v.s;
+  p.e = v.e;
+  p.k = v.k;
+  p.n = n;
+  p.nz = nz;
+  p.act = activation;
+  p.rows = v.rows;
+  p.gated = gated != 0;
+  p.bias_f32 = bias_dtype == MOE_F32;
+  return hip_status(moe::launch_expert_act_backward(v, p, plan, static_cast<char*>(workspace), static_cast<int>(dtype),
+                                                    static_cast<hipStream_t>(stream)),
+                    "moe_expert_act_backward");
+}
+
 moe_status_t moe_expert_gemm_wgrad(const moe_layout_t* layout, const void* a, int32_t gather,
                                    const void* grad_out, int32_t m, int32_t n, moe_dtype_t dtype,
                                    moe_dtype_t grad_w_dtype, void* grad_w, void* stream) {

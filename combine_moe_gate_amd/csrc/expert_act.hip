@@ -1,0 +1,565 @@
+// The experts' products with bias, activation (plain or gated), route weight and residual
+// applied to the float32 sums before their one rounding, on gfx950 matrix cores.
+//
+// For each placed row r of expert x, with z = A(r) @ W[x]^T + b[x] (A(r) = a[src[r]] or
+// a[r]):   out[r] = w_r u + residual(r),   u = act(z), or act(z_gate) * z_up for a gated
+// projection, whose weights hold the n gate rows, then the n up rows. Kept apart from the
+// plain product, the activation would read and write every [rows, n] value again.
+//
+// Two kernels, by how many rows an expert has on average:
+//
+// Tiles (long segments; bound by the matrix cores). A workgroup of eight waves, 2 along the
+// rows by 4 along the columns, multiplies up to 288 rows by 256 weight rows of one expert
+// (v_mfma_f32_16x16x32, float32 accumulators). A segment of R rows is cut into the fewest
+// tiles of at most 288 rows, of heights that differ by at most 32: tiles of a fixed 256
+// would leave a segment of 530 rows a third tile of 18, and a quarter of a uniform batch's
+// products on rows that are not there; this way fewer than 32 rows per expert are. The
+// height is a multiple of 32 rows (FM 16-row MFMA tiles for each of the two waves along the
+// rows), and the main loop is compiled for each of the nine. Operands go to LDS directly
+// (64-element K steps, two stages, XOR-swizzled: conflict-free 16-byte fragment reads, whole
+// 128-byte lines from memory). Fragments of the token rows are read kAhead MFMA groups
+// before their use, across the K step's border: the next stage is published kAhead groups
+// before the step ends, and the loads of the stage after it start there.
+// For a gated projection a wave's 64 weight rows are 32 gate rows and the 32 up rows that
+// meet them, so both products of an output are in one wave. The finished sums leave through
+// a piece of LDS of the wave's own, 16 rows at a time, and come back as eight consecutive
+// features per lane: bias, residual and results then move as 16-byte pieces, and the
+// epilogue's code exists once whatever the tile's height.
+//
+// Few rows (decoding; bound by reading the weights). A workgroup of four waves multiplies
+// up to 16 F rows by 64 weight rows, each wave a quarter of the K steps: weights go from
+// memory straight to the registers the MFMA reads, several steps ahead (nothing is reused,
+// so LDS would only add a stop), and the four partial sums meet in LDS.
+#include <atomic>
+
+#include "expert_act.h"
+
+namespace moe {
+
+typedef float f32x4_t __attribute__((ext_vector_type(4)));
+
+template <int DT>
+__device__ __forceinline__ f32x4_t mfma_16x16x32(const chunk_t& a, const chunk_t& b, f32x4_t c) {
+  if constexpr (DT == kBF16)
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, a), __builtin_bit_cast(bf16x8_t, b), c,
+                                                    0, 0, 0);
+  else
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8_t, a), __builtin_bit_cast(f16x8_t, b), c,
+                                                   0, 0, 0);
+}
+
+// ---------------------------------------------------------------------------------
+// tiles
+
+constexpr int kActUnits = 9;                       // a tile's most units of 32 rows
+constexpr int kActBM = 32 * kActUnits;
+constexpr int kActBN = 256;                        // weight rows per tile
+constexpr int kActThreads = 512;
+constexpr int kActBand = 8;                        // row-blocks per band of the tile order
+constexpr int kActRowBytes = 128;                  // a staged row: 64 elements
+constexpr int kActAStage = kActBM * kActRowBytes, kActBStage = kActBN * kActRowBytes;
+constexpr int kActStage = kActAStage + kActBStage;
+constexpr int kSlabPitch = 64 * 4 + 16;            // bytes per row of a wave's 16 x 64 float32 slab
+constexpr int kActLds = 2 * kActStage + kActBM * 8;
+static_assert(8 * 16 * kSlabPitch <= 2 * kActStage, "the slabs reuse the stages");
+
+// Row-blocks of a segment of `rows` rows: as few as hold it, of nearly equal height.
+__device__ __forceinline__ int act_blocks(int rows) {
+  const int units = (rows + 31) / 32;
+  return (units + kActUnits - 1) / kActUnits;
+}
+
+struct ActTile {
+  int expert, unit0, units, cb;  // expert (-1: none), first 32-row unit, units, column-block
+};
+
+// This workgroup's tile: the tiles of all experts numbered expert by expert, inside an
+// expert in bands of kActBand row-blocks, column-block by column-block, row-block fastest;
+// workgroup b takes tile (b mod 8) T8 + b / 8, so that each XCD walks one stretch of that
+// order and its resident workgroups share weight tiles and rows through its L2.
+__device__ __forceinline__ ActTile act_tile(int b, int e, const int32_t* __restrict__ kept, int col_blocks) {
+  const int lane = lane_id();
+  ActTile tc{-1, 0, 0, 0};
+  int total = 0;
+  for (int c0 = 0; c0 < e; c0 += kWave) {
+    const int x = c0 + lane;
+    total += __builtin_amdgcn_readlane(wave_inclusive_scan(x < e ? act_blocks(kept[x]) : 0), kWave - 1);
+  }
+  const int64_t tiles = static_cast<int64_t>(total) * col_blocks;
+  const int64_t per_xcd = (tiles + kXcds - 1) / kXcds;
+  const int64_t slot = b / kXcds, t = (b % kXcds) * per_xcd + slot;
+  if (slot >= per_xcd || t >= tiles) return tc;
+  int before = 0;
+  for (int c0 = 0; c0 < e; c0 += kWave) {
+    const int x = c0 + lane;
+    const int rows = x < e ? kept[x] : 0;
+    const int nb = act_blocks(rows);
+    const int incl = wave_inclusive_scan(nb);
+    const int64_t lo = static_cast<int64_t>(before + incl - nb) * col_blocks;
+    const int64_t hi = static_cast<int64_t>(before + incl) * col_blocks;
+    const uint64_t hit = __ballot(t >= lo && t < hi);
+    if (hit != 0ull) {
+      const int owner = static_cast<int>(__builtin_ctzll(hit));
+      const int R = __builtin_amdgcn_readlane(nb, owner);
+      const int units = (__builtin_amdgcn_readlane(rows, owner) + 31) / 32;
+      const int first = before + __builtin_amdgcn_readlane(incl, owner) - R;
+      const int u = static_cast<int>(t - static_cast<int64_t>(first) * col_blocks);
+      const int band = u / (kActBand * col_blocks);
+      const int left = R - band * kActBand;
+      const int in_band = left < kActBand ? left : kActBand;
+      const int v = u - band * kActBand * col_blocks;
+      const int rb = band * kActBand + v % in_band;
+      const int base = units / R, extra = units % R;  // the first `extra` blocks are a unit taller
+      tc.expert = c0 + owner;
+      tc.cb = v / in_band;
+      tc.units = base + (rb < extra);
+      tc.unit0 = rb * base + (rb < extra ? rb : extra);
+      return tc;
+    }
+    before += __builtin_amdgcn_readlane(incl, kWave - 1);
+  }
+  return tc;
+}
+
+// The tile's products and its epilogue, for a height of 32 FM rows.
+template <int DT, int FM>
+__device__ __forceinline__ void act_tile_body(const ExpertAct& p, const ActTile& tc, char* lds) {
+  constexpr int FN = 4;
+  // A K step's products in order: (k32 half, row tile), 2 FM slots of FN MFMAs, cut into
+  // groups of up to four slots whose fragments are read together; the last group lies in
+  // the second half.
+  constexpr int kSlots = 2 * FM, kGroups = FM <= 4 ? 2 : (kSlots + 3) / 4;
+  auto first_slot = [](int g) constexpr { return g * kSlots / kGroups; };
+  constexpr int kALoads = (4 * FM + 7) / 8;            // direct-to-LDS loads of 8 rows, per wave
+  const int lane = lane_id(), wv = wave_in_block();
+  const int wm = wv / 4, wn = wv % 4;
+  const int x = tc.expert;
+  const int row0 = p.offsets[x] + tc.unit0 * 32;
+  const int rem = p.kept[x] - tc.unit0 * 32;
+  const int nrows = rem < 32 * FM ? rem : 32 * FM;
+  const int out_cols = p.gated ? kActBN / 2 : kActBN;
+  const int col0 = tc.cb * out_cols;                   // first output feature
+  const int kchunks = p.m / 8, nk = (p.m + 63) / 64;
+
+  // per tile row: its token and route weight, for the epilogue
+  int* row_token = reinterpret_cast<int*>(lds + 2 * kActStage);
+  float* row_weight = reinterpret_cast<float*>(lds + 2 * kActStage + kActBM * 4);
+  if (static_cast<int>(threadIdx.x) < nrows) {
+    const int r = row0 + threadIdx.x;
+    const int t = p.src[r];
+    row_token[threadIdx.x] = t;
+    row_weight[threadIdx.x] = p.route_w != nullptr ? route_weight(p, r, t) : 1.0f;
+  }
+
+  // staged row and chunk of each load of this lane. Rows past the segment repeat its first
+  // one and weight rows past the last repeat it: both reach only results never stored.
+  const chunk_t* a_row[kALoads];
+  const chunk_t* b_row[4];
+  const chunk_t* wx = static_cast<const chunk_t*>(p.w) + static_cast<size_t>(x) * p.nz * kchunks;
+#pragma unroll
+  for (int q = 0; q < kALoads; ++q) {
+    const int r = (q * 8 + wv) * 8 + lane / 8;
+    const int rr = row0 + (r < nrows ? r : 0);
+    a_row[q] = static_cast<const chunk_t*>(p.a) + static_cast<size_t>(p.gather ? p.src[rr] : rr) * kchunks;
+  }
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    const int r = (q * 8 + wv) * 8 + lane / 8;
+    int j;
+    if (p.gated) {  // 32 gate rows, then the 32 up rows of the same features
+      const int f = col0 + (r / 64) * 32 + r % 32;
+      j = (f < p.n ? f : p.n - 1) + (r % 64 >= 32 ? p.n : 0);
+    } else {
+      j = col0 + r < p.n ? col0 + r : p.n - 1;
+    }
+    b_row[q] = wx + static_cast<size_t>(j) * kchunks;
+  }
+  // slot lane % 8 of staged row R takes chunk slot ^ (R / 2 % 8); the loads' first rows are
+  // multiples of 8, so R / 2 % 8 = 4 (load % 2) + lane / 16
+  const int swz = 4 * (wv % 2) + lane / 16;
+  const int chunk = (lane % 8) ^ swz;
+  auto issue = [&](int kt) {
+    char* st = lds + (kt % 2) * kActStage;
+    const int kq = kt * 8 + chunk;
+    const int at = kq < kchunks ? kq : 0;  // past the row's end: its first chunk, cleared once landed
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+      __builtin_amdgcn_global_load_lds(static_cast<const void*>(b_row[q] + at),
+                                       (lds_void_t*)(st + kActAStage + (q * 8 + wv) * 1024), 16, 0, 0);
+#pragma unroll
+    for (int q = 0; q < kALoads; ++q)
+      if (q * 8 + wv < 4 * FM)  // uniform
+        __builtin_amdgcn_global_load_lds(static_cast<const void*>(a_row[q] + at),
+                                         (lds_void_t*)(st + (q * 8 + wv) * 1024), 16, 0, 0);
+  };
+  auto clear_tail = [&](int kt) {
+    if (kt * 8 + chunk < kchunks) return;
+    char* st = lds + (kt % 2) * kActStage;
+    const chunk_t z = {0u, 0u, 0u, 0u};
+#pragma unroll
+    for (int q = 0; q < 4; ++q) *reinterpret_cast<chunk_t*>(st + kActAStage + (q * 8 + wv) * 1024 + lane * 16) = z;
+#pragma unroll
+    for (int q = 0; q < kALoads; ++q)
+      if (q * 8 + wv < 4 * FM) *reinterpret_cast<chunk_t*>(st + (q * 8 + wv) * 1024 + lane * 16) = z;
+  };
+
+  f32x4_t acc[FM][FN];
+#pragma unroll
+  for (int i = 0; i < FM; ++i)
+#pragma unroll
+    for (int j = 0; j < FN; ++j) acc[i][j] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+
+  // fragments: row lane % 16 of a 16-row MFMA tile, chunk 4 half + lane / 16, at slot
+  // chunk ^ (row / 2 % 8)
+  const int frag_row = (lane & 15) * kActRowBytes;
+  const int frag_swz = (lane & 15) >> 1;
+  const int a_base = wm * 16 * FM * kActRowBytes + frag_row;
+  const int b_base = kActAStage + wn * 64 * kActRowBytes + frag_row;
+  auto read_a = [&](int kt, int g, chunk_t (&f)[4]) {  // the fragments of group g
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const int slot = first_slot(g) + q;
+      if (slot < first_slot(g + 1))
+        f[q] = *reinterpret_cast<const chunk_t*>(lds + (kt % 2) * kActStage + a_base + (slot % FM) * 16 * kActRowBytes +
+                                                 (((4 * (slot / FM) + (lane >> 4)) ^ frag_swz) << 4));
+    }
+  };
+  auto read_b = [&](int kt, int half, chunk_t (&b)[FN]) {
+#pragma unroll
+    for (int j = 0; j < FN; ++j)
+      b[j] = *reinterpret_cast<const chunk_t*>(lds + (kt % 2) * kActStage + b_base + j * 16 * kActRowBytes +
+                                               (((4 * half + (lane >> 4)) ^ frag_swz) << 4));
+  };
+  // step kt is whole in LDS and every wave has read out the step before it
+  auto publish = [&](int kt) {
+    __builtin_amdgcn_s_waitcnt(wait_vm(0) & kWaitLdsOnly);  // all loads and LDS operations
+    if ((kt + 1) * 8 > kchunks) {
+      clear_tail(kt);
+      __builtin_amdgcn_s_waitcnt(kWaitLdsOnly);
+    }
+    stage_barrier();
+  };
+
+  issue(0);
+  publish(0);
+  if (nk > 1) issue(1);
+  chunk_t fa[2][4], fb[2][FN];
+  read_a(0, 0, fa[0]);
+  read_b(0, 0, fb[0]);
+
+  // Under each group's MFMAs the next group's fragments are read, and with the group before
+  // the first one of the second k32 half the weights' of that half. Before the last group's
+  // MFMAs the next step is published (by then every fragment of this step is in registers),
+  // the loads of the one after it start into this step's stage, and the next step's first
+  // fragments are read; after the last step these find old contents, which nothing uses.
+  for (int kt = 0; kt < nk; ++kt) {
+#pragma unroll
+    for (int g = 0; g < kGroups; ++g) {
+      __builtin_amdgcn_s_waitcnt(kWaitLdsOnly);  // this group's fragments have landed
+      __builtin_amdgcn_sched_barrier(0);
+      if (g + 1 < kGroups) {
+        read_a(kt, g + 1, fa[(g + 1) % 2]);
+        if (first_slot(g + 1) <= FM && first_slot(g + 2) > FM) read_b(kt, 1, fb[1]);
+      } else {
+        if (kt + 1 < nk) {
+          publish(kt + 1);
+          if (kt + 2 < nk) issue(kt + 2);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+        read_a(kt + 1, 0, fa[(g + 1) % 2]);
+        read_b(kt + 1, 0, fb[0]);  // the last group is all of the second half
+      }
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const int slot = first_slot(g) + q;
+        if (slot < first_slot(g + 1)) {
+#pragma unroll
+          for (int j = 0; j < FN; ++j)
+            acc[slot % FM][j] = mfma_16x16x32<DT>(fb[slot / FM][j], fa[g % 2][q], acc[slot % FM][j]);
+        }
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    if (kGroups % 2 != 0) {
+#pragma unroll
+      for (int q = 0; q < 4; ++q) fa[0][q] = fa[1][q];
+    }
+  }
+
+  // epilogue: each 16-row tile's sums through the wave's slab. Lane l holds token row
+  // l % 16, features 16 j + 4 (l / 16) .. + 3 of its 64; it takes back row l / 4, features
+  // 8 (l % 4) .. + 7 of each 32 (gated: the gate's and the up's).
+  __syncthreads();
+  char* slab = lds + wv * 16 * kSlabPitch;
+#pragma unroll 1
+  for (int i = 0; i < FM; ++i) {
+    if (wm * 16 * FM + i * 16 >= nrows) break;  // uniform
+#pragma unroll
+    for (int ii = 0; ii < FM; ++ii)
+      if (ii == i) {
+#pragma unroll
+        for (int j = 0; j < FN; ++j)
+          *reinterpret_cast<f32x4_t*>(slab + (lane & 15) * kSlabPitch + j * 64 + (lane >> 4) * 16) = acc[ii][j];
+      }
+    const int row = wm * 16 * FM + i * 16 + (lane >> 2);
+    const float* back = reinterpret_cast<const float*>(slab + (lane >> 2) * kSlabPitch) + 8 * (lane & 3);
+    float v[8], u[8];
+#pragma unroll
+    for (int q = 0; q < 8; ++q) {
+      v[q] = back[q];
+      u[q] = back[32 + q];
+    }
+    if (row < nrows) {
+      const int r = row0 + row, t = row_token[row];
+      const float w = row_weight[row];
+      const int c = col0 + wn * (out_cols / 4) + 8 * (lane & 3);
+      if (c < p.n) finish8<DT>(p, x, r, t, w, c, v, u);
+      if (!p.gated && c + 32 < p.n) finish8<DT>(p, x, r, t, w, c + 32, u, v);
+    }
+  }
+}
+
+template <int DT>
+__global__ __launch_bounds__(kActThreads) __attribute__((amdgpu_waves_per_eu(2, 2))) void expert_act_kernel(
+    ExpertAct p, int col_blocks, int tile_grid) {
+  extern __shared__ __attribute__((aligned(1024))) char lds[];
+  if (static_cast<int>(blockIdx.x) >= tile_grid) {
+    zero_unfilled(p, blockIdx.x - tile_grid, gridDim.x - tile_grid);
+    return;
+  }
+  const ActTile tc = act_tile(blockIdx.x, p.e, p.kept, col_blocks);
+  if (tc.expert < 0) return;
+  switch (tc.units) {
+    case 1: act_tile_body<DT, 1>(p, tc, lds); break;
+    case 2: act_tile_body<DT, 2>(p, tc, lds); break;
+    case 3: act_tile_body<DT, 3>(p, tc, lds); break;
+    case 4: act_tile_body<DT, 4>(p, tc, lds); break;
+    case 5: act_tile_body<DT, 5>(p, tc, lds); break;
+    case 6: act_tile_body<DT, 6>(p, tc, lds); break;
+    case 7: act_tile_body<DT, 7>(p, tc, lds); break;
+    case 8: act_tile_body<DT, 8>(p, tc, lds); break;
+    default: act_tile_body<DT, 9>(p, tc, lds); break;
+  }
+}
+
+// ---------------------------------------------------------------------------------
+// few rows
+
+constexpr int kFewThreads = 256, kFewWaves = 4;
+constexpr int kFewCols = 64;  // weight rows per workgroup
+
+template <int DT, int F>
+__global__ __launch_bounds__(kFewThreads) void expert_act_few_kernel(ExpertAct p, int col_blocks, int tile_grid) {
+  constexpr int kDepth = F == 4 ? 2 : 3;  // K steps of 64 elements in flight per wave
+  extern __shared__ __attribute__((aligned(1024))) char lds[];  // [wave][16 F rows][kSlabPitch]
+  if (static_cast<int>(blockIdx.x) >= tile_grid) {
+    zero_unfilled(p, blockIdx.x - tile_grid, gridDim.x - tile_grid);
+    return;
+  }
+  const TileCoord tc = find_tile<16 * F>(blockIdx.x, p.e, p.kept, col_blocks, kActBand);
+  const int x = tc.expert;
+  if (x < 0) return;
+  const int lane = lane_id(), wv = wave_in_block();
+  const int row0 = p.offsets[x] + tc.rb * 16 * F;
+  const int rem = p.kept[x] - tc.rb * 16 * F;
+  const int nrows = rem < 16 * F ? rem : 16 * F;
+  const int out_cols = p.gated ? kFewCols / 2 : kFewCols;
+  const int col0 = tc.cb * out_cols;
+  const int kchunks = p.m / 8;
+
+  const chunk_t* a_row[F];
+  const chunk_t* b_row[4];
+#pragma unroll
+  for (int i = 0; i < F; ++i) {
+    const int r = i * 16 + (lane & 15);
+    const int rr = row0 + (r < nrows ? r : 0);
+    a_row[i] = static_cast<const chunk_t*>(p.a) + static_cast<size_t>(p.gather ? p.src[rr] : rr) * kchunks + (lane >> 4);
+  }
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    int f;
+    if (p.gated) {
+      f = col0 + (j & 1) * 16 + (lane & 15);
+      f = (f < p.n ? f : p.n - 1) + (j >= 2 ? p.n : 0);
+    } else {
+      f = col0 + j * 16 + (lane & 15);
+      f = f < p.n ? f : p.n - 1;
+    }
+    b_row[j] = static_cast<const chunk_t*>(p.w) + (static_cast<size_t>(x) * p.nz + f) * kchunks + (lane >> 4);
+  }
+
+  f32x4_t acc[F][4];
+#pragma unroll
+  for (int i = 0; i < F; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) acc[i][j] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+
+  chunk_t fa[kDepth][2][F], fb[kDepth][2][4];
+  const int full = kchunks / 8;  // whole K steps; wave wv takes steps wv, wv + 4, ...
+  auto load = [&](int step, int d) {
+    const size_t at = static_cast<size_t>(step < full ? step : 0) * 8;  // past the end: loaded, not used
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) fb[d][h][j] = __builtin_nontemporal_load(b_row[j] + at + 4 * h);
+#pragma unroll
+      for (int i = 0; i < F; ++i) fa[d][h][i] = a_row[i][at + 4 * h];
+    }
+  };
+  auto multiply = [&](int d) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int i = 0; i < F; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) acc[i][j] = mfma_16x16x32<DT>(fb[d][h][j], fa[d][h][i], acc[i][j]);
+  };
+  if (full > wv) {
+#pragma unroll
+    for (int d = 0; d < kDepth; ++d) load(wv + d * kFewWaves, d);
+    int step = wv;
+    for (; step + (2 * kDepth - 1) * kFewWaves < full; step += kDepth * kFewWaves) {  // every refill is a real step
+#pragma unroll
+      for (int d = 0; d < kDepth; ++d) {
+        multiply(d);
+        load(step + (d + kDepth) * kFewWaves, d);
+      }
+    }
+    for (; step < full; step += kDepth * kFewWaves) {  // what is left: at most two rounds
+#pragma unroll
+      for (int d = 0; d < kDepth; ++d) {  // uniform conditions
+        if (step + d * kFewWaves < full) multiply(d);
+        if (step + (d + kDepth) * kFewWaves < full) load(step + (d + kDepth) * kFewWaves, d);
+      }
+    }
+  }
+  if (kchunks % 8 != 0 && wv == full % kFewWaves) {  // the last, partial step: zeros past the rows' end
+    const chunk_t z = {0u, 0u, 0u, 0u};
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const bool in = full * 8 + 4 * h + (lane >> 4) < kchunks;
+      const size_t at = static_cast<size_t>(full) * 8 + 4 * h;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) fb[0][h][j] = in ? b_row[j][at] : z;
+#pragma unroll
+      for (int i = 0; i < F; ++i) fa[0][h][i] = in ? a_row[i][at] : z;
+    }
+    multiply(0);
+  }
+
+#pragma unroll
+  for (int i = 0; i < F; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      *reinterpret_cast<f32x4_t*>(lds + (wv * 16 * F + i * 16 + (lane & 15)) * kSlabPitch + j * 64 + (lane >> 4) * 16) =
+          acc[i][j];
+  __syncthreads();
+  const int row = threadIdx.x / 4, q8 = 8 * (threadIdx.x % 4);
+  if (row >= nrows) return;
+  float v[8], u[8];
+#pragma unroll
+  for (int q = 0; q < 8; ++q) v[q] = u[q] = 0.0f;
+  for (int w = 0; w < kFewWaves; ++w) {
+    const float* part = reinterpret_cast<const float*>(lds + (w * 16 * F + row) * kSlabPitch) + q8;
+#pragma unroll
+    for (int q = 0; q < 8; ++q) {
+      v[q] += part[q];
+      u[q] += part[32 + q];
+    }
+  }
+  const int r = row0 + row, t = p.src[r];
+  const float w = p.route_w != nullptr ? route_weight(p, r, t) : 1.0f;
+  const int c = col0 + q8;
+  if (c < p.n) finish8<DT>(p, x, r, t, w, c, v, u);
+  if (!p.gated && c + 32 < p.n) finish8<DT>(p, x, r, t, w, c + 32, u, v);
+}
+
+// ---------------------------------------------------------------------------------
+// launches
+
+constexpr int kZeroBlocks = 64;  // workgroups that clear rows no route fills
+
+// F of the row tiles (16 F rows) for segments of few rows on average; 0: the large tiles.
+static int few_rows(const LayoutView& L) {
+  const int64_t most = L.capacity > 0 && L.capacity < L.s ? L.capacity : L.s;  // no expert has more rows
+  const int64_t routes = static_cast<int64_t>(L.s) * L.k;
+  const int64_t mean = (routes + L.e - 1) / L.e < most ? (routes + L.e - 1) / L.e : most;
+  return most <= 16 || mean <= 12 ? 1 : mean <= 24 ? 2 : mean <= 64 ? 4 : 0;
+}
+
+// At most this many row tiles of a height, known without reading the layout: a segment of R
+// rows has fewer than R / height + 1.
+static int64_t row_tiles(const LayoutView& L, int height) {
+  const int64_t routes = static_cast<int64_t>(L.s) * L.k;
+  const int64_t with_rows = routes < L.e ? routes : L.e;
+  if (L.capacity > 0) {
+    const int64_t most = L.capacity < L.s ? L.capacity : L.s;
+    const int64_t each = with_rows * ((most + height - 1) / height);
+    const int64_t all = routes / height + with_rows;
+    return each < all ? each : all;
+  }
+  return routes / height + with_rows;
+}
+
+int64_t expert_act_grid(const LayoutView& L, int n, bool gated) {
+  if (L.s == 0) return kZeroBlocks;
+  const int few = few_rows(L);
+  const int cols = (few ? kFewCols : kActBN) / (gated ? 2 : 1);
+  const int64_t col_blocks = (n + cols - 1) / cols;
+  const int64_t tiles = row_tiles(L, few ? 16 * few : kActBM) * col_blocks;
+  return (tiles + kXcds - 1) / kXcds * kXcds + kZeroBlocks;
+}
+
+// Dynamic LDS above the 64 KiB default needs the kernel's limit raised, once per device.
+static hipError_t allow_lds(const void* kernel, int bytes, std::atomic<uint64_t>& done) {
+  int dev = 0;
+  hipError_t err = hipGetDevice(&dev);
+  if (err != hipSuccess) return err;
+  const uint64_t bit = 1ull << (dev & 63);
+  if (dev < 64 && (done.load(std::memory_order_relaxed) & bit) != 0) return hipSuccess;
+  err = hipFuncSetAttribute(kernel, hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (err == hipSuccess && dev < 64) done.fetch_or(bit, std::memory_order_relaxed);
+  return err;
+}
+
+template <int DT, int F>
+static hipError_t launch_few(const ExpertAct& p, int col_blocks, int64_t grid, hipStream_t stream) {
+  static std::atomic<uint64_t> done{0};
+  constexpr int kBytes = kFewWaves * 16 * F * kSlabPitch;
+  auto kern = expert_act_few_kernel<DT, F>;
+  if (kBytes > 65536) {
+    const hipError_t err = allow_lds(reinterpret_cast<const void*>(kern), kBytes, done);
+    if (err != hipSuccess) return err;
+  }
+  kern<<<static_cast<unsigned>(grid), kFewThreads, kBytes, stream>>>(p, col_blocks, static_cast<int>(grid) - kZeroBlocks);
+  return hipGetLastError();
+}
+
+template <int DT>
+static hipError_t launch_dt(const LayoutView& L, const ExpertAct& p, hipStream_t stream) {
+  const int64_t grid = expert_act_grid(L, p.n, p.gated);
+  const int few = L.s == 0 ? 1 : few_rows(L);
+  const int cols = (few ? kFewCols : kActBN) / (p.gated ? 2 : 1);
+  const int col_blocks = (p.n + cols - 1) / cols;
+  switch (few) {
+    case 1: return launch_few<DT, 1>(p, col_blocks, grid, stream);
+    case 2: return launch_few<DT, 2>(p, col_blocks, grid, stream);
+    case 4: return launch_few<DT, 4>(p, col_blocks, grid, stream);
+    default: break;
+  }
+  static std::atomic<uint64_t> done{0};
+  auto kern = expert_act_kernel<DT>;
+  const hipError_t err = allow_lds(reinterpret_cast<const void*>(kern), kActLds, done);
+  if (err != hipSuccess) return err;
+  kern<<<static_cast<unsigned>(grid), kActThreads, kActLds, stream>>>(p, col_blocks,
+                                                                     static_cast<int>(grid) - kZeroBlocks);
+  return hipGetLastError();
+}
+
+hipError_t launch_expert_act(const LayoutView& L, const ExpertAct& p, int dtype, hipStream_t stream) {
+  if (p.rows == 0) return hipSuccess;
+  return dtype == kBF16 ? launch_dt<kBF16>(L, p, stream) : launch_dt<kF16>(L, p, stream);
+}
+
+}  // namespace moe

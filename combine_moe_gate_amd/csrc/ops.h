@@ -37,4 +37,51 @@ hipError_t launch_balance_loss_backward(const BalanceArgs& a, const int32_t* cou
                                         const float* grad_loss, const float* grad_z, float* grad_logits,
                                         hipStream_t stream);
 
+// ---------------------------------------------------------------------------------
+// expert products with an epilogue
+
+enum Act : int { kActNone = 0, kActRelu = 1, kActGelu = 2, kActGeluTanh = 3, kActSilu = 4 };
+
+// One grouped product out[r] = w_r act(A(r) W[x]^T + b[x]) + residual(r) (gated: act of the
+// first n products times the last n). Element types are 16-bit; nz = 2 n if gated, else n.
+struct ExpertAct {
+  const void* a;            // [s, m] if gather, else [rows, m]
+  const void* w;            // [e, nz, m]
+  const void* bias;         // [e, nz] (float32 if bias_f32), or null
+  const float* route_w;     // [s, k], or null
+  const void* residual;     // [s, n] if residual_gather, else [rows, n], or null
+  void* preact;             // [rows, nz], or null
+  void* out;                // [rows, n]
+  const int32_t *dst, *src, *kept, *offsets;
+  int32_t e, k, m, n, nz, act;
+  int64_t rows;
+  bool gather, gated, bias_f32, residual_gather;
+};
+hipError_t launch_expert_act(const LayoutView& L, const ExpertAct& p, int dtype, hipStream_t stream);
+int64_t expert_act_grid(const LayoutView& L, int n, bool gated);  // its workgroups
+
+// Its epilogue's backward (n, nz as above).
+struct ExpertActBackward {
+  const void* grad_out;     // [rows, n]
+  const void* preact;       // [rows, nz], or null where nothing needs it
+  const float* route_w;     // [s, k], or null
+  void* grad_preact;        // [rows, nz], or null
+  void* grad_bias;          // [e, nz] (float32 if bias_f32), or null
+  float* grad_w;            // [s, k], or null
+  void* grad_residual;      // [rows, n], or null
+  const int32_t *dst, *src, *kept, *offsets;
+  int32_t s, e, k, n, nz, act;
+  int64_t rows;
+  bool gated, bias_f32;
+};
+// The workspace: a partial bias row per row tile, a partial dot per row and column block.
+struct ExpertActBackwardPlan {
+  int32_t col_blocks;
+  int64_t slots, grid;
+  size_t off_bias, off_dots, bytes;
+};
+ExpertActBackwardPlan expert_act_backward_plan(const LayoutView& L, int n, bool gated);
+hipError_t launch_expert_act_backward(const LayoutView& L, const ExpertActBackward& p,
+                                      const ExpertActBackwardPlan& plan, char* ws, int dtype, hipStream_t stream);
+
 }  // namespace moe

@@ -375,6 +375,81 @@ moe_status_t moe_expert_gemm(const moe_layout_t* layout, const void* a, int32_t 
                              const float* topk_w, void* out, void* stream);
 
 /*
+ * Grouped expert product with an epilogue: moe_expert_gemm's rows and weights, with bias,
+ * activation, route weight and residual applied to the float32 sums before the one rounding
+ * to dtype. For each placed row r of expert x, with z = A(r) @ weights[x]^T + bias[x]:
+ *   out[r] = w_r u + res(r),   u = act(z), or with `gated` u = act(z[0:n]) * z[n:2n]
+ * (weights then hold 2n rows per expert: the n gate rows, then the n up rows; let nz = 2n if
+ * gated, else n). Rows no route fills are zero.
+ *   activation  MOE_ACT_NONE, _RELU, _GELU (z Phi(z)), _GELU_TANH (0.5 z (1 + tanh(sqrt(2/pi)
+ *               (z + 0.044715 z^3)))) or _SILU (z / (1 + exp(-z)))
+ *   bias        [e, nz] of bias_dtype (MOE_F32 or dtype), or NULL
+ *   topk_w      [s, k] float32, w_r the weight of the route placed at r, or NULL (1)
+ *   residual    [rows, n], res(r) = residual[r], or with residual_gather [s, n], res(r) =
+ *               residual[src[r]]; of dtype; or NULL (0)
+ *   preact      [rows, nz] of dtype out: z rounded, for moe_expert_act_backward, or NULL;
+ *               rows no route fills are zero
+ *   a, gather, weights [e, nz, m], m, n, dtype, out [rows, n]: as in moe_expert_gemm; m and n
+ *   multiples of 8; every pointer to element rows and the bias 16-byte aligned. out and
+ *   preact may not overlap each other, a or residual. A NULL epilogue means all defaults.
+ * Sums are float32 (order unspecified, one order per sizes: the results are reproducible);
+ * weights, activation and residual are float32 operations, each rounded.
+ */
+typedef enum moe_activation {
+  MOE_ACT_NONE = 0,
+  MOE_ACT_RELU = 1,
+  MOE_ACT_GELU = 2,
+  MOE_ACT_GELU_TANH = 3,
+  MOE_ACT_SILU = 4
+} moe_activation_t;
+
+typedef struct moe_expert_epilogue {
+  int32_t activation;      /* moe_activation_t */
+  int32_t gated;           /* 0 or 1 */
+  const void* bias;
+  int32_t bias_dtype;      /* moe_dtype_t: MOE_F32 or the element type */
+  int32_t residual_gather; /* 0 or 1 */
+  const float* topk_w;
+  const void* residual;
+  void* preact;
+} moe_expert_epilogue_t;
+
+moe_status_t moe_expert_gemm_act(const moe_layout_t* layout, const void* a, int32_t gather,
+                                 const void* weights, int32_t m, int32_t n, moe_dtype_t dtype,
+                                 const moe_expert_epilogue_t* epilogue, void* out, void* stream);
+
+/*
+ * Backward of moe_expert_gemm_act's epilogue, from the kept z: with g = w_r grad_out[r] for
+ * each placed row r of expert x and d = act', all in float32,
+ *   grad_preact[r]  = g d(z), or gated: (g z_up d(z_gate), g act(z_gate)), rounded to dtype
+ *   grad_bias[x]    = sum over expert x's placed rows of the unrounded grad_preact[r]
+ *                     (float32 sums, rounded once to bias_dtype; 0 for an expert with no row)
+ *   grad_topk_w[t,j] = <grad_out[r], u(z[r])> for the route placed at r, 0 for a dropped one
+ *   grad_residual[r] = grad_out[r] for placed rows, 0 for the others (a bit copy)
+ * relu' is 0 at 0. Rows no route fills are zero in grad_preact and not read in grad_out and
+ * preact. The gradients of a and weights are then moe_expert_gemm_dgrad and
+ * moe_expert_gemm_wgrad of grad_preact (with n = nz); that of a gathered residual is
+ * moe_dispatch_backward of grad_out.
+ *   grad_out [rows, n]; preact [rows, nz] as kept by the forward (NULL allowed for
+ *   MOE_ACT_NONE, not gated and without grad_topk_w: nothing needs it); both of dtype.
+ *   topk_w [s, k] or NULL as in the forward; grad_preact [rows, nz] of dtype, grad_bias
+ *   [e, nz] of bias_dtype (MOE_F32 or dtype), grad_topk_w [s, k] float32 (needs topk_w),
+ *   grad_residual [rows, n] of dtype: each may be NULL (not wanted). The outputs of rows may
+ *   not overlap the inputs of rows or each other.
+ *   workspace: moe_expert_act_backward_workspace_bytes bytes, 256-byte aligned (may be NULL
+ *   if grad_bias and grad_topk_w are; not kept after the call; calls that may overlap in
+ *   time need one each).
+ */
+size_t moe_expert_act_backward_workspace_bytes(const moe_layout_t* layout, int32_t n,
+                                               int32_t gated);
+moe_status_t moe_expert_act_backward(const moe_layout_t* layout, const void* grad_out,
+                                     const void* preact, int32_t n, moe_dtype_t dtype,
+                                     int32_t activation, int32_t gated, const float* topk_w,
+                                     void* grad_preact, moe_dtype_t bias_dtype, void* grad_bias,
+                                     float* grad_topk_w, void* grad_residual, void* workspace,
+                                     size_t workspace_bytes, void* stream);
+
+/*
  * Input-row gradient of moe_expert_gemm ([DS-8213] first commit: the backward replays the
  * forward's grouping on the same handle; review-fix commit: the groups are the offsets'
  * segments). For expert x and each row r in [offsets[x], offsets[x] + kept[x]):

@@ -56,3 +56,4 @@ from .moe import (  # noqa: F401
     FLAG_REPLAY_MISMATCH,
 )
 from .router import Balance, balance_loss, balance_loss_backward  # noqa: F401
+from .epilogue import expert_act_backward, expert_gemm_act  # noqa: F401
