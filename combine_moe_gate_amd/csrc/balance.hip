@@ -82,9 +82,12 @@ __device__ __forceinline__ float lanes_reduce(float v, Op op) {
     v = op(v, dpp_move<0x140>(v));  // row_mirror
   }
   if constexpr (LPT == 64) {
-    auto at = [&](int l) { return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), l)); };
-    const float a = at(0), b = at(16), c = at(32), d = at(48);
-    v = op(op(a, b), op(c, d));
+    // gfx950's swaps give every lane the values of its own and of the neighbouring row, then
+    // of both halves of the wave
+    const auto p = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    v = op(__uint_as_float(p[0]), __uint_as_float(p[1]));
+    const auto q = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    v = op(__uint_as_float(q[0]), __uint_as_float(q[1]));
   }
   return v;
 }
@@ -198,7 +201,7 @@ template <int LPT, int NV, bool VEC>
 __global__ __launch_bounds__(kBalBlock) void balance_tile_kernel(BalanceArgs a, int tile, int pitch, bool single,
                                                                  BalancePartials part, BalanceOut out) {
   constexpr int kGroups = kBalBlock / LPT;  // tokens in work at once
-  constexpr int U = NV >= 16 ? 1 : 2;       // rows loaded ahead of the softmax
+  constexpr int U = NV >= 16 ? 2 : 4;       // rows loaded ahead of the softmax
   constexpr int kCols = LPT * NV;
   __shared__ float sums[kBalWaves][kCols];
   __shared__ int32_t hist[kCols];
@@ -340,7 +343,7 @@ __global__ __launch_bounds__(kBalBlock) void balance_reduce_kernel(BalanceArgs a
   double p[4] = {0.0, 0.0, 0.0, 0.0};
   int32_t q[4] = {0, 0, 0, 0};
   if (c4 < pitch) {
-#pragma unroll 4
+#pragma unroll 8
     for (int i = row; i < ns; i += kRows) {
       const size_t at = static_cast<size_t>(s0 + i) * pitch + c4;
       const chunk_t v = *reinterpret_cast<const chunk_t*>(part.probs + at);
@@ -403,7 +406,7 @@ __global__ __launch_bounds__(kBalBlock) void balance_backward_kernel(
     BalanceArgs a, int tile, const int32_t* __restrict__ counts, const int32_t* __restrict__ tokens,
     const float* __restrict__ grad_loss, const float* __restrict__ grad_z, float* __restrict__ grad) {
   constexpr int kGroups = kBalBlock / LPT;
-  constexpr int U = NV >= 16 ? 1 : 2;
+  constexpr int U = NV >= 16 ? 2 : 4;
   const int tid = threadIdx.x;
   const int r = tid % LPT, gid = tid / LPT;
   const int t0 = blockIdx.x * tile;
@@ -528,7 +531,7 @@ hipError_t launch_balance_loss_backward(const BalanceArgs& a, const int32_t* cou
   if (a.s == 0) return hipSuccess;
   with_rows(a.e, rows16(a.logits, a.e) && rows16(grad_logits, a.e), [&](auto shape, auto vec) {
     using S = decltype(shape);
-    constexpr int kAtOnce = kBalBlock / S::lpt * (S::nv >= 16 ? 1 : 2);
+    constexpr int kAtOnce = kBalBlock / S::lpt * (S::nv >= 16 ? 2 : 4);
     // whole rounds of tokens, up to 2048 workgroups
     int tile = (a.s + 2047) / 2048;
     tile = (tile + kAtOnce - 1) / kAtOnce * kAtOnce;

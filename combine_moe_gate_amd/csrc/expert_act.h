@@ -15,11 +15,31 @@ __device__ __forceinline__ float sigmoid(float x) {
 constexpr float kTanhB = 1.5957691216057308f;   // 2 sqrt(2 / pi)
 constexpr float kTanhQ = 0.044715f;
 
+// Phi(z), the normal distribution function, with E = exp(-z^2 / 2) on the way (Abramowitz and
+// Stegun, Handbook of Mathematical Functions, formula 7.1.26: erfc within 1.5e-7 as a fifth
+// degree polynomial in 1 / (1 + 0.3275911 x) times exp(-x^2), x = |z| / sqrt 2). A third of
+// the library erff's instructions, which a tile's epilogue pays for each of its outputs: on
+// 65536 x 4096 outputs of 1024 products each the kernel takes 0.60 ms with it, 0.71 without.
+__device__ __forceinline__ float normal_cdf(float z, float* E) {
+  const float x = __builtin_fabsf(z) * 0.7071067811865476f;
+  const float t = __builtin_amdgcn_rcpf(__builtin_fmaf(0.3275911f, x, 1.0f));
+  float q = __builtin_fmaf(t, 0.5f * 1.061405429f, 0.5f * -1.453152027f);
+  q = __builtin_fmaf(t, q, 0.5f * 1.421413741f);
+  q = __builtin_fmaf(t, q, 0.5f * -0.284496736f);
+  q = __builtin_fmaf(t, q, 0.5f * 0.254829592f);
+  *E = __builtin_amdgcn_exp2f(x * x * -1.4426950408889634f);
+  q = q * t * *E;  // erfc(x) / 2
+  return z < 0.0f ? q : 1.0f - q;
+}
+
 // act(z); gelu_tanh through tanh(y) = 2 sigmoid(2 y) - 1.
 __device__ __forceinline__ float activate(int act, float z) {
   switch (act) {
     case kActRelu: return z > 0.0f || z != z ? z : 0.0f;
-    case kActGelu: return 0.5f * z * (1.0f + erff(z * 0.7071067811865476f));
+    case kActGelu: {
+      float E;
+      return z * normal_cdf(z, &E);
+    }
     case kActGeluTanh: return z * sigmoid(kTanhB * (z + kTanhQ * z * z * z));
     case kActSilu: return z * sigmoid(z);
     default: return z;
@@ -123,6 +143,92 @@ __device__ __forceinline__ void zero_unfilled(const ExpertAct& p, int b, int nb)
     for (int r = p.offsets[x] + p.kept[x] + sub; r < p.offsets[x + 1]; r += per) clear(r);
   }
   for (int64_t r = static_cast<int64_t>(p.offsets[p.e]) + wave; r < p.rows; r += waves) clear(static_cast<int>(r));
+}
+
+// Inclusive sum over the wave's lanes, by DPP moves alone: shifts by 1, 2, 4, 8 within each
+// row of 16, then each odd row takes the last lane before it, then the upper half.
+__device__ __forceinline__ int wave_scan(int v) {
+  v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xf, 0xf, false);  // row_shr:1
+  v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xf, 0xf, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xf, 0xf, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xf, 0xf, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xa, 0xf, false);  // row_bcast:15 into rows 1, 3
+  v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xc, 0xf, false);  // row_bcast:31 into rows 2, 3
+  return v;
+}
+
+struct SegmentTile {
+  int expert;      // -1: this workgroup has no tile
+  int rows;        // placed rows of the expert
+  int offset;      // its first buffer row
+  int blocks;      // its row-blocks
+  int rb, cb;      // row-block and column-block
+};
+
+// This workgroup's tile. A segment of r rows has blocks(r) row-blocks. The tiles of all
+// experts are numbered expert by expert, inside an expert in bands of `band` row-blocks,
+// column-block by column-block, row-block fastest; workgroup b (dealt round-robin over the 8
+// XCDs) takes tile (b mod 8) T8 + b / 8, T8 = ceil(tiles / 8), so that each XCD walks one
+// stretch of that order and its resident workgroups share weights and rows through its L2.
+// Each lane holds up to 16 neighbouring experts, so one load round and one scan find it.
+template <class Blocks>
+__device__ __forceinline__ SegmentTile segment_tile(int b, int e, const int32_t* __restrict__ kept,
+                                                    const int32_t* __restrict__ offsets, int col_blocks, int band,
+                                                    Blocks blocks) {
+  const int lane = lane_id();
+  const int each = (e + kWave - 1) / kWave;  // at most 16
+  int rows[16], offs[16], sum = 0;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    rows[i] = offs[i] = 0;
+    if (i < each) {  // uniform
+      const int x = lane * each + i;
+      if (x < e) {
+        rows[i] = kept[x];
+        offs[i] = offsets[x];
+      }
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < 16; ++i)
+    if (i < each) sum += blocks(rows[i]);
+  const int upto = wave_scan(sum);
+  const int total = __builtin_amdgcn_readlane(upto, kWave - 1);
+  SegmentTile tc{-1, 0, 0, 0, 0, 0};
+  const int64_t tiles = static_cast<int64_t>(total) * col_blocks;
+  const int64_t per_xcd = (tiles + kXcds - 1) / kXcds;
+  const int64_t slot = b / kXcds, t = (b % kXcds) * per_xcd + slot;
+  if (slot >= per_xcd || t >= tiles) return tc;
+  const int q = static_cast<int>(t / col_blocks);  // its ordinal among the row-blocks, less the band order
+  int run = upto - sum, at = 0, at_rows = 0, at_off = 0, first = 0;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    if (i < each) {
+      const int nb = blocks(rows[i]);
+      if (q >= run && q < run + nb) {
+        at = lane * each + i;
+        at_rows = rows[i];
+        at_off = offs[i];
+        first = run;
+      }
+      run += nb;
+    }
+  }
+  const uint64_t hit = __ballot(q >= upto - sum && q < upto);  // one lane: the ranges partition [0, total)
+  const int owner = static_cast<int>(__builtin_ctzll(hit));
+  tc.expert = __builtin_amdgcn_readlane(at, owner);
+  tc.rows = __builtin_amdgcn_readlane(at_rows, owner);
+  tc.offset = __builtin_amdgcn_readlane(at_off, owner);
+  first = __builtin_amdgcn_readlane(first, owner);
+  tc.blocks = blocks(tc.rows);
+  const int u = static_cast<int>(t - static_cast<int64_t>(first) * col_blocks);
+  const int bd = u / (band * col_blocks);
+  const int left = tc.blocks - bd * band;
+  const int in_band = left < band ? left : band;
+  const int v = u - bd * band * col_blocks;
+  tc.cb = __builtin_amdgcn_readfirstlane(v / in_band);  // uniform as they are: kept in scalar registers
+  tc.rb = __builtin_amdgcn_readfirstlane(bd * band + v % in_band);
+  return tc;
 }
 
 }  // namespace moe

@@ -31,6 +31,7 @@
 // memory straight to the registers the MFMA reads, several steps ahead (nothing is reused,
 // so LDS would only add a stop), and the four partial sums meet in LDS.
 #include <atomic>
+#include <utility>
 
 #include "expert_act.h"
 
@@ -61,7 +62,7 @@ constexpr int kActAStage = kActBM * kActRowBytes, kActBStage = kActBN * kActRowB
 constexpr int kActStage = kActAStage + kActBStage;
 constexpr int kSlabPitch = 64 * 4 + 16;            // bytes per row of a wave's 16 x 64 float32 slab
 constexpr int kActLds = 2 * kActStage + kActBM * 8;
-static_assert(8 * 16 * kSlabPitch <= 2 * kActStage, "the slabs reuse the stages");
+static_assert(8 * 2 * 16 * kSlabPitch <= 2 * kActStage, "the slabs reuse the stages");
 
 // Row-blocks of a segment of `rows` rows: as few as hold it, of nearly equal height.
 __device__ __forceinline__ int act_blocks(int rows) {
@@ -70,55 +71,23 @@ __device__ __forceinline__ int act_blocks(int rows) {
 }
 
 struct ActTile {
-  int expert, unit0, units, cb;  // expert (-1: none), first 32-row unit, units, column-block
+  int expert, unit0, units, cb, rows, offset;  // expert (-1: none), first 32-row unit, units, column-block
 };
 
-// This workgroup's tile: the tiles of all experts numbered expert by expert, inside an
-// expert in bands of kActBand row-blocks, column-block by column-block, row-block fastest;
-// workgroup b takes tile (b mod 8) T8 + b / 8, so that each XCD walks one stretch of that
-// order and its resident workgroups share weight tiles and rows through its L2.
-__device__ __forceinline__ ActTile act_tile(int b, int e, const int32_t* __restrict__ kept, int col_blocks) {
-  const int lane = lane_id();
-  ActTile tc{-1, 0, 0, 0};
-  int total = 0;
-  for (int c0 = 0; c0 < e; c0 += kWave) {
-    const int x = c0 + lane;
-    total += __builtin_amdgcn_readlane(wave_inclusive_scan(x < e ? act_blocks(kept[x]) : 0), kWave - 1);
-  }
-  const int64_t tiles = static_cast<int64_t>(total) * col_blocks;
-  const int64_t per_xcd = (tiles + kXcds - 1) / kXcds;
-  const int64_t slot = b / kXcds, t = (b % kXcds) * per_xcd + slot;
-  if (slot >= per_xcd || t >= tiles) return tc;
-  int before = 0;
-  for (int c0 = 0; c0 < e; c0 += kWave) {
-    const int x = c0 + lane;
-    const int rows = x < e ? kept[x] : 0;
-    const int nb = act_blocks(rows);
-    const int incl = wave_inclusive_scan(nb);
-    const int64_t lo = static_cast<int64_t>(before + incl - nb) * col_blocks;
-    const int64_t hi = static_cast<int64_t>(before + incl) * col_blocks;
-    const uint64_t hit = __ballot(t >= lo && t < hi);
-    if (hit != 0ull) {
-      const int owner = static_cast<int>(__builtin_ctzll(hit));
-      const int R = __builtin_amdgcn_readlane(nb, owner);
-      const int units = (__builtin_amdgcn_readlane(rows, owner) + 31) / 32;
-      const int first = before + __builtin_amdgcn_readlane(incl, owner) - R;
-      const int u = static_cast<int>(t - static_cast<int64_t>(first) * col_blocks);
-      const int band = u / (kActBand * col_blocks);
-      const int left = R - band * kActBand;
-      const int in_band = left < kActBand ? left : kActBand;
-      const int v = u - band * kActBand * col_blocks;
-      const int rb = band * kActBand + v % in_band;
-      const int base = units / R, extra = units % R;  // the first `extra` blocks are a unit taller
-      tc.expert = c0 + owner;
-      tc.cb = v / in_band;
-      tc.units = base + (rb < extra);
-      tc.unit0 = rb * base + (rb < extra ? rb : extra);
-      return tc;
-    }
-    before += __builtin_amdgcn_readlane(incl, kWave - 1);
-  }
-  return tc;
+__device__ __forceinline__ ActTile act_tile(int b, int e, const int32_t* __restrict__ kept,
+                                            const int32_t* __restrict__ offsets, int col_blocks) {
+  const SegmentTile s = segment_tile(b, e, kept, offsets, col_blocks, kActBand, [](int r) { return act_blocks(r); });
+  if (s.expert < 0) return ActTile{-1, 0, 0, 0, 0, 0};
+  const int units = (s.rows + 31) / 32;
+  const int base = units / s.blocks, extra = units % s.blocks;  // the first `extra` blocks are a unit taller
+  return ActTile{s.expert, s.rb * base + (s.rb < extra ? s.rb : extra), base + (s.rb < extra), s.cb, s.rows,
+                 s.offset};
+}
+
+// f(0), f(1), ... with compile-time arguments.
+template <int... I, class F>
+__device__ __forceinline__ void static_for(std::integer_sequence<int, I...>, F f) {
+  (f(std::integral_constant<int, I>{}), ...);
 }
 
 // The tile's products and its epilogue, for a height of 32 FM rows.
@@ -134,34 +103,18 @@ __device__ __forceinline__ void act_tile_body(const ExpertAct& p, const ActTile&
   const int lane = lane_id(), wv = wave_in_block();
   const int wm = wv / 4, wn = wv % 4;
   const int x = tc.expert;
-  const int row0 = p.offsets[x] + tc.unit0 * 32;
-  const int rem = p.kept[x] - tc.unit0 * 32;
+  const int row0 = tc.offset + tc.unit0 * 32;
+  const int rem = tc.rows - tc.unit0 * 32;
   const int nrows = rem < 32 * FM ? rem : 32 * FM;
   const int out_cols = p.gated ? kActBN / 2 : kActBN;
   const int col0 = tc.cb * out_cols;                   // first output feature
   const int kchunks = p.m / 8, nk = (p.m + 63) / 64;
-
-  // per tile row: its token and route weight, for the epilogue
-  int* row_token = reinterpret_cast<int*>(lds + 2 * kActStage);
-  float* row_weight = reinterpret_cast<float*>(lds + 2 * kActStage + kActBM * 4);
-  if (static_cast<int>(threadIdx.x) < nrows) {
-    const int r = row0 + threadIdx.x;
-    const int t = p.src[r];
-    row_token[threadIdx.x] = t;
-    row_weight[threadIdx.x] = p.route_w != nullptr ? route_weight(p, r, t) : 1.0f;
-  }
 
   // staged row and chunk of each load of this lane. Rows past the segment repeat its first
   // one and weight rows past the last repeat it: both reach only results never stored.
   const chunk_t* a_row[kALoads];
   const chunk_t* b_row[4];
   const chunk_t* wx = static_cast<const chunk_t*>(p.w) + static_cast<size_t>(x) * p.nz * kchunks;
-#pragma unroll
-  for (int q = 0; q < kALoads; ++q) {
-    const int r = (q * 8 + wv) * 8 + lane / 8;
-    const int rr = row0 + (r < nrows ? r : 0);
-    a_row[q] = static_cast<const chunk_t*>(p.a) + static_cast<size_t>(p.gather ? p.src[rr] : rr) * kchunks;
-  }
 #pragma unroll
   for (int q = 0; q < 4; ++q) {
     const int r = (q * 8 + wv) * 8 + lane / 8;
@@ -178,20 +131,49 @@ __device__ __forceinline__ void act_tile_body(const ExpertAct& p, const ActTile&
   // multiples of 8, so R / 2 % 8 = 4 (load % 2) + lane / 16
   const int swz = 4 * (wv % 2) + lane / 16;
   const int chunk = (lane % 8) ^ swz;
-  auto issue = [&](int kt) {
-    char* st = lds + (kt % 2) * kActStage;
+  auto chunk_at = [&](int kt) {
     const int kq = kt * 8 + chunk;
-    const int at = kq < kchunks ? kq : 0;  // past the row's end: its first chunk, cleared once landed
+    return kq < kchunks ? kq : 0;  // past the row's end: its first chunk, cleared once landed
+  };
+  auto issue_b = [&](int kt) {
+    char* st = lds + (kt % 2) * kActStage + kActAStage;
+    const int at = chunk_at(kt);
 #pragma unroll
     for (int q = 0; q < 4; ++q)
       __builtin_amdgcn_global_load_lds(static_cast<const void*>(b_row[q] + at),
-                                       (lds_void_t*)(st + kActAStage + (q * 8 + wv) * 1024), 16, 0, 0);
+                                       (lds_void_t*)(st + (q * 8 + wv) * 1024), 16, 0, 0);
+  };
+  // the weights' first loads start before the rows' addresses are read from the layout
+  issue_b(0);
+  if (nk > 1) issue_b(1);
+  __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+  for (int q = 0; q < kALoads; ++q) {
+    const int r = (q * 8 + wv) * 8 + lane / 8;
+    const int rr = row0 + (r < nrows ? r : 0);
+    a_row[q] = static_cast<const chunk_t*>(p.a) + static_cast<size_t>(p.gather ? p.src[rr] : rr) * kchunks;
+  }
+  auto issue_a = [&](int kt) {
+    char* st = lds + (kt % 2) * kActStage;
+    const int at = chunk_at(kt);
 #pragma unroll
     for (int q = 0; q < kALoads; ++q)
       if (q * 8 + wv < 4 * FM)  // uniform
         __builtin_amdgcn_global_load_lds(static_cast<const void*>(a_row[q] + at),
                                          (lds_void_t*)(st + (q * 8 + wv) * 1024), 16, 0, 0);
   };
+  issue_a(0);
+  if (nk > 1) issue_a(1);
+  // per tile row: its token and route weight, for the epilogue
+  int* row_token = reinterpret_cast<int*>(lds + 2 * kActStage);
+  float* row_weight = reinterpret_cast<float*>(lds + 2 * kActStage + kActBM * 4);
+  if (static_cast<int>(threadIdx.x) < nrows) {
+    const int r = row0 + threadIdx.x;
+    const int t = p.src[r];
+    row_token[threadIdx.x] = t;
+    row_weight[threadIdx.x] = p.route_w != nullptr ? route_weight(p, r, t) : 1.0f;
+  }
+
   auto clear_tail = [&](int kt) {
     if (kt * 8 + chunk < kchunks) return;
     char* st = lds + (kt % 2) * kActStage;
@@ -232,7 +214,7 @@ __device__ __forceinline__ void act_tile_body(const ExpertAct& p, const ActTile&
   };
   // step kt is whole in LDS and every wave has read out the step before it
   auto publish = [&](int kt) {
-    __builtin_amdgcn_s_waitcnt(wait_vm(0) & kWaitLdsOnly);  // all loads and LDS operations
+    __builtin_amdgcn_s_waitcnt(wait_vm(0) & ~0xF00);  // all loads and LDS operations
     if ((kt + 1) * 8 > kchunks) {
       clear_tail(kt);
       __builtin_amdgcn_s_waitcnt(kWaitLdsOnly);
@@ -240,9 +222,7 @@ __device__ __forceinline__ void act_tile_body(const ExpertAct& p, const ActTile&
     stage_barrier();
   };
 
-  issue(0);
   publish(0);
-  if (nk > 1) issue(1);
   chunk_t fa[2][4], fb[2][FN];
   read_a(0, 0, fa[0]);
   read_b(0, 0, fb[0]);
@@ -263,7 +243,10 @@ __device__ __forceinline__ void act_tile_body(const ExpertAct& p, const ActTile&
       } else {
         if (kt + 1 < nk) {
           publish(kt + 1);
-          if (kt + 2 < nk) issue(kt + 2);
+          if (kt + 2 < nk) {
+            issue_b(kt + 2);
+            issue_a(kt + 2);
+          }
         }
         __builtin_amdgcn_sched_barrier(0);
         read_a(kt + 1, 0, fa[(g + 1) % 2]);
@@ -287,36 +270,50 @@ __device__ __forceinline__ void act_tile_body(const ExpertAct& p, const ActTile&
     }
   }
 
-  // epilogue: each 16-row tile's sums through the wave's slab. Lane l holds token row
-  // l % 16, features 16 j + 4 (l / 16) .. + 3 of its 64; it takes back row l / 4, features
-  // 8 (l % 4) .. + 7 of each 32 (gated: the gate's and the up's).
+  // epilogue: each 16-row tile's sums through one of the wave's two slabs. Lane l holds token
+  // row l % 16, features 16 j + 4 (l / 16) .. + 3 of its 64; it takes back row l / 4, features
+  // 8 (l % 4) .. + 7 of each 32 (gated: the gate's and the up's). The next tile goes through
+  // LDS while one is finished.
   __syncthreads();
-  char* slab = lds + wv * 16 * kSlabPitch;
-#pragma unroll 1
-  for (int i = 0; i < FM; ++i) {
-    if (wm * 16 * FM + i * 16 >= nrows) break;  // uniform
-#pragma unroll
-    for (int ii = 0; ii < FM; ++ii)
+  char* slabs = lds + wv * 2 * 16 * kSlabPitch;
+  const int below = nrows - wm * 16 * FM;
+  const int tiles = below <= 0 ? 0 : below < 16 * FM ? (below + 15) / 16 : FM;
+  auto pass = [&](int i, float (&v)[8], float (&u)[8]) __attribute__((always_inline)) {
+    char* slab = slabs + (i % 2) * 16 * kSlabPitch;
+    static_for(std::make_integer_sequence<int, FM>{}, [&](auto ii) __attribute__((always_inline)) {
       if (ii == i) {
 #pragma unroll
         for (int j = 0; j < FN; ++j)
           *reinterpret_cast<f32x4_t*>(slab + (lane & 15) * kSlabPitch + j * 64 + (lane >> 4) * 16) = acc[ii][j];
+        // the empty asm keeps the branches apart: with their stores folded into one, they
+        // would index the accumulators dynamically and so move them to memory
+        asm volatile("" ::"i"(decltype(ii)::value) : "memory");
       }
-    const int row = wm * 16 * FM + i * 16 + (lane >> 2);
+    });
     const float* back = reinterpret_cast<const float*>(slab + (lane >> 2) * kSlabPitch) + 8 * (lane & 3);
-    float v[8], u[8];
 #pragma unroll
     for (int q = 0; q < 8; ++q) {
       v[q] = back[q];
       u[q] = back[32 + q];
     }
-    if (row < nrows) {
-      const int r = row0 + row, t = row_token[row];
-      const float w = row_weight[row];
-      const int c = col0 + wn * (out_cols / 4) + 8 * (lane & 3);
-      if (c < p.n) finish8<DT>(p, x, r, t, w, c, v, u);
-      if (!p.gated && c + 32 < p.n) finish8<DT>(p, x, r, t, w, c + 32, u, v);
-    }
+  };
+  auto finish = [&](int i, float (&v)[8], float (&u)[8]) __attribute__((always_inline)) {
+    const int row = wm * 16 * FM + i * 16 + (lane >> 2);
+    if (row >= nrows) return;
+    const int r = row0 + row, t = row_token[row];
+    const float w = row_weight[row];
+    const int c = col0 + wn * (out_cols / 4) + 8 * (lane & 3);
+    if (c < p.n) finish8<DT>(p, x, r, t, w, c, v, u);
+    if (!p.gated && c + 32 < p.n) finish8<DT>(p, x, r, t, w, c + 32, u, v);
+  };
+  float v[2][8], u[2][8];
+  if (tiles > 0) pass(0, v[0], u[0]);
+#pragma unroll 1
+  for (int i = 0; i < tiles; i += 2) {  // uniform conditions
+    if (i + 1 < tiles) pass(i + 1, v[1], u[1]);
+    finish(i, v[0], u[0]);
+    if (i + 2 < tiles) pass(i + 2, v[0], u[0]);
+    if (i + 1 < tiles) finish(i + 1, v[1], u[1]);
   }
 }
 
@@ -328,7 +325,7 @@ __global__ __launch_bounds__(kActThreads) __attribute__((amdgpu_waves_per_eu(2, 
     zero_unfilled(p, blockIdx.x - tile_grid, gridDim.x - tile_grid);
     return;
   }
-  const ActTile tc = act_tile(blockIdx.x, p.e, p.kept, col_blocks);
+  const ActTile tc = act_tile(blockIdx.x, p.e, p.kept, p.offsets, col_blocks);
   if (tc.expert < 0) return;
   switch (tc.units) {
     case 1: act_tile_body<DT, 1>(p, tc, lds); break;
@@ -347,62 +344,67 @@ __global__ __launch_bounds__(kActThreads) __attribute__((amdgpu_waves_per_eu(2, 
 // few rows
 
 constexpr int kFewThreads = 256, kFewWaves = 4;
-constexpr int kFewCols = 64;  // weight rows per workgroup
 
-template <int DT, int F>
-__global__ __launch_bounds__(kFewThreads) void expert_act_few_kernel(ExpertAct p, int col_blocks, int tile_grid) {
-  constexpr int kDepth = F == 4 ? 2 : 3;  // K steps of 64 elements in flight per wave
-  extern __shared__ __attribute__((aligned(1024))) char lds[];  // [wave][16 F rows][kSlabPitch]
+template <int DT, int F, int FB>
+__global__ __launch_bounds__(kFewThreads, F == 4 ? 2 : F == 2 || FB == 4 ? 3 : 4) void expert_act_few_kernel(ExpertAct p, int col_blocks,
+                                                                                  int tile_grid) {
+  constexpr int kDepth = F == 4 ? 1 : FB == 2 ? 4 : F == 1 ? 3 : 2;  // K steps of 64 elements in flight per wave
+  constexpr int kCols = 16 * FB;                        // weight rows per workgroup
+  constexpr int kPitch = kCols * 4 + 16;                // bytes per row of a wave's float32 sums
+  extern __shared__ __attribute__((aligned(1024))) char lds[];  // [wave][16 F rows][kPitch]
   if (static_cast<int>(blockIdx.x) >= tile_grid) {
     zero_unfilled(p, blockIdx.x - tile_grid, gridDim.x - tile_grid);
     return;
   }
-  const TileCoord tc = find_tile<16 * F>(blockIdx.x, p.e, p.kept, col_blocks, kActBand);
+  const SegmentTile tc =
+      segment_tile(blockIdx.x, p.e, p.kept, p.offsets, col_blocks, kActBand, [](int r) { return (r + 16 * F - 1) / (16 * F); });
   const int x = tc.expert;
   if (x < 0) return;
   const int lane = lane_id(), wv = wave_in_block();
-  const int row0 = p.offsets[x] + tc.rb * 16 * F;
-  const int rem = p.kept[x] - tc.rb * 16 * F;
+  const int row0 = tc.offset + tc.rb * 16 * F;
+  const int rem = tc.rows - tc.rb * 16 * F;
   const int nrows = rem < 16 * F ? rem : 16 * F;
-  const int out_cols = p.gated ? kFewCols / 2 : kFewCols;
+  const int out_cols = p.gated ? kCols / 2 : kCols;
   const int col0 = tc.cb * out_cols;
   const int kchunks = p.m / 8;
 
   const chunk_t* a_row[F];
-  const chunk_t* b_row[4];
 #pragma unroll
   for (int i = 0; i < F; ++i) {
     const int r = i * 16 + (lane & 15);
     const int rr = row0 + (r < nrows ? r : 0);
     a_row[i] = static_cast<const chunk_t*>(p.a) + static_cast<size_t>(p.gather ? p.src[rr] : rr) * kchunks + (lane >> 4);
   }
+  // The first half of the fragments are gate rows and the second the up rows that meet them,
+  // or all are plain; each fragment by a uniform base and a lane's own offset in its 16 rows.
+  const char* b_base[FB];
+  uint32_t b_off[FB];
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    int f;
-    if (p.gated) {
-      f = col0 + (j & 1) * 16 + (lane & 15);
-      f = (f < p.n ? f : p.n - 1) + (j >= 2 ? p.n : 0);
-    } else {
-      f = col0 + j * 16 + (lane & 15);
-      f = f < p.n ? f : p.n - 1;
-    }
-    b_row[j] = static_cast<const chunk_t*>(p.w) + (static_cast<size_t>(x) * p.nz + f) * kchunks + (lane >> 4);
+  for (int j = 0; j < FB; ++j) {
+    int f = p.gated ? col0 + j % (FB / 2) * 16 : col0 + j * 16;
+    f = f < p.n ? f : 0;  // past the last feature: any rows, their sums are not stored
+    const int have = p.n - f < 16 ? p.n - f : 16;
+    const int first = p.gated && j >= FB / 2 ? p.n + f : f;
+    b_base[j] = static_cast<const char*>(p.w) + (static_cast<size_t>(x) * p.nz + first) * kchunks * 16;
+    b_off[j] = static_cast<uint32_t>((lane & 15) < have ? lane & 15 : 0) * kchunks * 16u + (lane >> 4) * 16u;
   }
 
-  f32x4_t acc[F][4];
+  f32x4_t acc[F][FB];
 #pragma unroll
   for (int i = 0; i < F; ++i)
 #pragma unroll
-    for (int j = 0; j < 4; ++j) acc[i][j] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+    for (int j = 0; j < FB; ++j) acc[i][j] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
 
-  chunk_t fa[kDepth][2][F], fb[kDepth][2][4];
+  chunk_t fa[kDepth][2][F], fb[kDepth][2][FB];
   const int full = kchunks / 8;  // whole K steps; wave wv takes steps wv, wv + 4, ...
   auto load = [&](int step, int d) {
-    const size_t at = static_cast<size_t>(step < full ? step : 0) * 8;  // past the end: loaded, not used
+    const size_t at = static_cast<size_t>(step) * 8;
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
 #pragma unroll
-      for (int j = 0; j < 4; ++j) fb[d][h][j] = __builtin_nontemporal_load(b_row[j] + at + 4 * h);
+      for (int j = 0; j < FB; ++j)
+        fb[d][h][j] = __builtin_nontemporal_load(
+            reinterpret_cast<const chunk_t*>(b_base[j] + static_cast<size_t>(step) * 128 + 64 * h + b_off[j]));
 #pragma unroll
       for (int i = 0; i < F; ++i) fa[d][h][i] = a_row[i][at + 4 * h];
     }
@@ -413,25 +415,24 @@ __global__ __launch_bounds__(kFewThreads) void expert_act_few_kernel(ExpertAct p
 #pragma unroll
       for (int i = 0; i < F; ++i)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) acc[i][j] = mfma_16x16x32<DT>(fb[d][h][j], fa[d][h][i], acc[i][j]);
+        for (int j = 0; j < FB; ++j) acc[i][j] = mfma_16x16x32<DT>(fb[d][h][j], fa[d][h][i], acc[i][j]);
   };
-  if (full > wv) {
 #pragma unroll
-    for (int d = 0; d < kDepth; ++d) load(wv + d * kFewWaves, d);
-    int step = wv;
-    for (; step + (2 * kDepth - 1) * kFewWaves < full; step += kDepth * kFewWaves) {  // every refill is a real step
+  for (int d = 0; d < kDepth; ++d)
+    if (wv + d * kFewWaves < full) load(wv + d * kFewWaves, d);  // uniform
+  int step = wv;
+  for (; step + (2 * kDepth - 1) * kFewWaves < full; step += kDepth * kFewWaves) {  // every refill is a real step
 #pragma unroll
-      for (int d = 0; d < kDepth; ++d) {
-        multiply(d);
-        load(step + (d + kDepth) * kFewWaves, d);
-      }
+    for (int d = 0; d < kDepth; ++d) {
+      multiply(d);
+      load(step + (d + kDepth) * kFewWaves, d);
     }
-    for (; step < full; step += kDepth * kFewWaves) {  // what is left: at most two rounds
+  }
+  for (; step < full; step += kDepth * kFewWaves) {  // what is left: at most two rounds
 #pragma unroll
-      for (int d = 0; d < kDepth; ++d) {  // uniform conditions
-        if (step + d * kFewWaves < full) multiply(d);
-        if (step + (d + kDepth) * kFewWaves < full) load(step + (d + kDepth) * kFewWaves, d);
-      }
+    for (int d = 0; d < kDepth; ++d) {  // uniform conditions
+      if (step + d * kFewWaves < full) multiply(d);
+      if (step + (d + kDepth) * kFewWaves < full) load(step + (d + kDepth) * kFewWaves, d);
     }
   }
   if (kchunks % 8 != 0 && wv == full % kFewWaves) {  // the last, partial step: zeros past the rows' end
@@ -441,7 +442,8 @@ __global__ __launch_bounds__(kFewThreads) void expert_act_few_kernel(ExpertAct p
       const bool in = full * 8 + 4 * h + (lane >> 4) < kchunks;
       const size_t at = static_cast<size_t>(full) * 8 + 4 * h;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) fb[0][h][j] = in ? b_row[j][at] : z;
+      for (int j = 0; j < FB; ++j)
+        fb[0][h][j] = in ? *reinterpret_cast<const chunk_t*>(b_base[j] + at * 16 + b_off[j]) : z;
 #pragma unroll
       for (int i = 0; i < F; ++i) fa[0][h][i] = in ? a_row[i][at] : z;
     }
@@ -451,28 +453,30 @@ __global__ __launch_bounds__(kFewThreads) void expert_act_few_kernel(ExpertAct p
 #pragma unroll
   for (int i = 0; i < F; ++i)
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
-      *reinterpret_cast<f32x4_t*>(lds + (wv * 16 * F + i * 16 + (lane & 15)) * kSlabPitch + j * 64 + (lane >> 4) * 16) =
+    for (int j = 0; j < FB; ++j)
+      *reinterpret_cast<f32x4_t*>(lds + (wv * 16 * F + i * 16 + (lane & 15)) * kPitch + j * 64 + (lane >> 4) * 16) =
           acc[i][j];
   __syncthreads();
-  const int row = threadIdx.x / 4, q8 = 8 * (threadIdx.x % 4);
+  // a thread per row and eight features of each half
+  constexpr int kPieces = FB;  // 16 FB / 2 / 8
+  const int row = threadIdx.x / kPieces, q8 = 8 * (threadIdx.x % kPieces);
   if (row >= nrows) return;
   float v[8], u[8];
 #pragma unroll
   for (int q = 0; q < 8; ++q) v[q] = u[q] = 0.0f;
   for (int w = 0; w < kFewWaves; ++w) {
-    const float* part = reinterpret_cast<const float*>(lds + (w * 16 * F + row) * kSlabPitch) + q8;
+    const float* part = reinterpret_cast<const float*>(lds + (w * 16 * F + row) * kPitch) + q8;
 #pragma unroll
     for (int q = 0; q < 8; ++q) {
       v[q] += part[q];
-      u[q] += part[32 + q];
+      u[q] += part[8 * FB + q];
     }
   }
   const int r = row0 + row, t = p.src[r];
   const float w = p.route_w != nullptr ? route_weight(p, r, t) : 1.0f;
   const int c = col0 + q8;
   if (c < p.n) finish8<DT>(p, x, r, t, w, c, v, u);
-  if (!p.gated && c + 32 < p.n) finish8<DT>(p, x, r, t, w, c + 32, u, v);
+  if (!p.gated && c + 8 * FB < p.n) finish8<DT>(p, x, r, t, w, c + 8 * FB, u, v);
 }
 
 // ---------------------------------------------------------------------------------
@@ -502,13 +506,27 @@ static int64_t row_tiles(const LayoutView& L, int height) {
   return routes / height + with_rows;
 }
 
+// How a launch is shaped: F (above) and the weight rows per workgroup.
+struct ActShape {
+  int few, cols;
+  int64_t col_blocks, tiles;
+};
+static ActShape act_shape(const LayoutView& L, int n, bool gated) {
+  ActShape a{L.s == 0 ? 1 : few_rows(L), kActBN, 0, 0};
+  const int per = gated ? 2 : 1;
+  auto fit = [&](int cols) {
+    a.cols = cols;
+    a.col_blocks = (static_cast<int64_t>(n) * per + cols - 1) / cols;
+    a.tiles = L.s == 0 ? 0 : row_tiles(L, a.few ? 16 * a.few : kActBM) * a.col_blocks;
+  };
+  fit(a.few ? 64 : kActBN);
+  // half as wide where that leaves fewer than four workgroups per CU
+  if (a.few == 1 && a.tiles < 1024) fit(32);
+  return a;
+}
+
 int64_t expert_act_grid(const LayoutView& L, int n, bool gated) {
-  if (L.s == 0) return kZeroBlocks;
-  const int few = few_rows(L);
-  const int cols = (few ? kFewCols : kActBN) / (gated ? 2 : 1);
-  const int64_t col_blocks = (n + cols - 1) / cols;
-  const int64_t tiles = row_tiles(L, few ? 16 * few : kActBM) * col_blocks;
-  return (tiles + kXcds - 1) / kXcds * kXcds + kZeroBlocks;
+  return (act_shape(L, n, gated).tiles + kXcds - 1) / kXcds * kXcds + kZeroBlocks;
 }
 
 // Dynamic LDS above the 64 KiB default needs the kernel's limit raised, once per device.
@@ -523,11 +541,11 @@ static hipError_t allow_lds(const void* kernel, int bytes, std::atomic<uint64_t>
   return err;
 }
 
-template <int DT, int F>
+template <int DT, int F, int FB>
 static hipError_t launch_few(const ExpertAct& p, int col_blocks, int64_t grid, hipStream_t stream) {
   static std::atomic<uint64_t> done{0};
-  constexpr int kBytes = kFewWaves * 16 * F * kSlabPitch;
-  auto kern = expert_act_few_kernel<DT, F>;
+  constexpr int kBytes = kFewWaves * 16 * F * (16 * FB * 4 + 16);
+  auto kern = expert_act_few_kernel<DT, F, FB>;
   if (kBytes > 65536) {
     const hipError_t err = allow_lds(reinterpret_cast<const void*>(kern), kBytes, done);
     if (err != hipSuccess) return err;
@@ -538,16 +556,13 @@ static hipError_t launch_few(const ExpertAct& p, int col_blocks, int64_t grid, h
 
 template <int DT>
 static hipError_t launch_dt(const LayoutView& L, const ExpertAct& p, hipStream_t stream) {
+  const ActShape a = act_shape(L, p.n, p.gated);
   const int64_t grid = expert_act_grid(L, p.n, p.gated);
-  const int few = L.s == 0 ? 1 : few_rows(L);
-  const int cols = (few ? kFewCols : kActBN) / (p.gated ? 2 : 1);
-  const int col_blocks = (p.n + cols - 1) / cols;
-  switch (few) {
-    case 1: return launch_few<DT, 1>(p, col_blocks, grid, stream);
-    case 2: return launch_few<DT, 2>(p, col_blocks, grid, stream);
-    case 4: return launch_few<DT, 4>(p, col_blocks, grid, stream);
-    default: break;
-  }
+  const int col_blocks = static_cast<int>(a.col_blocks);
+  if (a.few == 1 && a.cols == 32) return launch_few<DT, 1, 2>(p, col_blocks, grid, stream);
+  if (a.few == 1) return launch_few<DT, 1, 4>(p, col_blocks, grid, stream);
+  if (a.few == 2) return launch_few<DT, 2, 4>(p, col_blocks, grid, stream);
+  if (a.few == 4) return launch_few<DT, 4, 4>(p, col_blocks, grid, stream);
   static std::atomic<uint64_t> done{0};
   auto kern = expert_act_kernel<DT>;
   const hipError_t err = allow_lds(reinterpret_cast<const void*>(kern), kActLds, done);

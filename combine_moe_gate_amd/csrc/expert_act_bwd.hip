@@ -32,9 +32,10 @@ __device__ __forceinline__ void act_and_slope(float z, float* f, float* d) {
     *d = z > 0.0f ? 1.0f : 0.0f;
   } else if constexpr (ACT == kActGelu) {
     const float y = clamp_to(z, 30.0f);
-    const float cdf = 0.5f * (1.0f + erff(y * 0.7071067811865476f));
+    float E;
+    const float cdf = normal_cdf(y, &E);
     *f = z * cdf;
-    *d = cdf + y * 0.3989422804014327f * __builtin_amdgcn_exp2f(y * y * -0.7213475204444817f);
+    *d = cdf + y * 0.3989422804014327f * E;
   } else if constexpr (ACT == kActGeluTanh) {
     const float y = clamp_to(z, 12.0f);
     const float s = sigmoid(kTanhB * (y + kTanhQ * y * y * y));
@@ -80,11 +81,12 @@ __global__ __launch_bounds__(kBwdThreads) void expert_act_backward_kernel(Expert
     for (int64_t r = static_cast<int64_t>(p.offsets[p.e]) + wave; r < p.rows; r += waves) clear(static_cast<int>(r));
     return;
   }
-  const TileCoord tc = find_tile<kBwdRows>(blockIdx.x, p.e, p.kept, col_blocks, 8);
+  const SegmentTile tc =
+      segment_tile(blockIdx.x, p.e, p.kept, p.offsets, col_blocks, 8, [](int r) { return (r + kBwdRows - 1) / kBwdRows; });
   const int x = tc.expert;
   if (x < 0) return;
-  const int row0 = p.offsets[x] + tc.rb * kBwdRows;
-  const int rem = p.kept[x] - tc.rb * kBwdRows;
+  const int row0 = tc.offset + tc.rb * kBwdRows;
+  const int rem = tc.rows - tc.rb * kBwdRows;
   const int nrows = rem < kBwdRows ? rem : kBwdRows;
   const int c = tc.cb * kBwdCols + 8 * lane;
   const bool in = c < p.n;
@@ -155,7 +157,7 @@ __global__ __launch_bounds__(kBwdThreads) void expert_act_backward_kernel(Expert
   if (p.grad_bias == nullptr) return;
   // Tile rb of expert x owns partial row offsets[x] / kBwdRows + x + rb: as floor(a + b) >=
   // floor(a) + ceil(b) - 1, the next expert's first is past this one's last.
-  const size_t slot = static_cast<size_t>(p.offsets[x] / kBwdRows) + x + tc.rb;
+  const size_t slot = static_cast<size_t>(tc.offset / kBwdRows) + x + tc.rb;
 #pragma unroll
   for (int h = 0; h < H; ++h) {
     __syncthreads();
