@@ -15,6 +15,7 @@ function names are those of the C ABI in include/moe_gate.h:
     flags, checksum = moe_layout_read(layout)              # synchronises; tests/debug
     h       = moe_expert_gemm_act(layout, x, weights, bias=b, act="silu", gated=True)
     gz, gb, gw, gr = moe_expert_act_backward(layout, grad_h, preact, act="silu", gated=True)
+    ga      = moe_expert_act_dgrad(layout, gz, weights)    # rows' gradient; weights': moe_expert_gemm_wgrad
     counts, tokens, probs, loss, z = moe_balance_loss(logits, idx, mask, groups)
     gl      = moe_balance_loss_backward(logits, counts, tokens, k, grad_loss, grad_z, mask, groups)
 
@@ -119,6 +120,7 @@ _SIGNATURES = {
     "moe_layout_read": (ctypes.c_int, [ctypes.POINTER(LayoutStruct), _P, _P, _P]),
     "moe_expert_gemm_act": (ctypes.c_int, [ctypes.POINTER(LayoutStruct), _P, _I, _P, _I, _I, ctypes.c_int,
                                            ctypes.POINTER(Epilogue), _P, _P]),
+    "moe_expert_act_dgrad": (ctypes.c_int, [ctypes.POINTER(LayoutStruct), _P, _P, _I, _I, ctypes.c_int, _P, _P]),
     "moe_expert_act_backward_workspace_bytes": (ctypes.c_size_t, [ctypes.POINTER(LayoutStruct), _I, _I]),
     "moe_expert_act_backward": (ctypes.c_int, [ctypes.POINTER(LayoutStruct), _P, _P, _I, ctypes.c_int, _I, _I, _P, _P,
                                                ctypes.c_int, _P, _P, _P, _P, ctypes.c_size_t, _P]),
@@ -555,7 +557,7 @@ def moe_expert_act_backward(layout: Layout, grad_out: torch.Tensor, preact=None,
     without need_w). grad_preact [rows, weight rows]; grad_bias [e, weight rows] of
     bias_dtype (float32 or grad_out's dtype; None: not wanted); grad_w [s, k] float32 (needs
     w); grad_residual [rows, n], for a residual of buffer rows. The gradients of a and
-    weights are moe_expert_gemm_dgrad and _wgrad of grad_preact.
+    weights are moe_expert_act_dgrad and moe_expert_gemm_wgrad of grad_preact.
     """
     _expect(grad_out, "grad_out", (layout.rows, None), _GEMM_DTYPES)
     n, dt = grad_out.shape[1], grad_out.dtype
@@ -583,6 +585,23 @@ def moe_expert_act_backward(layout: Layout, grad_out: torch.Tensor, preact=None,
             code, int(bool(gated)), _ptr(w), _ptr(gz), _DTYPE_CODE[bias_dtype] if gb is not None else MOE_F32, _ptr(gb),
             _ptr(gw), _ptr(gr), _ptr(workspace), workspace.numel() if workspace is not None else 0)
     return gz, gb, gw, gr
+
+
+def moe_expert_act_dgrad(layout: Layout, grad_preact: torch.Tensor, weights: torch.Tensor, out=None):
+    """Input-row gradient of moe_expert_gemm_act: grad_a[r] = grad_preact[r] @ weights[x] for
+    the placed rows of expert x, [rows, m] (zero rows where no route is placed): the product
+    of moe_expert_gemm_dgrad on the forward's tiles. The token gradient of a gathered forward
+    is moe_dispatch_backward(layout, grad_a)."""
+    _expect(grad_preact, "grad_preact", (layout.rows, None), _GEMM_DTYPES)
+    nz = grad_preact.shape[1]
+    _expect(weights, "weights", (layout.e, nz, None), grad_preact.dtype)
+    m = weights.shape[2]
+    _expect(out, "out", (layout.rows, m), grad_preact.dtype)
+    _same_device(layout, grad_preact, weights, out)
+    out = out if out is not None else torch.empty((layout.rows, m), dtype=grad_preact.dtype, device=grad_preact.device)
+    _launch(grad_preact, lib().moe_expert_act_dgrad, layout.byref(), _ptr(grad_preact), _ptr(weights), m, nz,
+            _DTYPE_CODE[grad_preact.dtype], _ptr(out))
+    return out
 
 
 def moe_renormalize_kept(layout: Layout, w: torch.Tensor, out=None):
@@ -703,7 +722,7 @@ __all__ = [
     "moe_dispatch_replay", "moe_combine", "moe_combine_backward", "moe_dispatch_backward",
     "moe_layout_read", "moe_dispatch_weighted", "moe_dispatch_weighted_backward",
     "moe_renormalize_kept", "moe_renormalize_kept_backward", "moe_expert_gemm", "moe_expert_gemm_wgrad", "moe_expert_gemm_dgrad",
-    "moe_expert_gemm_act", "moe_expert_act_backward", "ACTIVATIONS",
+    "moe_expert_gemm_act", "moe_expert_act_backward", "moe_expert_act_dgrad", "ACTIVATIONS",
     "moe_balance_loss", "moe_balance_loss_backward", "workspace_bytes", "Layout",
     "LayoutOptions", "MoeError", "lib", "EXPORTS",
 ]

@@ -35,11 +35,11 @@ import torch.utils.checkpoint
 from torch.autograd.function import once_differentiable
 
 from . import (FLAG_REPLAY_MISMATCH, Layout, moe_balance_loss, moe_balance_loss_backward, moe_combine,
-               moe_combine_backward, moe_dispatch, moe_dispatch_backward, moe_dispatch_layout, moe_dispatch_replay,
-               moe_dispatch_weighted, moe_dispatch_weighted_backward, moe_expert_act_backward,
-               moe_expert_gemm, moe_expert_gemm_act, moe_expert_gemm_dgrad, moe_expert_gemm_wgrad, moe_gate_topk,
-               moe_gate_topk_backward, moe_layout_read, moe_renormalize_kept,
-               moe_renormalize_kept_backward)
+               moe_combine_backward, moe_dispatch, moe_dispatch_backward, moe_dispatch_layout,
+               moe_dispatch_replay, moe_dispatch_weighted, moe_dispatch_weighted_backward,
+               moe_expert_act_backward, moe_expert_act_dgrad, moe_expert_gemm, moe_expert_gemm_act,
+               moe_expert_gemm_dgrad, moe_expert_gemm_wgrad, moe_gate_topk, moe_gate_topk_backward,
+               moe_layout_read, moe_renormalize_kept, moe_renormalize_kept_backward)
 
 
 class _Gate(torch.autograd.Function):
@@ -250,7 +250,7 @@ class _ExpertAct(torch.autograd.Function):
                 bias_dtype=ctx.bias_dtype if need_bias else None, need_w=need_w, need_residual=rows_res)
             g_z = gz if need_z else g_out
         if need_a:
-            g_a = moe_expert_gemm_dgrad(L, g_z, weights)
+            g_a = moe_expert_act_dgrad(L, g_z, weights)
             if ctx.gather:
                 g_a = moe_dispatch_backward(L, g_a)
         if need_weights:

@@ -605,6 +605,43 @@ moe_status_t moe_expert_gemm_act(const moe_layout_t* layout, const void* a, int3
                     "moe_expert_gemm_act");
 }
 
+moe_status_t moe_expert_act_dgrad(const moe_layout_t* layout, const void* grad_preact,
+                                  const void* weights, int32_t m, int32_t nz, moe_dtype_t dtype,
+                                  void* grad_a, void* stream) {
+  moe::LayoutView v;
+  MOE_TRY(view_of(layout, &v));
+  if (dtype != MOE_BF16 && dtype != MOE_F16)
+    return fail(MOE_ERR_UNSUPPORTED, "moe_expert_act_dgrad supports bf16 and f16 only (got dtype %d)",
+                static_cast<int>(dtype));
+  int64_t rc_in = 0, rc_out = 0;
+  MOE_TRY(check_rows(nz, dtype, &rc_in));
+  MOE_TRY(check_rows(m, dtype, &rc_out));
+  if (moe::expert_act_dgrad_grid(v, m) > INT32_MAX)
+    return fail(MOE_ERR_UNSUPPORTED, "rows x m too large for one input-gradient launch");
+  MOE_TRY(check_array(grad_preact, v.s > 0 ? v.rows : 0, "grad_preact", true));
+  MOE_TRY(check_array(weights, v.s > 0 ? v.e : 0, "weights", true));
+  MOE_TRY(check_array(grad_a, v.rows, "grad_a", true));
+  const size_t eb = elem_bytes(dtype);
+  if (overlap(grad_a, static_cast<size_t>(v.rows) * m * eb, grad_preact, static_cast<size_t>(v.rows) * nz * eb))
+    return fail(MOE_ERR_INVALID_ARG, "grad_preact and grad_a may not overlap");
+  moe::ExpertAct p{};
+  p.a = grad_preact;
+  p.w = weights;
+  p.out = grad_a;
+  p.dst = v.dst;
+  p.src = v.src;
+  p.kept = v.kept;
+  p.offsets = v.offsets;
+  p.e = v.e;
+  p.k = v.k;
+  p.m = nz;
+  p.n = p.nz = m;
+  p.act = MOE_ACT_NONE;
+  p.rows = v.rows;
+  return hip_status(moe::launch_expert_act_dgrad(v, p, static_cast<int>(dtype), static_cast<hipStream_t>(stream)),
+                    "moe_expert_act_dgrad");
+}
+
 size_t moe_expert_act_backward_workspace_bytes(const moe_layout_t* layout, int32_t n, int32_t gated) {
   const std::string saved = g_last_error;
   moe::LayoutView v;

@@ -33,7 +33,8 @@ constexpr int kBalBlock = 512;  // threads per workgroup of both directions
 constexpr int kBalWaves = kBalBlock / kWave;
 constexpr int kBalTiles = 512;  // most tiles: two workgroups per CU
 constexpr int kBalMinTile = 32;
-constexpr int kBalChunk = 128;  // experts per workgroup of the second launch
+constexpr int kBalChunk = 16;  // experts per workgroup of the second launch
+constexpr int kBalReduce = 256;  // its threads
 // Batches of up to this many logits are one tile, finished by the first launch alone.
 constexpr int64_t kBalSingle = 16384;
 
@@ -60,6 +61,7 @@ BalancePlan balance_plan(int32_t s, int32_t e, int32_t g) {
   p.off_z = take(static_cast<size_t>(p.slots) * 8);
   p.off_tokens = take(static_cast<size_t>(p.slots) * 4);
   p.off_dots = take(static_cast<size_t>(g) * p.chunks * 8);
+  p.off_arrived = take(static_cast<size_t>(g) * 4);
   p.bytes = at;
   return p;
 }
@@ -169,10 +171,15 @@ __device__ __forceinline__ void row_softmax(float (&v)[NV], float* inv, float* l
 
 // Sum over the workgroup, in lane and wave order; every thread gets it. `red` holds a
 // value per wave.
-template <class T>
-__device__ __forceinline__ T block_sum(T v, T* red) {
+__device__ __forceinline__ int wave_total(int v) {
 #pragma unroll
   for (int o = 1; o < kWave; o <<= 1) v += __shfl_xor(v, o, kWave);
+  return v;
+}
+__device__ __forceinline__ double wave_total(double v) { return wave_sum(v); }
+template <class T>
+__device__ __forceinline__ T block_sum(T v, T* red) {
+  v = wave_total(v);
   __syncthreads();
   if (lane_id() == 0) red[wave_in_block()] = v;
   __syncthreads();
@@ -195,13 +202,14 @@ struct BalancePartials {
   double* z;        // [slots]
   int32_t* tokens;  // [slots]
   double* dots;     // [g, chunks]
+  int32_t* arrived; // [g]
 };
 
 template <int LPT, int NV, bool VEC>
 __global__ __launch_bounds__(kBalBlock) void balance_tile_kernel(BalanceArgs a, int tile, int pitch, bool single,
                                                                  BalancePartials part, BalanceOut out) {
   constexpr int kGroups = kBalBlock / LPT;  // tokens in work at once
-  constexpr int U = NV >= 16 ? 2 : 4;       // rows loaded ahead of the softmax
+  constexpr int U = NV >= 16 ? 1 : 2;       // rows in work at once per lane group
   constexpr int kCols = LPT * NV;
   __shared__ float sums[kBalWaves][kCols];
   __shared__ int32_t hist[kCols];
@@ -212,6 +220,8 @@ __global__ __launch_bounds__(kBalBlock) void balance_tile_kernel(BalanceArgs a, 
   const int t0 = blockIdx.x * tile;
   const int t1 = a.s - t0 > tile ? t0 + tile : a.s;
 
+  if (!single)  // for the second launch
+    for (int i = blockIdx.x * kBalBlock + tid; i < a.g; i += gridDim.x * kBalBlock) part.arrived[i] = 0;
   int j = 0;
   if (a.groups != nullptr) {
     j = group_at(a.groups, a.g, t0);
@@ -226,33 +236,62 @@ __global__ __launch_bounds__(kBalBlock) void balance_tile_kernel(BalanceArgs a, 
       hi = last < t1 ? last : t1;
     }
     if (lo >= hi && !single) continue;  // uniform; a single tile finishes its group, empty or not
-    for (int c = tid; c < kCols; c += kBalBlock) hist[c] = 0;
 
-    float acc[NV];
+    // U rows per lane group at a time, the next ones loaded while these are worked on
+    float v[2][U][NV], acc[NV];
+    bool live[2][U];
+    auto load = [&](int tb, int b) __attribute__((always_inline)) {
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int t = tb + u * kGroups + gid;
+        live[b][u] = t < hi && (a.mask == nullptr || a.mask[t] != 0);
+        load_row<LPT, NV, VEC>(a.logits + static_cast<size_t>(t < hi ? t : lo) * a.e, a.e, r, live[b][u], v[b][u]);
+      }
+    };
+    if (lo < hi) load(lo, 0);
+
+    // the routes meanwhile: a lane per route, 64 / k tokens to a wave; valid ones are counted,
+    // one naming no expert, or the expert of an earlier route of its token, is not
+    for (int c = tid; c < kCols; c += kBalBlock) hist[c] = 0;
+    __syncthreads();
+    const int tokens = kWave / a.k, jj = lane % a.k;
+    for (int tb = lo + wv * tokens; tb < hi; tb += kBalWaves * tokens) {  // uniform per wave
+      const int t = tb + lane / a.k;
+      const bool mine = lane < tokens * a.k && t < hi && (a.mask == nullptr || a.mask[t] != 0);
+      const int x = mine ? a.idx[static_cast<size_t>(t) * a.k + jj] : -1;
+      bool ok = x >= 0 && x < a.e;
+      for (int d = 1; d < a.k; ++d) {
+        const int y = __shfl_up(x, d, kWave);
+        ok = ok && !(d <= jj && y == x);
+      }
+      if (ok) atomicAdd(&hist[x], 1);
+    }
+
 #pragma unroll
     for (int i = 0; i < NV; ++i) acc[i] = 0.0f;
     double zacc = 0.0;
     int count = 0;
-    for (int tb = lo; tb < hi; tb += U * kGroups) {  // the same trips for every lane
-      float v[U][NV];
-      bool live[U];
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int t = tb + u * kGroups + gid;
-        live[u] = t < hi && (a.mask == nullptr || a.mask[t] != 0);
-        load_row<LPT, NV, VEC>(a.logits + static_cast<size_t>(t < hi ? t : lo) * a.e, a.e, r, live[u], v[u]);
-      }
+    auto work = [&](int b) __attribute__((always_inline)) {
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         float inv, lse;
-        row_softmax<LPT, NV>(v[u], &inv, &lse);  // a row that is not live is all -inf: adds nothing
+        row_softmax<LPT, NV>(v[b][u], &inv, &lse);  // a row that is not live is all -inf: adds nothing
 #pragma unroll
-        for (int i = 0; i < NV; ++i) acc[i] += v[u][i] * inv;
+        for (int i = 0; i < NV; ++i) acc[i] = __builtin_fmaf(v[b][u][i], inv, acc[i]);
         if (r == 0) {
           zacc += static_cast<double>(lse) * static_cast<double>(lse);
-          count += live[u];
+          count += live[b][u];
         }
       }
+    };
+    constexpr int kStep = U * kGroups;
+    for (int tb = lo; tb < hi; tb += 2 * kStep) {  // the same trips for every lane
+      const bool more = hi - tb > kStep;           // no overflow: tb < hi
+      if (more) load(tb + kStep, 1);
+      work(0);
+      if (!more) break;
+      if (hi - tb > 2 * kStep) load(tb + 2 * kStep, 0);
+      work(1);
     }
     // the wave's token groups add up column by column, then the waves in order through LDS
 #pragma unroll
@@ -263,19 +302,6 @@ __global__ __launch_bounds__(kBalBlock) void balance_tile_kernel(BalanceArgs a, 
     }
     const double zsum = block_sum(zacc, red_z);  // its barriers also order sums and hist
     const int nsum = block_sum(count, red_n);
-    // the routes: valid ones are counted, a route naming no expert or one that an earlier
-    // route of its token named is not
-    for (int q = tid; q < (hi - lo) * a.k; q += kBalBlock) {
-      const int t = lo + q / a.k, jj = q % a.k;
-      if (a.mask != nullptr && a.mask[t] == 0) continue;
-      const int32_t* route = a.idx + static_cast<size_t>(t) * a.k;
-      const int x = route[jj];
-      bool ok = x >= 0 && x < a.e;
-      for (int p = 0; p < jj; ++p) ok = ok && route[p] != x;
-      if (ok) atomicAdd(&hist[x], 1);
-    }
-    __syncthreads();
-
     if (!single) {
       const size_t slot = static_cast<size_t>(blockIdx.x) + j;
       for (int c = tid; c < pitch; c += kBalBlock) {
@@ -311,15 +337,18 @@ __global__ __launch_bounds__(kBalBlock) void balance_tile_kernel(BalanceArgs a, 
 }
 
 // Forward, second launch: workgroup (chunk, group) adds the group's partial rows over
-// kBalChunk experts: 32 lanes of four experts by 16 rows at a time, in float64, then the
-// 16 in order. With more than one chunk the chunks' shares of the loss meet in a third.
-__global__ __launch_bounds__(kBalBlock) void balance_reduce_kernel(BalanceArgs a, int tile, int ntiles, int pitch,
-                                                                   int chunks, BalancePartials part, BalanceOut out) {
-  constexpr int kRows = kBalBlock / 32;
+// kBalChunk experts: 4 lanes of four experts by 64 rows at a time, in float64, then the 64 in
+// order. One workgroup alone draws the partial rows, which other XCDs wrote, at some 40 GB/s:
+// 512 rows of 128 experts in one workgroup took 15 us, in eight they take 5. The chunks'
+// shares of the loss go to the group's last workgroup to arrive (counted on `arrived`, which
+// the first launch clears), which adds them in chunk order.
+__global__ __launch_bounds__(kBalReduce) void balance_reduce_kernel(BalanceArgs a, int tile, int pitch, int chunks,
+                                                                    BalancePartials part, BalanceOut out) {
+  constexpr int kRows = kBalReduce / 4;
   __shared__ double psum[kRows][kBalChunk];
   __shared__ int32_t csum[kRows][kBalChunk];
-  __shared__ double red_z[kBalWaves];
-  __shared__ int32_t red_n[kBalWaves];
+  __shared__ double red_z[kBalReduce / kWave];
+  __shared__ int32_t red_n[kBalReduce / kWave];
   const int tid = threadIdx.x, chunk = blockIdx.x % chunks, j = blockIdx.x / chunks;
   int lo = 0, hi = a.s;
   if (a.groups != nullptr) {
@@ -329,21 +358,11 @@ __global__ __launch_bounds__(kBalBlock) void balance_reduce_kernel(BalanceArgs a
   const int64_t s0 = lo < hi ? lo / tile + static_cast<int64_t>(j) : 0;
   const int ns = lo < hi ? (hi - 1) / tile - lo / tile + 1 : 0;
 
-  int count = 0;
-  double zacc = 0.0;
-  for (int i = tid; i < ns; i += kBalBlock) {
-    count += part.tokens[s0 + i];
-    zacc += part.z[s0 + i];
-  }
-  const int nsum = block_sum(count, red_n);
-  const double zsum = block_sum(zacc, red_z);
-  const double n = nsum > 0 ? static_cast<double>(nsum) : 1.0;
-
-  const int c4 = chunk * kBalChunk + 4 * (tid % 32), row = tid / 32;
+  const int c4 = chunk * kBalChunk + 4 * (tid % 4), row = tid / 4;
   double p[4] = {0.0, 0.0, 0.0, 0.0};
   int32_t q[4] = {0, 0, 0, 0};
   if (c4 < pitch) {
-#pragma unroll 8
+#pragma unroll 4
     for (int i = row; i < ns; i += kRows) {
       const size_t at = static_cast<size_t>(s0 + i) * pitch + c4;
       const chunk_t v = *reinterpret_cast<const chunk_t*>(part.probs + at);
@@ -355,17 +374,27 @@ __global__ __launch_bounds__(kBalBlock) void balance_reduce_kernel(BalanceArgs a
       }
     }
   }
+  int count = 0;
+  double zacc = 0.0;
+  for (int i = tid; i < ns; i += kBalReduce) {
+    count += part.tokens[s0 + i];
+    zacc += part.z[s0 + i];
+  }
 #pragma unroll
   for (int u = 0; u < 4; ++u) {
-    psum[row][4 * (tid % 32) + u] = p[u];
-    csum[row][4 * (tid % 32) + u] = q[u];
+    psum[row][4 * (tid % 4) + u] = p[u];
+    csum[row][4 * (tid % 4) + u] = q[u];
   }
-  __syncthreads();
+  const int nsum = block_sum(count, red_n);  // its barriers also order psum and csum
+  const double zsum = block_sum(zacc, red_z);
+  const double n = nsum > 0 ? static_cast<double>(nsum) : 1.0;
+
   double dot = 0.0;
   const int c = chunk * kBalChunk + tid;
   if (tid < kBalChunk && c < a.e) {
     double sum = 0.0;
     int32_t cnt = 0;
+#pragma unroll 8
     for (int w = 0; w < kRows; ++w) {
       sum += psum[w][tid];
       cnt += csum[w][tid];
@@ -375,26 +404,29 @@ __global__ __launch_bounds__(kBalBlock) void balance_reduce_kernel(BalanceArgs a
     out.counts[static_cast<size_t>(j) * a.e + c] = cnt;
     dot = static_cast<double>(cnt) * sum;
   }
-  dot = block_sum(dot, red_z);
-  if (tid == 0) {
-    if (chunk == 0) {
-      out.tokens[j] = nsum;
-      out.z[j] = static_cast<float>(zsum / n);
-    }
-    if (chunks == 1) out.loss[j] = static_cast<float>(dot * a.e / (static_cast<double>(a.k) * n));
-    else part.dots[static_cast<size_t>(j) * chunks + chunk] = dot;
+  if (tid >= kWave) return;  // the first wave holds every share
+  dot = wave_sum(dot);
+  if (chunk == 0 && tid == 0) {
+    out.tokens[j] = nsum;
+    out.z[j] = static_cast<float>(zsum / n);
   }
-}
-
-__global__ __launch_bounds__(kBlock) void balance_finish_kernel(BalanceArgs a, int chunks, const double* __restrict__ dots,
-                                                                const int32_t* __restrict__ tokens,
-                                                                float* __restrict__ loss) {
-  const int j = blockIdx.x * kBlock + threadIdx.x;
-  if (j >= a.g) return;
-  double dot = 0.0;
-  for (int c = 0; c < chunks; ++c) dot += dots[static_cast<size_t>(j) * chunks + c];
-  const double n = tokens[j] > 0 ? static_cast<double>(tokens[j]) : 1.0;
-  loss[j] = static_cast<float>(dot * a.e / (static_cast<double>(a.k) * n));
+  const double scale = a.e / (static_cast<double>(a.k) * n);
+  if (chunks == 1) {
+    if (tid == 0) out.loss[j] = static_cast<float>(dot * scale);
+    return;
+  }
+  double* dots = part.dots + static_cast<size_t>(j) * chunks;
+  int before = 0;
+  if (tid == 0) {
+    __hip_atomic_store(dots + chunk, dot, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    before = __hip_atomic_fetch_add(part.arrived + j, 1, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT);
+  }
+  if (__builtin_amdgcn_readfirstlane(before) != chunks - 1) return;
+  // at most 1024 / kBalChunk = 64 chunks: one per lane, added in a fixed order
+  static_assert(1024 / kBalChunk <= kWave, "one lane per chunk");
+  const double mine = tid < chunks ? __hip_atomic_load(dots + tid, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) : 0.0;
+  const double total = wave_sum(mine);
+  if (tid == 0) out.loss[j] = static_cast<float>(total * scale);
 }
 
 // ---------------------------------------------------------------------------------
@@ -406,7 +438,7 @@ __global__ __launch_bounds__(kBalBlock) void balance_backward_kernel(
     BalanceArgs a, int tile, const int32_t* __restrict__ counts, const int32_t* __restrict__ tokens,
     const float* __restrict__ grad_loss, const float* __restrict__ grad_z, float* __restrict__ grad) {
   constexpr int kGroups = kBalBlock / LPT;
-  constexpr int U = NV >= 16 ? 2 : 4;
+  constexpr int U = NV >= 16 ? 1 : 2;
   const int tid = threadIdx.x;
   const int r = tid % LPT, gid = tid / LPT;
   const int t0 = blockIdx.x * tile;
@@ -507,7 +539,8 @@ hipError_t launch_balance_loss(const BalanceArgs& a, const BalancePlan& p, char*
   const BalanceOut out{counts, tokens, probs, loss, z};
   const BalancePartials part{reinterpret_cast<float*>(ws + p.off_probs), reinterpret_cast<int32_t*>(ws + p.off_counts),
                              reinterpret_cast<double*>(ws + p.off_z), reinterpret_cast<int32_t*>(ws + p.off_tokens),
-                             reinterpret_cast<double*>(ws + p.off_dots)};
+                             reinterpret_cast<double*>(ws + p.off_dots),
+                             reinterpret_cast<int32_t*>(ws + p.off_arrived)};
   // groups given by offsets may leave tokens out, so only a whole batch is finished at once
   const bool single = p.ntiles == 1 && a.g == 1 && a.groups == nullptr;
   with_rows(a.e, rows16(a.logits, a.e), [&](auto shape, auto vec) {
@@ -517,11 +550,8 @@ hipError_t launch_balance_loss(const BalanceArgs& a, const BalancePlan& p, char*
   });
   hipError_t err = hipGetLastError();
   if (err != hipSuccess || single) return err;
-  balance_reduce_kernel<<<static_cast<unsigned>(a.g) * p.chunks, kBalBlock, 0, stream>>>(a, p.tile, p.ntiles, p.pitch,
-                                                                                       p.chunks, part, out);
-  err = hipGetLastError();
-  if (err != hipSuccess || p.chunks == 1) return err;
-  balance_finish_kernel<<<(a.g + kBlock - 1) / kBlock, kBlock, 0, stream>>>(a, p.chunks, part.dots, tokens, loss);
+  balance_reduce_kernel<<<static_cast<unsigned>(a.g) * p.chunks, kBalReduce, 0, stream>>>(a, p.tile, p.pitch, p.chunks,
+                                                                                        part, out);
   return hipGetLastError();
 }
 
@@ -531,7 +561,7 @@ hipError_t launch_balance_loss_backward(const BalanceArgs& a, const int32_t* cou
   if (a.s == 0) return hipSuccess;
   with_rows(a.e, rows16(a.logits, a.e) && rows16(grad_logits, a.e), [&](auto shape, auto vec) {
     using S = decltype(shape);
-    constexpr int kAtOnce = kBalBlock / S::lpt * (S::nv >= 16 ? 2 : 4);
+    constexpr int kAtOnce = kBalBlock / S::lpt * (S::nv >= 16 ? 1 : 2);
     // whole rounds of tokens, up to 2048 workgroups
     int tile = (a.s + 2047) / 2048;
     tile = (tile + kAtOnce - 1) / kAtOnce * kAtOnce;

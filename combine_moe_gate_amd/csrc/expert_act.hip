@@ -64,24 +64,53 @@ constexpr int kSlabPitch = 64 * 4 + 16;            // bytes per row of a wave's 
 constexpr int kActLds = 2 * kActStage + kActBM * 8;
 static_assert(8 * 2 * 16 * kSlabPitch <= 2 * kActStage, "the slabs reuse the stages");
 
+// The most units of a tile: with [K][N] weights nine would not fit the registers.
+template <bool KN>
+constexpr int act_units = KN ? kActUnits - 1 : kActUnits;
+
 // Row-blocks of a segment of `rows` rows: as few as hold it, of nearly equal height.
+template <bool KN>
 __device__ __forceinline__ int act_blocks(int rows) {
   const int units = (rows + 31) / 32;
-  return (units + kActUnits - 1) / kActUnits;
+  return (units + act_units<KN> - 1) / act_units<KN>;
 }
 
 struct ActTile {
   int expert, unit0, units, cb, rows, offset;  // expert (-1: none), first 32-row unit, units, column-block
 };
 
+template <bool KN>
 __device__ __forceinline__ ActTile act_tile(int b, int e, const int32_t* __restrict__ kept,
                                             const int32_t* __restrict__ offsets, int col_blocks) {
-  const SegmentTile s = segment_tile(b, e, kept, offsets, col_blocks, kActBand, [](int r) { return act_blocks(r); });
+  const SegmentTile s = segment_tile(b, e, kept, offsets, col_blocks, kActBand, [](int r) { return act_blocks<KN>(r); });
   if (s.expert < 0) return ActTile{-1, 0, 0, 0, 0, 0};
   const int units = (s.rows + 31) / 32;
   const int base = units / s.blocks, extra = units % s.blocks;  // the first `extra` blocks are a unit taller
   return ActTile{s.expert, s.rb * base + (s.rb < extra ? s.rb : extra), base + (s.rb < extra), s.cb, s.rows,
                  s.offset};
+}
+
+// Four weight fragments of a [K][N] stage: for tile j two transposing reads at at[j] and 4 K
+// rows (2048 bytes) on. They are written out with their wait because the compiler lets no
+// transposing read it knows start while direct-to-LDS loads are in flight, and those are in
+// flight nearly always.
+__device__ __forceinline__ void read_tr16(const uint32_t (&at)[4], chunk_t (&b)[4]) {
+  uint2 lo[4], hi[4];
+  asm volatile(
+      "ds_read_b64_tr_b16 %0, %8\n\t"
+      "ds_read_b64_tr_b16 %4, %8 offset:2048\n\t"
+      "ds_read_b64_tr_b16 %1, %9\n\t"
+      "ds_read_b64_tr_b16 %5, %9 offset:2048\n\t"
+      "ds_read_b64_tr_b16 %2, %10\n\t"
+      "ds_read_b64_tr_b16 %6, %10 offset:2048\n\t"
+      "ds_read_b64_tr_b16 %3, %11\n\t"
+      "ds_read_b64_tr_b16 %7, %11 offset:2048\n\t"
+      "s_waitcnt lgkmcnt(0)"
+      : "=&v"(lo[0]), "=&v"(lo[1]), "=&v"(lo[2]), "=&v"(lo[3]), "=&v"(hi[0]), "=&v"(hi[1]), "=&v"(hi[2]), "=&v"(hi[3])
+      : "v"(at[0]), "v"(at[1]), "v"(at[2]), "v"(at[3])
+      : "memory");
+#pragma unroll
+  for (int j = 0; j < 4; ++j) b[j] = chunk_t{lo[j].x, lo[j].y, hi[j].x, hi[j].y};
 }
 
 // f(0), f(1), ... with compile-time arguments.
@@ -90,8 +119,9 @@ __device__ __forceinline__ void static_for(std::integer_sequence<int, I...>, F f
   (f(std::integral_constant<int, I>{}), ...);
 }
 
-// The tile's products and its epilogue, for a height of 32 FM rows.
-template <int DT, int FM>
+// The tile's products and its epilogue, for a height of 32 FM rows. KN: weights stored
+// [K][N] per expert (the input gradient).
+template <int DT, bool KN, int FM>
 __device__ __forceinline__ void act_tile_body(const ExpertAct& p, const ActTile& tc, char* lds) {
   constexpr int FN = 4;
   // A K step's products in order: (k32 half, row tile), 2 FM slots of FN MFMAs, cut into
@@ -115,17 +145,28 @@ __device__ __forceinline__ void act_tile_body(const ExpertAct& p, const ActTile&
   const chunk_t* a_row[kALoads];
   const chunk_t* b_row[4];
   const chunk_t* wx = static_cast<const chunk_t*>(p.w) + static_cast<size_t>(x) * p.nz * kchunks;
+  const int nchunks = p.n / 8;
+  // [K][N]: lane l of a load fills slot l % 32 of staged K row 2 (load) + l / 32 with chunk
+  // slot ^ kn_swizzle(row); columns past the last repeat its chunk. A wave's loads are 16 rows
+  // apart, which changes neither the swizzle nor the chunk: b_row[0] serves them all.
+  auto kn_swizzle = [](int row) { return 4 * (row % 4) + 2 * ((row >> 3) & 1); };
+  auto kn_row = [&](int q) { return (q * 8 + wv) * 2 + lane / 32; };
+  if constexpr (KN) {
+    const int c = col0 / 8 + ((lane % 32) ^ kn_swizzle(kn_row(0)));
+    b_row[0] = wx + static_cast<size_t>(kn_row(0)) * nchunks + (c < nchunks ? c : nchunks - 1);
+  } else {
 #pragma unroll
-  for (int q = 0; q < 4; ++q) {
-    const int r = (q * 8 + wv) * 8 + lane / 8;
-    int j;
-    if (p.gated) {  // 32 gate rows, then the 32 up rows of the same features
-      const int f = col0 + (r / 64) * 32 + r % 32;
-      j = (f < p.n ? f : p.n - 1) + (r % 64 >= 32 ? p.n : 0);
-    } else {
-      j = col0 + r < p.n ? col0 + r : p.n - 1;
+    for (int q = 0; q < 4; ++q) {
+      const int r = (q * 8 + wv) * 8 + lane / 8;
+      int j;
+      if (p.gated) {  // 32 gate rows, then the 32 up rows of the same features
+        const int f = col0 + (r / 64) * 32 + r % 32;
+        j = (f < p.n ? f : p.n - 1) + (r % 64 >= 32 ? p.n : 0);
+      } else {
+        j = col0 + r < p.n ? col0 + r : p.n - 1;
+      }
+      b_row[q] = wx + static_cast<size_t>(j) * kchunks;
     }
-    b_row[q] = wx + static_cast<size_t>(j) * kchunks;
   }
   // slot lane % 8 of staged row R takes chunk slot ^ (R / 2 % 8); the loads' first rows are
   // multiples of 8, so R / 2 % 8 = 4 (load % 2) + lane / 16
@@ -137,11 +178,25 @@ __device__ __forceinline__ void act_tile_body(const ExpertAct& p, const ActTile&
   };
   auto issue_b = [&](int kt) {
     char* st = lds + (kt % 2) * kActStage + kActAStage;
-    const int at = chunk_at(kt);
+    if constexpr (KN) {
+      const int64_t step = static_cast<int64_t>(kt) * 64 * nchunks;
 #pragma unroll
-    for (int q = 0; q < 4; ++q)
-      __builtin_amdgcn_global_load_lds(static_cast<const void*>(b_row[q] + at),
-                                       (lds_void_t*)(st + (q * 8 + wv) * 1024), 16, 0, 0);
+      for (int q = 0; q < 4; ++q) {
+        int64_t at = step + q * 16 * static_cast<int64_t>(nchunks);
+        if ((kt + 1) * 64 > p.m) {  // uniform: K rows past the end load the last one, cleared once landed
+          const int over = kt * 64 + kn_row(0) + 16 * q - (p.m - 1);
+          if (over > 0) at -= static_cast<int64_t>(over) * nchunks;
+        }
+        __builtin_amdgcn_global_load_lds(static_cast<const void*>(b_row[0] + at),
+                                         (lds_void_t*)(st + (q * 8 + wv) * 1024), 16, 0, 0);
+      }
+    } else {
+      const int at = chunk_at(kt);
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        __builtin_amdgcn_global_load_lds(static_cast<const void*>(b_row[q] + at),
+                                         (lds_void_t*)(st + (q * 8 + wv) * 1024), 16, 0, 0);
+    }
   };
   // the weights' first loads start before the rows' addresses are read from the layout
   issue_b(0);
@@ -175,14 +230,16 @@ __device__ __forceinline__ void act_tile_body(const ExpertAct& p, const ActTile&
   }
 
   auto clear_tail = [&](int kt) {
-    if (kt * 8 + chunk < kchunks) return;
     char* st = lds + (kt % 2) * kActStage;
     const chunk_t z = {0u, 0u, 0u, 0u};
+    const bool past = kt * 8 + chunk >= kchunks;
 #pragma unroll
-    for (int q = 0; q < 4; ++q) *reinterpret_cast<chunk_t*>(st + kActAStage + (q * 8 + wv) * 1024 + lane * 16) = z;
+    for (int q = 0; q < 4; ++q)
+      if (KN ? kt * 64 + kn_row(0) + 16 * q >= p.m : past)
+        *reinterpret_cast<chunk_t*>(st + kActAStage + (q * 8 + wv) * 1024 + lane * 16) = z;
 #pragma unroll
     for (int q = 0; q < kALoads; ++q)
-      if (q * 8 + wv < 4 * FM) *reinterpret_cast<chunk_t*>(st + (q * 8 + wv) * 1024 + lane * 16) = z;
+      if (q * 8 + wv < 4 * FM && past) *reinterpret_cast<chunk_t*>(st + (q * 8 + wv) * 1024 + lane * 16) = z;
   };
 
   f32x4_t acc[FM][FN];
@@ -206,7 +263,22 @@ __device__ __forceinline__ void act_tile_body(const ExpertAct& p, const ActTile&
                                                  (((4 * (slot / FM) + (lane >> 4)) ^ frag_swz) << 4));
     }
   };
+  // [K][N]: gfx950's transposing LDS read hands lane i of each 16-lane group column i of the
+  // four K rows its lanes point at, lane i at row i / 4, columns 4 (i % 4) .. + 3; two reads
+  // make the lane's eight K rows. The swizzle puts the 32 lanes served together on 32
+  // different 8-byte pieces of the 256-byte bank row.
+  const uint32_t lds_at = static_cast<uint32_t>(reinterpret_cast<uintptr_t>((lds_void_t*)lds));
+  const int kn_at = (8 * (lane >> 4) + ((lane & 15) >> 2)) * 512 + (lane & 1) * 8;
+  const int kn_slot = (8 * wn + ((lane & 3) >> 1)) ^ kn_swizzle(8 * (lane >> 4) + ((lane & 15) >> 2));
   auto read_b = [&](int kt, int half, chunk_t (&b)[FN]) {
+    if constexpr (KN) {
+      const uint32_t st = lds_at + (kt % 2) * kActStage + kActAStage + half * 32 * 512 + kn_at;
+      uint32_t at[4];
+#pragma unroll
+      for (int j = 0; j < FN; ++j) at[j] = st + ((kn_slot ^ (2 * j)) << 4);
+      read_tr16(at, b);
+      return;
+    }
 #pragma unroll
     for (int j = 0; j < FN; ++j)
       b[j] = *reinterpret_cast<const chunk_t*>(lds + (kt % 2) * kActStage + b_base + j * 16 * kActRowBytes +
@@ -317,7 +389,7 @@ __device__ __forceinline__ void act_tile_body(const ExpertAct& p, const ActTile&
   }
 }
 
-template <int DT>
+template <int DT, bool KN>
 __global__ __launch_bounds__(kActThreads) __attribute__((amdgpu_waves_per_eu(2, 2))) void expert_act_kernel(
     ExpertAct p, int col_blocks, int tile_grid) {
   extern __shared__ __attribute__((aligned(1024))) char lds[];
@@ -325,18 +397,20 @@ __global__ __launch_bounds__(kActThreads) __attribute__((amdgpu_waves_per_eu(2, 
     zero_unfilled(p, blockIdx.x - tile_grid, gridDim.x - tile_grid);
     return;
   }
-  const ActTile tc = act_tile(blockIdx.x, p.e, p.kept, p.offsets, col_blocks);
+  const ActTile tc = act_tile<KN>(blockIdx.x, p.e, p.kept, p.offsets, col_blocks);
   if (tc.expert < 0) return;
   switch (tc.units) {
-    case 1: act_tile_body<DT, 1>(p, tc, lds); break;
-    case 2: act_tile_body<DT, 2>(p, tc, lds); break;
-    case 3: act_tile_body<DT, 3>(p, tc, lds); break;
-    case 4: act_tile_body<DT, 4>(p, tc, lds); break;
-    case 5: act_tile_body<DT, 5>(p, tc, lds); break;
-    case 6: act_tile_body<DT, 6>(p, tc, lds); break;
-    case 7: act_tile_body<DT, 7>(p, tc, lds); break;
-    case 8: act_tile_body<DT, 8>(p, tc, lds); break;
-    default: act_tile_body<DT, 9>(p, tc, lds); break;
+    case 1: act_tile_body<DT, KN, 1>(p, tc, lds); break;
+    case 2: act_tile_body<DT, KN, 2>(p, tc, lds); break;
+    case 3: act_tile_body<DT, KN, 3>(p, tc, lds); break;
+    case 4: act_tile_body<DT, KN, 4>(p, tc, lds); break;
+    case 5: act_tile_body<DT, KN, 5>(p, tc, lds); break;
+    case 6: act_tile_body<DT, KN, 6>(p, tc, lds); break;
+    case 7: act_tile_body<DT, KN, 7>(p, tc, lds); break;
+    case 8: act_tile_body<DT, KN, 8>(p, tc, lds); break;
+    default:
+      if constexpr (!KN) act_tile_body<DT, KN, 9>(p, tc, lds);
+      break;
   }
 }
 
@@ -506,18 +580,19 @@ static int64_t row_tiles(const LayoutView& L, int height) {
   return routes / height + with_rows;
 }
 
-// How a launch is shaped: F (above) and the weight rows per workgroup.
+// How a launch is shaped: F (above; `kn`: the large tiles in any case) and the weight rows
+// per workgroup.
 struct ActShape {
   int few, cols;
   int64_t col_blocks, tiles;
 };
-static ActShape act_shape(const LayoutView& L, int n, bool gated) {
-  ActShape a{L.s == 0 ? 1 : few_rows(L), kActBN, 0, 0};
+static ActShape act_shape(const LayoutView& L, int n, bool gated, bool kn) {
+  ActShape a{kn ? 0 : L.s == 0 ? 1 : few_rows(L), kActBN, 0, 0};
   const int per = gated ? 2 : 1;
   auto fit = [&](int cols) {
     a.cols = cols;
     a.col_blocks = (static_cast<int64_t>(n) * per + cols - 1) / cols;
-    a.tiles = L.s == 0 ? 0 : row_tiles(L, a.few ? 16 * a.few : kActBM) * a.col_blocks;
+    a.tiles = L.s == 0 ? 0 : row_tiles(L, a.few ? 16 * a.few : kn ? 32 * act_units<true> : kActBM) * a.col_blocks;
   };
   fit(a.few ? 64 : kActBN);
   // half as wide where that leaves fewer than four workgroups per CU
@@ -526,7 +601,11 @@ static ActShape act_shape(const LayoutView& L, int n, bool gated) {
 }
 
 int64_t expert_act_grid(const LayoutView& L, int n, bool gated) {
-  return (act_shape(L, n, gated).tiles + kXcds - 1) / kXcds * kXcds + kZeroBlocks;
+  return (act_shape(L, n, gated, false).tiles + kXcds - 1) / kXcds * kXcds + kZeroBlocks;
+}
+
+int64_t expert_act_dgrad_grid(const LayoutView& L, int m) {
+  return (act_shape(L, m, false, true).tiles + kXcds - 1) / kXcds * kXcds + kZeroBlocks;
 }
 
 // Dynamic LDS above the 64 KiB default needs the kernel's limit raised, once per device.
@@ -554,17 +633,11 @@ static hipError_t launch_few(const ExpertAct& p, int col_blocks, int64_t grid, h
   return hipGetLastError();
 }
 
-template <int DT>
-static hipError_t launch_dt(const LayoutView& L, const ExpertAct& p, hipStream_t stream) {
-  const ActShape a = act_shape(L, p.n, p.gated);
-  const int64_t grid = expert_act_grid(L, p.n, p.gated);
-  const int col_blocks = static_cast<int>(a.col_blocks);
-  if (a.few == 1 && a.cols == 32) return launch_few<DT, 1, 2>(p, col_blocks, grid, stream);
-  if (a.few == 1) return launch_few<DT, 1, 4>(p, col_blocks, grid, stream);
-  if (a.few == 2) return launch_few<DT, 2, 4>(p, col_blocks, grid, stream);
-  if (a.few == 4) return launch_few<DT, 4, 4>(p, col_blocks, grid, stream);
+// `few` and the tiles' width as act_shape() gave them.
+template <int DT, bool KN>
+static hipError_t launch_tiles(const ExpertAct& p, int col_blocks, int64_t grid, hipStream_t stream) {
   static std::atomic<uint64_t> done{0};
-  auto kern = expert_act_kernel<DT>;
+  auto kern = expert_act_kernel<DT, KN>;
   const hipError_t err = allow_lds(reinterpret_cast<const void*>(kern), kActLds, done);
   if (err != hipSuccess) return err;
   kern<<<static_cast<unsigned>(grid), kActThreads, kActLds, stream>>>(p, col_blocks,
@@ -572,9 +645,29 @@ static hipError_t launch_dt(const LayoutView& L, const ExpertAct& p, hipStream_t
   return hipGetLastError();
 }
 
+template <int DT>
+static hipError_t launch_dt(const LayoutView& L, const ExpertAct& p, hipStream_t stream) {
+  const ActShape a = act_shape(L, p.n, p.gated, false);
+  const int64_t grid = expert_act_grid(L, p.n, p.gated);
+  const int col_blocks = static_cast<int>(a.col_blocks);
+  if (a.few == 1 && a.cols == 32) return launch_few<DT, 1, 2>(p, col_blocks, grid, stream);
+  if (a.few == 1) return launch_few<DT, 1, 4>(p, col_blocks, grid, stream);
+  if (a.few == 2) return launch_few<DT, 2, 4>(p, col_blocks, grid, stream);
+  if (a.few == 4) return launch_few<DT, 4, 4>(p, col_blocks, grid, stream);
+  return launch_tiles<DT, false>(p, col_blocks, grid, stream);
+}
+
 hipError_t launch_expert_act(const LayoutView& L, const ExpertAct& p, int dtype, hipStream_t stream) {
   if (p.rows == 0) return hipSuccess;
   return dtype == kBF16 ? launch_dt<kBF16>(L, p, stream) : launch_dt<kF16>(L, p, stream);
+}
+
+hipError_t launch_expert_act_dgrad(const LayoutView& L, const ExpertAct& p, int dtype, hipStream_t stream) {
+  if (p.rows == 0) return hipSuccess;
+  const int64_t grid = expert_act_dgrad_grid(L, p.n);
+  const int col_blocks = static_cast<int>(act_shape(L, p.n, false, true).col_blocks);
+  return dtype == kBF16 ? launch_tiles<kBF16, true>(p, col_blocks, grid, stream)
+                        : launch_tiles<kF16, true>(p, col_blocks, grid, stream);
 }
 
 }  // namespace moe

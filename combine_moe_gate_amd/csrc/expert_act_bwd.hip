@@ -98,7 +98,6 @@ __global__ __launch_bounds__(kBwdThreads) void expert_act_backward_kernel(Expert
         if (p.dst[static_cast<size_t>(t) * p.k + j] == r) w = p.route_w[static_cast<size_t>(t) * p.k + j];
       row_w[tid] = w;
     }
-    __syncthreads();
   }
 
   float acc[H][8];
@@ -108,19 +107,23 @@ __global__ __launch_bounds__(kBwdThreads) void expert_act_backward_kernel(Expert
     for (int q = 0; q < 8; ++q) acc[h][q] = 0.0f;
   const uint16_t* gout = static_cast<const uint16_t*>(p.grad_out) + c;
   const uint16_t* zin = static_cast<const uint16_t*>(p.preact) + c;
-  for (int i = wv; i < nrows; i += kBwdWaves) {  // uniform per wave
-    const int r = row0 + i;
+  // kDepth rows of a wave in flight: each is loaded that many rows before it is worked on
+  constexpr int kDepth = 4;
+  chunk_t gv[kDepth], zv[kDepth][H];
+  auto load = [&](int i, int b) __attribute__((always_inline)) {
     const chunk_t none = {0u, 0u, 0u, 0u};
-    const chunk_t gv = in ? *reinterpret_cast<const chunk_t*>(gout + static_cast<size_t>(r) * p.n) : none;
-    chunk_t zv[H];
+    const size_t r = static_cast<size_t>(row0 + i);
+    gv[b] = in ? *reinterpret_cast<const chunk_t*>(gout + r * p.n) : none;
 #pragma unroll
     for (int h = 0; h < H; ++h)
-      zv[h] = in && p.preact != nullptr
-                  ? *reinterpret_cast<const chunk_t*>(zin + static_cast<size_t>(r) * p.nz + h * p.n) : none;
+      zv[b][h] = in && p.preact != nullptr ? *reinterpret_cast<const chunk_t*>(zin + r * p.nz + h * p.n) : none;
+  };
+  auto work = [&](int i, int b) __attribute__((always_inline)) {
+    const int r = row0 + i;
     float g[8], z[H][8], d[H][8];
-    unpack<DT>(gv, g);
+    unpack<DT>(gv[b], g);
 #pragma unroll
-    for (int h = 0; h < H; ++h) unpack<DT>(zv[h], z[h]);
+    for (int h = 0; h < H; ++h) unpack<DT>(zv[b][h], z[h]);
     const float w = p.route_w != nullptr ? row_w[i] : 1.0f;
     float dot = 0.0f;
 #pragma unroll
@@ -147,11 +150,22 @@ __global__ __launch_bounds__(kBwdThreads) void expert_act_backward_kernel(Expert
               pack<DT>(d[h]);
       }
       if (p.grad_residual != nullptr)
-        *reinterpret_cast<chunk_t*>(static_cast<uint16_t*>(p.grad_residual) + static_cast<size_t>(r) * p.n + c) = gv;
+        *reinterpret_cast<chunk_t*>(static_cast<uint16_t*>(p.grad_residual) + static_cast<size_t>(r) * p.n + c) = gv[b];
     }
     if (p.grad_w != nullptr) {  // lanes past n hold zeros
       const double total = wave_sum(static_cast<double>(dot));
       if (lane == 0) dot_part[static_cast<size_t>(r) * col_blocks + tc.cb] = total;
+    }
+  };
+#pragma unroll
+  for (int b = 0; b < kDepth; ++b)
+    if (wv + b * kBwdWaves < nrows) load(wv + b * kBwdWaves, b);
+  if (p.route_w != nullptr) __syncthreads();  // row_w
+  for (int i = wv; i < nrows; i += kDepth * kBwdWaves) {  // uniform conditions per wave
+#pragma unroll
+    for (int b = 0; b < kDepth; ++b) {
+      if (i + b * kBwdWaves < nrows) work(i + b * kBwdWaves, b);
+      if (i + (b + kDepth) * kBwdWaves < nrows) load(i + (b + kDepth) * kBwdWaves, b);
     }
   }
   if (p.grad_bias == nullptr) return;

@@ -27,7 +27,7 @@ struct BalanceArgs {
 struct BalancePlan {
   int32_t tile, ntiles, pitch, chunks;
   int64_t slots;
-  size_t off_probs, off_counts, off_z, off_tokens, off_dots, bytes;
+  size_t off_probs, off_counts, off_z, off_tokens, off_dots, off_arrived, bytes;
 };
 BalancePlan balance_plan(int32_t s, int32_t e, int32_t g);
 
@@ -59,6 +59,10 @@ struct ExpertAct {
 };
 hipError_t launch_expert_act(const LayoutView& L, const ExpertAct& p, int dtype, hipStream_t stream);
 int64_t expert_act_grid(const LayoutView& L, int n, bool gated);  // its workgroups
+// Its input gradient: out[r] = a[r] @ W[x] with W [e, m, n] (m weight rows, n inputs): the
+// struct's a = the gradient rows [rows, m], out [rows, n], nz = n; no epilogue.
+hipError_t launch_expert_act_dgrad(const LayoutView& L, const ExpertAct& p, int dtype, hipStream_t stream);
+int64_t expert_act_dgrad_grid(const LayoutView& L, int n);
 
 // Its epilogue's backward (n, nz as above).
 struct ExpertActBackward {

@@ -427,9 +427,9 @@ moe_status_t moe_expert_gemm_act(const moe_layout_t* layout, const void* a, int3
  *   grad_topk_w[t,j] = <grad_out[r], u(z[r])> for the route placed at r, 0 for a dropped one
  *   grad_residual[r] = grad_out[r] for placed rows, 0 for the others (a bit copy)
  * relu' is 0 at 0. Rows no route fills are zero in grad_preact and not read in grad_out and
- * preact. The gradients of a and weights are then moe_expert_gemm_dgrad and
- * moe_expert_gemm_wgrad of grad_preact (with n = nz); that of a gathered residual is
- * moe_dispatch_backward of grad_out.
+ * preact. The gradients of a and weights are then moe_expert_act_dgrad (or
+ * moe_expert_gemm_dgrad) and moe_expert_gemm_wgrad of grad_preact (with n = nz); that of a
+ * gathered residual is moe_dispatch_backward of grad_out.
  *   grad_out [rows, n]; preact [rows, nz] as kept by the forward (NULL allowed for
  *   MOE_ACT_NONE, not gated and without grad_topk_w: nothing needs it); both of dtype.
  *   topk_w [s, k] or NULL as in the forward; grad_preact [rows, nz] of dtype, grad_bias
@@ -448,6 +448,18 @@ moe_status_t moe_expert_act_backward(const moe_layout_t* layout, const void* gra
                                      void* grad_preact, moe_dtype_t bias_dtype, void* grad_bias,
                                      float* grad_topk_w, void* grad_residual, void* workspace,
                                      size_t workspace_bytes, void* stream);
+
+/*
+ * Input-row gradient of moe_expert_gemm_act, from its epilogue's grad_preact [rows, nz]:
+ *   grad_a[r, :] = grad_preact[r, :] @ weights[x]       (weights [e, nz, m], grad_a [rows, m])
+ * for the placed rows r of expert x, rows no route fills zero: moe_expert_gemm_dgrad's
+ * product on the tiles of moe_expert_gemm_act (whose heights follow the segments), summed in
+ * another order. The gradient of gathered token rows is moe_dispatch_backward of grad_a.
+ * Arguments as in moe_expert_gemm_dgrad, with n = nz.
+ */
+moe_status_t moe_expert_act_dgrad(const moe_layout_t* layout, const void* grad_preact,
+                                  const void* weights, int32_t m, int32_t nz, moe_dtype_t dtype,
+                                  void* grad_a, void* stream);
 
 /*
  * Input-row gradient of moe_expert_gemm ([DS-8213] first commit: the backward replays the
@@ -510,7 +522,7 @@ moe_status_t moe_expert_gemm_wgrad(const moe_layout_t* layout, const void* a, in
  * loss and z float64, rounded once. A token whose logits are all -inf has no distribution:
  * it counts among the tokens, its routes are counted, and it adds 0 to probs and z. NaN or
  * +inf in an unpadded token's logits makes probs, loss and z of its group NaN, no other's.
- * One launch for a single group of up to 16384 logits, else two (three for e > 128).
+ * One launch for a single group of up to 16384 logits, else two.
  */
 size_t moe_balance_workspace_bytes(int32_t s, int32_t e, int32_t g);
 moe_status_t moe_balance_loss(const float* logits, const int32_t* topk_idx,

@@ -82,6 +82,19 @@ def test_backward_argument_checks(lib):
         assert "overlap" in lib.moe_last_error().decode()
 
 
+@no_gpu_only
+def test_input_gradient_argument_checks(lib):
+    st = _fake_handle(40, 8, 2, 0, 1 << 24, M.workspace_bytes(40, 8, 2, 0))
+
+    def call(g=at(0), w=at(1), m=64, nz=64, dtype=1, out=at(2), layout=st):
+        return lib.moe_expert_act_dgrad(ctypes.byref(layout), g, w, m, nz, dtype, out, None)
+
+    assert call(dtype=0) == 2 and call(nz=4) == 5 and call(m=12) == 5 and call(m=0) == 1
+    assert call(g=None) == 1 and call(w=None) == 1 and call(out=None) == 1
+    assert call(out=at(2, 8)) == 5 and call(layout=M.LayoutStruct()) == 4
+    assert call(out=at(0, 512)) == 1 and "overlap" in lib.moe_last_error().decode()
+
+
 def test_binding_refuses_mismatched_tensors(monkeypatch):
     def refuse():
         raise AssertionError("the library was called with arguments the binding should have refused")
@@ -108,6 +121,8 @@ def test_binding_refuses_mismatched_tensors(monkeypatch):
         (lambda: M.moe_expert_act_backward(L, g, act="silu"), "preact is required"),
         (lambda: M.moe_expert_act_backward(L, g, z, gated=True, need_w=True), "w is required"),
         (lambda: M.moe_expert_act_backward(L, g, z, gated=True, bias_dtype=torch.float16), "bias_dtype must be"),
+        (lambda: M.moe_expert_act_dgrad(L, z, w[:, :15]), "weights must have shape [4, 16, *]"),
+        (lambda: M.moe_expert_act_dgrad(L, z, w, out=g[:11]), "out must have shape [12, 8]"),
         (lambda: M.moe_expert_gemm_act(L, x, w), "on the GPU"),
     ]:
         with pytest.raises(ValueError) as err:

@@ -168,6 +168,13 @@ def run_case(idx, m, n, e, cap, pad, rm, dtype, name, gated, bias, weighted, res
     got = M.moe_expert_act_backward(Lg, dev(g), dev(zk), act=name, gated=gated, w=dev(w), need_w=weighted,
                                     bias_dtype=torch.float32 if bias_dt == "f32" else big[0].dtype, need_residual=True)
     check_backward(got, L, g, zk, dtype, name, gated, w, bias_dt, what)
+    gz = to_host(got[0])
+    ga = torch.full((L.rows + 2, m), 3.0, dtype=big[0].dtype, device="cuda")
+    M.moe_expert_act_dgrad(Lg, got[0], dev(wts), out=ga[1:-1])
+    assert (ga[0] == 3).all() and (ga[-1] == 3).all(), "rows beside the input gradient were written"
+    _, want = oracle.expert_gemm_dgrad(L, gz, wts, dtype)
+    _, mag = oracle.expert_gemm_dgrad(L, absolute(gz, dtype), absolute(wts, dtype), dtype)
+    within(to_host(ga[1:-1].contiguous()), want, (nz + 3) * 2 * U * mag, dtype, what + ", grad_a")
     if gated or name != "none":
         less = M.moe_expert_act_backward(Lg, dev(g), dev(zk), act=name, gated=gated, w=dev(w))
         assert_bits_equal(to_host(less[0]), to_host(got[0]), "grad_preact alone")
@@ -276,6 +283,30 @@ def test_nan_and_inf_stay_where_they_are():
         assert np.array_equal(np.isfinite(f), np.isfinite(out))
 
 
+def test_input_gradient_of_whole_numbers_is_exact():
+    """K tails of every length, and infinities in weights past which nothing may reach."""
+    announce("expert act dgrad integers")
+    rng = np.random.default_rng(11)
+    for s, e, k, nz, m, dtype in ((700, 3, 2, 8, 264, "bf16"), (90, 1, 1, 72, 8, "f16"), (300, 4, 1, 200, 520, "bf16"),
+                                  (2000, 4, 2, 64, 136, "f16"), (20, 8, 2, 136, 72, "bf16")):
+        idx = W.random_idx(rng, s, e, k)
+        L, Lg = oracle.dispatch_layout(idx, e, 0), M.moe_dispatch_layout(to_dev(idx), e, 0)
+        g = W.cast_input(rng.integers(-2, 3, (L.rows, nz)).astype(np.float32), dtype)
+        wts = W.cast_input(rng.integers(-2, 3, (e, nz, m)).astype(np.float32), dtype)
+        want, _ = oracle.expert_gemm_dgrad(L, g, wts, dtype)
+        got = M.moe_expert_act_dgrad(Lg, to_dev(g, dtype), to_dev(wts, dtype))
+        assert_bits_equal(to_host(got), want, f"{s} {nz} {m}")
+        assert torch.equal(got, M.moe_expert_gemm_dgrad(Lg, to_dev(g, dtype), to_dev(wts, dtype)))
+        w32 = oracle.to_f32(wts, dtype).copy()
+        w32[0, nz - 1, 3], g32 = np.inf, np.abs(oracle.to_f32(g, dtype)) + 1  # positive rows: sums of one sign at inf
+        got = M.moe_expert_act_dgrad(Lg, to_dev(W.cast_input(g32, dtype), dtype), to_dev(W.cast_input(w32, dtype), dtype))
+        f = oracle.to_f32(to_host(got), dtype)
+        rows = slice(int(L.offsets[0]), int(L.offsets[0]) + int(L.kept[0]))
+        assert np.isposinf(f[rows, 3]).all()
+        f[rows, 3] = 0
+        assert np.isfinite(f).all()
+
+
 @pytest.mark.parametrize("name", E.ACTS)
 def test_activations_over_their_range(name):
     """One product per output sets z to any element value: every finite bf16 from 1e-3 to 1e5,
@@ -333,7 +364,7 @@ def test_replays_from_a_graph_and_runs_beside_another_stream(s):
         L = M.moe_dispatch_layout(idx, e, 0)
         out, pre = M.moe_expert_gemm_act(L, x, wts, bias=bias, act="silu", gated=True, w=w, save_preact=True)
         gz, gb, gw, _ = M.moe_expert_act_backward(L, g, pre, act="silu", gated=True, w=w, need_w=True, bias_dtype=torch.bfloat16)
-        return out, pre, gz, gb, gw, M.moe_expert_gemm_dgrad(L, gz, wts), M.moe_expert_gemm_wgrad(L, x, gz)
+        return out, pre, gz, gb, gw, M.moe_expert_act_dgrad(L, gz, wts), M.moe_expert_gemm_wgrad(L, x, gz)
 
     first = [t.clone() for t in step()]
     torch.cuda.synchronize()
@@ -422,7 +453,7 @@ def test_autograd_matches_the_oracle_chain(name, gated, gather, weighted, bias, 
                                                bias_dtype=None if b is None else b.dtype, need_w=weighted, need_residual=True)
     check_backward((gz, gb, gw, gr), L, g, to_host(pre), dtype, name, gated, None if w is None else to_host(w),
                    "f32" if bias == "f32" else dtype, "chain")
-    ga = M.moe_expert_gemm_dgrad(Lg, gz, wts.detach())
+    ga = M.moe_expert_act_dgrad(Lg, gz, wts.detach())
     assert torch.equal(grads["x"], M.moe_dispatch_backward(Lg, ga) if gather else ga)
     assert torch.equal(grads["wts"], M.moe_expert_gemm_wgrad(Lg, x.detach(), gz, gather=gather, out_dtype=td))
     if b is not None:
