@@ -171,14 +171,14 @@ def _check(status: int) -> None:
 if hasattr(torch._C, "_cuda_getCurrentRawStream"):
     def _stream(t: torch.Tensor):
         """The current HIP stream of t's device, as the library takes it (void*)."""
-        return ctypes.c_void_p(torch._C._cuda_getCurrentRawStream(t.get_device()))
+        return torch._C._cuda_getCurrentRawStream(t.get_device())
 else:  # older torch: the public (slower) route
     def _stream(t: torch.Tensor):
-        return ctypes.c_void_p(torch.cuda.current_stream(t.device).cuda_stream)
+        return torch.cuda.current_stream(t.device).cuda_stream
 
 
 def _ptr(t):
-    return ctypes.c_void_p(t.data_ptr()) if t is not None else ctypes.c_void_p(0)
+    return t.data_ptr() if t is not None else None  # as ctypes takes a void*
 
 
 def _require_gpu(*tensors):
@@ -627,18 +627,18 @@ def moe_renormalize_kept_backward(layout: Layout, w: torch.Tensor, grad_out: tor
 def _launch(t: torch.Tensor, fn, *args) -> None:
     """fn(*args, current stream of t's device), with that device current (a launch goes to
     the current device's stream); its status checked."""
-    if torch.cuda.current_device() == t.get_device():
+    if torch._C._cuda_getDevice() == t.get_device():
         _check(fn(*args, _stream(t)))
     else:
         with torch.cuda.device(t.device):
             _check(fn(*args, _stream(t)))
 
 
-def _one_device(*tensors) -> None:
-    _require_gpu(*tensors)
-    devices = {t.device for t in tensors if t is not None}
-    if len(devices) > 1:
-        raise ValueError(f"all tensors must be on one device, got {sorted(map(str, devices))}")
+def _one_device(first, *others) -> None:
+    _require_gpu(first, *others)
+    for t in others:
+        if t is not None and t.get_device() != first.get_device():
+            raise ValueError(f"all tensors must be on one device, got {first.device} and {t.device}")
 
 
 def _group_count(mask, groups, s: int) -> int:
@@ -676,15 +676,16 @@ def moe_balance_loss(logits: torch.Tensor, idx: torch.Tensor, mask=None, groups=
                 raise ValueError(f"out: {name} is None")
             _expect(t, name, shape, dt)
     _one_device(logits, idx, mask, groups, workspace, *(out or ()))
-    dev = logits.device
     if out is None:
-        out = (torch.empty((g, e), dtype=torch.int32, device=dev), torch.empty(g, dtype=torch.int32, device=dev),
-               torch.empty((g, e), dtype=torch.float32, device=dev), torch.empty(g, dtype=torch.float32, device=dev),
-               torch.empty(g, dtype=torch.float32, device=dev))
-    if workspace is None:
-        workspace = torch.empty(lib().moe_balance_workspace_bytes(s, e, g), dtype=torch.uint8, device=dev)
-    _launch(logits, lib().moe_balance_loss, _ptr(logits), _ptr(idx), _ptr(mask), _ptr(groups), s, e, k, g,
-            *(_ptr(t) for t in out), _ptr(workspace), workspace.numel())
+        like = logits.new_empty
+        out = (like((g, e), dtype=torch.int32), like(g, dtype=torch.int32), like((g, e)), like(g), like(g))
+    nbytes = lib().moe_balance_workspace_bytes(s, e, g)
+    if workspace is None and nbytes:
+        workspace = logits.new_empty(nbytes, dtype=torch.uint8)
+    counts, tokens, probs, loss, z = out
+    _launch(logits, lib().moe_balance_loss, logits.data_ptr(), idx.data_ptr(), _ptr(mask), _ptr(groups), s, e, k, g,
+            counts.data_ptr(), tokens.data_ptr(), probs.data_ptr(), loss.data_ptr(), z.data_ptr(), _ptr(workspace),
+            workspace.numel() if workspace is not None else 0)
     return tuple(out)
 
 

@@ -874,10 +874,10 @@ moe_status_t moe_balance_loss(const float* logits, const int32_t* topk_idx,
   MOE_TRY(check_array(probs, g, "probs", false));
   MOE_TRY(check_array(loss, g, "loss", false));
   MOE_TRY(check_array(z, g, "z", false));
-  if (workspace == nullptr) return fail(MOE_ERR_INVALID_ARG, "workspace is NULL");
+  const moe::BalancePlan p = moe::balance_plan(s, e, g);
+  if (workspace == nullptr && p.bytes > 0) return fail(MOE_ERR_INVALID_ARG, "workspace is NULL");
   if ((reinterpret_cast<uintptr_t>(workspace) & (kAlign - 1)) != 0)
     return fail(MOE_ERR_MISALIGNED, "workspace is not %zu-byte aligned", kAlign);
-  const moe::BalancePlan p = moe::balance_plan(s, e, g);
   if (workspace_bytes < p.bytes)
     return fail(MOE_ERR_WORKSPACE, "workspace has %zu bytes, the balance loss needs %zu", workspace_bytes, p.bytes);
   const moe::BalanceArgs a{logits, topk_idx, token_mask, groups, s, e, k, g};

@@ -50,6 +50,7 @@ BalancePlan balance_plan(int32_t s, int32_t e, int32_t g) {
   p.pitch = (e + 3) / 4 * 4;
   p.chunks = (e + kBalChunk - 1) / kBalChunk;
   p.slots = static_cast<int64_t>(p.ntiles) + g - 1;
+  if (p.ntiles == 1 && g == 1) return p;  // finished by the first launch: no partial rows
   size_t at = 0;
   auto take = [&](size_t n) {
     const size_t here = at;
@@ -231,9 +232,10 @@ __global__ __launch_bounds__(kBalBlock) void balance_tile_kernel(BalanceArgs a, 
     int lo = t0, hi = t1;
     if (a.groups != nullptr) {
       const int first = a.groups[j], last = a.groups[j + 1];
-      if (first >= t1) break;
+      if (first >= t1 && !single) break;
       lo = first > t0 ? first : t0;
       hi = last < t1 ? last : t1;
+      if (hi < lo) hi = lo;
     }
     if (lo >= hi && !single) continue;  // uniform; a single tile finishes its group, empty or not
 
@@ -541,8 +543,7 @@ hipError_t launch_balance_loss(const BalanceArgs& a, const BalancePlan& p, char*
                              reinterpret_cast<double*>(ws + p.off_z), reinterpret_cast<int32_t*>(ws + p.off_tokens),
                              reinterpret_cast<double*>(ws + p.off_dots),
                              reinterpret_cast<int32_t*>(ws + p.off_arrived)};
-  // groups given by offsets may leave tokens out, so only a whole batch is finished at once
-  const bool single = p.ntiles == 1 && a.g == 1 && a.groups == nullptr;
+  const bool single = p.ntiles == 1 && a.g == 1;
   with_rows(a.e, rows16(a.logits, a.e), [&](auto shape, auto vec) {
     using S = decltype(shape);
     balance_tile_kernel<S::lpt, S::nv, decltype(vec)::value>

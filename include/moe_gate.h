@@ -517,7 +517,8 @@ moe_status_t moe_expert_gemm_wgrad(const moe_layout_t* layout, const void* a, in
  *              unspecified results, never an access out of bounds); NULL (g = 1): all tokens
  *   counts [g, e] int32, tokens [g] int32, probs [g, e], loss [g], z [g] float32: out
  *   workspace  device buffer of moe_balance_workspace_bytes(s, e, g) bytes, 256-byte aligned
- *              (not kept after the call; calls that may overlap in time need one each)
+ *              (not kept after the call; calls that may overlap in time need one each). 0
+ *              bytes: none is needed, NULL will do (or the sizes are refused by the call)
  * Probabilities and their sums over a tile of tokens are float32, sums over tiles, the
  * loss and z float64, rounded once. A token whose logits are all -inf has no distribution:
  * it counts among the tokens, its routes are counted, and it adds 0 to probs and z. NaN or

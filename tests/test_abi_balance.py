@@ -23,7 +23,8 @@ def lib():
 
 def test_workspace_bytes(lib):
     f = lib.moe_balance_workspace_bytes
-    assert f(0, 8, 1) > 0 and f(256, 8, 1) % 256 == 0
+    assert f(0, 8, 1) == 0 and f(256, 8, 1) == 0  # one launch, no partial rows
+    assert f(0, 8, 2) > 0 and f(256, 8, 2) % 256 == 0
     # a partial row of 2 x 4 bytes per expert for each of up to 512 tiles
     assert f(100000, 128, 1) >= 512 * 128 * 8 > f(100000, 128, 1) - (1 << 15)
     assert f(100000, 128, 100) > f(100000, 128, 1)
@@ -32,9 +33,9 @@ def test_workspace_bytes(lib):
 
 @no_gpu_only
 def test_balance_argument_checks(lib):
-    need = lib.moe_balance_workspace_bytes(100, 8, 1)
+    need = lib.moe_balance_workspace_bytes(10000, 8, 1)
 
-    def fwd(logits=P[0], idx=P[1], mask=None, groups=None, s=100, e=8, k=2, g=1, counts=P[2], tokens=P[3], probs=P[4],
+    def fwd(logits=P[0], idx=P[1], mask=None, groups=None, s=10000, e=8, k=2, g=1, counts=P[2], tokens=P[3], probs=P[4],
             loss=P[5], z=P[6], ws=P[7], n=need):
         return lib.moe_balance_loss(logits, idx, mask, groups, s, e, k, g, counts, tokens, probs, loss, z, ws, n, None)
 

@@ -114,6 +114,8 @@ CASES = [
     (3000, 64, 4, list(range(0, 3001, 3)), 0.2),            # a thousand groups
     (3000, 32, 2, [5, 5, 31, 32, 33, 96, 1500, 2990], 0.1), # tokens before and after every group
     (200, 32, 2, None, 1.0),            # nothing but padding
+    (200, 32, 2, [50, 170], 0.2),       # one group of part of the batch, in one launch
+    (200, 32, 2, [200, 200], 0.0),      # and of none of it
 ]
 
 
@@ -325,8 +327,9 @@ def test_refusals():
     ok = M.moe_balance_loss(logits, idx)
     with pytest.raises(ValueError, match="contiguous"):
         M.moe_balance_loss(torch.randn((8, 10), device="cuda").t(), idx)
+    groups = torch.tensor([0, 5, 10], dtype=torch.int32, device="cuda")
     with pytest.raises(M.MoeError, match="MOE_ERR_WORKSPACE"):
-        M.moe_balance_loss(logits, idx, workspace=torch.empty(64, dtype=torch.uint8, device="cuda"))
+        M.moe_balance_loss(logits, idx, groups=groups, workspace=torch.empty(64, dtype=torch.uint8, device="cuda"))
     with pytest.raises(M.MoeError, match="k must be"):
         M.moe_balance_loss(logits, torch.zeros((10, 9), dtype=torch.int32, device="cuda"))
     with pytest.raises(M.MoeError, match="overlap"):
