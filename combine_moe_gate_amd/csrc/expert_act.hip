@@ -6,7 +6,8 @@
 // projection, whose weights hold the n gate rows, then the n up rows. Kept apart from the
 // plain product, the activation would read and write every [rows, n] value again.
 //
-// Two kernels, by how many rows an expert has on average:
+// Two kernels, chosen by the rows an expert has on average and by the workgroups there would
+// be (act_shape() below):
 //
 // Tiles (long segments; bound by the matrix cores). A workgroup of eight waves, 2 along the
 // rows by 4 along the columns, multiplies up to 288 rows by 256 weight rows of one expert
@@ -17,9 +18,9 @@
 // height is a multiple of 32 rows (FM 16-row MFMA tiles for each of the two waves along the
 // rows), and the main loop is compiled for each of the nine. Operands go to LDS directly
 // (64-element K steps, two stages, XOR-swizzled: conflict-free 16-byte fragment reads, whole
-// 128-byte lines from memory). Fragments of the token rows are read kAhead MFMA groups
-// before their use, across the K step's border: the next stage is published kAhead groups
-// before the step ends, and the loads of the stage after it start there.
+// 128-byte lines from memory). Fragments are read a group of up to four MFMA row tiles ahead
+// of their use, across the K step's border: the next stage is published, by the step's one
+// barrier, before its last group's MFMAs, and the loads of the stage after it start there.
 // For a gated projection a wave's 64 weight rows are 32 gate rows and the 32 up rows that
 // meet them, so both products of an output are in one wave. The finished sums leave through
 // a piece of LDS of the wave's own, 16 rows at a time, and come back as eight consecutive
@@ -27,9 +28,19 @@
 // epilogue's code exists once whatever the tile's height.
 //
 // Few rows (decoding; bound by reading the weights). A workgroup of four waves multiplies
-// up to 16 F rows by 64 weight rows, each wave a quarter of the K steps: weights go from
+// up to 16 F rows by 16 FB weight rows, each wave a quarter of the K steps: weights go from
 // memory straight to the registers the MFMA reads, several steps ahead (nothing is reused,
 // so LDS would only add a stop), and the four partial sums meet in LDS.
+//
+// The input-row gradient runs the tiles on the same weights, which are [K][N] to it: pieces
+// of 64 K rows by 256 features are staged as they lie and read through LDS's transposing
+// reads, and a tile has at most 256 rows (nine units would spill).
+//
+// Measured (bf16, random routing): 65536 rows of 128 experts by 4096 x 4096 (gated, 2.2
+// TFLOP) with bias and kept pre-activations 2.1 ms, 1040 TFLOP/s; one dense expert 1250
+// TFLOP/s, where the same loop without loads from memory reaches 1530 and a library product
+// of that size 1340. 32768 rows by 2816 x 2816, weights read once 2.1 GB: 0.58 ms, 3.7 TB/s.
+// One token, 8 experts of 128, 201 MB of weights: 40 us, 5.0 TB/s.
 #include <atomic>
 #include <utility>
 
@@ -420,9 +431,9 @@ __global__ __launch_bounds__(kActThreads) __attribute__((amdgpu_waves_per_eu(2, 
 constexpr int kFewThreads = 256, kFewWaves = 4;
 
 template <int DT, int F, int FB>
-__global__ __launch_bounds__(kFewThreads, F == 4 ? 2 : F == 2 || FB == 4 ? 3 : 4) void expert_act_few_kernel(ExpertAct p, int col_blocks,
-                                                                                  int tile_grid) {
-  constexpr int kDepth = F == 4 ? 1 : FB == 2 ? 4 : F == 1 ? 3 : 2;  // K steps of 64 elements in flight per wave
+__global__ __launch_bounds__(kFewThreads, F == 4 ? 2 : 4) void expert_act_few_kernel(ExpertAct p, int col_blocks,
+                                                                                     int tile_grid) {
+  constexpr int kDepth = F == 4 ? 1 : 4;  // K steps of 64 elements in flight per wave
   constexpr int kCols = 16 * FB;                        // weight rows per workgroup
   constexpr int kPitch = kCols * 4 + 16;                // bytes per row of a wave's float32 sums
   extern __shared__ __attribute__((aligned(1024))) char lds[];  // [wave][16 F rows][kPitch]
@@ -558,14 +569,6 @@ __global__ __launch_bounds__(kFewThreads, F == 4 ? 2 : F == 2 || FB == 4 ? 3 : 4
 
 constexpr int kZeroBlocks = 64;  // workgroups that clear rows no route fills
 
-// F of the row tiles (16 F rows) for segments of few rows on average; 0: the large tiles.
-static int few_rows(const LayoutView& L) {
-  const int64_t most = L.capacity > 0 && L.capacity < L.s ? L.capacity : L.s;  // no expert has more rows
-  const int64_t routes = static_cast<int64_t>(L.s) * L.k;
-  const int64_t mean = (routes + L.e - 1) / L.e < most ? (routes + L.e - 1) / L.e : most;
-  return most <= 16 || mean <= 12 ? 1 : mean <= 24 ? 2 : mean <= 64 ? 4 : 0;
-}
-
 // At most this many row tiles of a height, known without reading the layout: a segment of R
 // rows has fewer than R / height + 1.
 static int64_t row_tiles(const LayoutView& L, int height) {
@@ -580,24 +583,47 @@ static int64_t row_tiles(const LayoutView& L, int height) {
   return routes / height + with_rows;
 }
 
-// How a launch is shaped: F (above; `kn`: the large tiles in any case) and the weight rows
-// per workgroup.
+// How a launch is shaped: F of its row tiles (16 F rows; 0: the large tiles), the weight rows
+// per workgroup, and its workgroups.
 struct ActShape {
   int few, cols;
   int64_t col_blocks, tiles;
 };
+
+// The large tiles move the most once there are enough of them to fill the CUs several times;
+// until then the last of few rounds is mostly idle. F = 1 is for experts with a handful of
+// rows, its 32 weight rows per workgroup (against 64: 40 us to 51 for one token's 8 of 128
+// experts, 1536 x 4096 gated; 89 to 92 for 24 tokens of 64 experts, 2816 x 1408). F = 4, 64
+// weight rows wide, is for small products, where all its workgroups are resident at once
+// (two per CU) and each is short. Microseconds, bf16, random rows (`mean` per expert):
+//   experts, weight rows x length   mean    F = 1   F = 4   large tiles
+//   128, 4096 x 4096                4       816             735   (2064 of them)
+//   64, 2816 x 1408                 4       101     105     109   (704)
+//   64, 2816 x 1408                 12      115     113     107
+//   64, 2816 x 1408                 64              235     127
+//   8, 1024 x 1024                  12      7.5     10      11    (32)
+//   8, 1024 x 4096                  24      33      32      47
+//   16, 528 x 520                   64      11      8.2     12.5  (57)
+//   16, 528 x 520                   128     17      11      16
+//   8, 2048 x 1024                  64      33      22      18    (F = 4 would be 512)
+constexpr int64_t kActMany = 1024, kActFewMost = 448;
+constexpr int kActOneMean = 8, kActOneSmall = 12;
 static ActShape act_shape(const LayoutView& L, int n, bool gated, bool kn) {
-  ActShape a{kn ? 0 : L.s == 0 ? 1 : few_rows(L), kActBN, 0, 0};
-  const int per = gated ? 2 : 1;
-  auto fit = [&](int cols) {
-    a.cols = cols;
-    a.col_blocks = (static_cast<int64_t>(n) * per + cols - 1) / cols;
-    a.tiles = L.s == 0 ? 0 : row_tiles(L, a.few ? 16 * a.few : kn ? 32 * act_units<true> : kActBM) * a.col_blocks;
+  auto shape = [&](int few) {
+    ActShape a{few, few == 1 ? 32 : few == 4 ? 64 : kActBN, 0, 0};
+    a.col_blocks = (static_cast<int64_t>(n) * (gated ? 2 : 1) + a.cols - 1) / a.cols;
+    a.tiles = L.s == 0 ? 0 : row_tiles(L, few ? 16 * few : kn ? 32 * act_units<true> : kActBM) * a.col_blocks;
+    return a;
   };
-  fit(a.few ? 64 : kActBN);
-  // half as wide where that leaves fewer than four workgroups per CU
-  if (a.few == 1 && a.tiles < 1024) fit(32);
-  return a;
+  const ActShape large = shape(0);
+  if (kn || large.tiles >= kActMany) return large;
+  const int64_t routes = static_cast<int64_t>(L.s) * L.k;
+  int64_t mean = (routes + L.e - 1) / L.e;
+  if (L.capacity > 0 && mean > L.capacity) mean = L.capacity;
+  const ActShape small = shape(4);
+  const bool fits = small.tiles <= kActFewMost;
+  if (mean <= (fits ? kActOneSmall : kActOneMean)) return shape(1);
+  return fits ? small : large;
 }
 
 int64_t expert_act_grid(const LayoutView& L, int n, bool gated) {
@@ -633,7 +659,6 @@ static hipError_t launch_few(const ExpertAct& p, int col_blocks, int64_t grid, h
   return hipGetLastError();
 }
 
-// `few` and the tiles' width as act_shape() gave them.
 template <int DT, bool KN>
 static hipError_t launch_tiles(const ExpertAct& p, int col_blocks, int64_t grid, hipStream_t stream) {
   static std::atomic<uint64_t> done{0};
@@ -650,9 +675,7 @@ static hipError_t launch_dt(const LayoutView& L, const ExpertAct& p, hipStream_t
   const ActShape a = act_shape(L, p.n, p.gated, false);
   const int64_t grid = expert_act_grid(L, p.n, p.gated);
   const int col_blocks = static_cast<int>(a.col_blocks);
-  if (a.few == 1 && a.cols == 32) return launch_few<DT, 1, 2>(p, col_blocks, grid, stream);
-  if (a.few == 1) return launch_few<DT, 1, 4>(p, col_blocks, grid, stream);
-  if (a.few == 2) return launch_few<DT, 2, 4>(p, col_blocks, grid, stream);
+  if (a.few == 1) return launch_few<DT, 1, 2>(p, col_blocks, grid, stream);
   if (a.few == 4) return launch_few<DT, 4, 4>(p, col_blocks, grid, stream);
   return launch_tiles<DT, false>(p, col_blocks, grid, stream);
 }
