@@ -21,7 +21,13 @@
 // a sum over the LPT lanes, DPP steps without LDS. Tiles are contiguous tokens; a tile
 // adds up its waves' sums in a fixed order and writes one partial row per group it meets,
 // and a second launch adds the partial rows of each group, in float64 and tile order.
-// Nothing depends on an order of arrival: the only atomics are the LDS integer counts.
+// Nothing depends on an order of arrival: sums are taken in a fixed order, and the only
+// atomics are integer counts.
+//
+// Measured: 65536 tokens, 512 experts, 10 routes: forward 35-43 us and 7 us for the partial
+// rows, 137 MB read, 3.2-3.9 TB/s; backward 45 us, 268 MB, 6.0 TB/s. 32768 tokens, 128 experts,
+// 8 routes: 10 + 7 us and 10 us, mostly the time of a launch and a tile's first loads. One
+// tile, 256 tokens, 8 experts: 5 us and 3 us.
 #include <type_traits>
 
 #include "moe_device.h"
@@ -345,8 +351,8 @@ __global__ __launch_bounds__(kBalBlock) void balance_tile_kernel(BalanceArgs a, 
 // Forward, second launch: workgroup (chunk, group) adds the group's partial rows over
 // kBalChunk experts: 4 lanes of four experts by 64 rows at a time, in float64, then the 64 in
 // order. One workgroup alone draws the partial rows, which other XCDs wrote, at some 40 GB/s:
-// 512 rows of 128 experts in one workgroup took 15 us, in eight they take 5. The chunks'
-// shares of the loss go to the group's last workgroup to arrive (counted on `arrived`, which
+// 512 rows of 128 experts in one workgroup took 15 us, in eight they take 7, most of it the
+// launch and two rounds of loads. The chunks' shares of the loss go to the group's last workgroup to arrive (counted on `arrived`, which
 // the first launch clears), which adds them in chunk order.
 __global__ __launch_bounds__(kBalReduce) void balance_reduce_kernel(BalanceArgs a, int tile, int pitch, int chunks,
                                                                     BalancePartials part, BalanceOut out) {

@@ -18,8 +18,9 @@ constexpr float kTanhQ = 0.044715f;
 // Phi(z), the normal distribution function, with E = exp(-z^2 / 2) on the way (Abramowitz and
 // Stegun, Handbook of Mathematical Functions, formula 7.1.26: erfc within 1.5e-7 as a fifth
 // degree polynomial in 1 / (1 + 0.3275911 x) times exp(-x^2), x = |z| / sqrt 2). A third of
-// the library erff's instructions, which a tile's epilogue pays for each of its outputs: on
-// 65536 x 4096 outputs of 1024 products each the kernel takes 0.60 ms with it, 0.71 without.
+// the library erff's instructions, which a tile's epilogue pays for each of its outputs: 65536
+// x 4096 outputs of 256 products each take 380 us with it, 469 with erff. Its error is
+// absolute, as that of 1 + erff is: z Phi(z) is within 1e-7 |z|.
 __device__ __forceinline__ float normal_cdf(float z, float* E) {
   const float x = __builtin_fabsf(z) * 0.7071067811865476f;
   const float t = __builtin_amdgcn_rcpf(__builtin_fmaf(0.3275911f, x, 1.0f));

@@ -11,7 +11,11 @@
 // 16-byte pieces (gated: of both halves), so the bias sums of its features stay in a lane's
 // registers over the rows. The waves' sums meet in LDS in order and go out as one partial
 // row; a row's dot is reduced across the wave in float64 and goes out per column block. A
-// second launch adds both up in a fixed order. No floating-point atomics.
+// second launch adds both up in a fixed order. No floating-point atomics. Four rows per wave
+// are in flight, since a row's loads alone would leave memory idle while it is finished.
+//
+// Measured: 49152 rows of 1408 gated features (0.69 GB) 134 us, 5.2 TB/s; 2000 rows of 264
+// gated features with bias 20 us and 4 us for the sums.
 #include "expert_act.h"
 
 namespace moe {

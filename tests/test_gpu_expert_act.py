@@ -227,13 +227,45 @@ def test_uneven_segments():
         run_case(idx, 200, 272, 6, 0, 1, False, "f16", "gelu_tanh", gated, "own", True, "rows", True, 5)
 
 
+WIDE = [  # products wide enough for the large tiles, columns as above
+    (1000, 264, 1000, 8, 2, 0, 1, False, "bf16", "silu", True, "f32", True, "tokens", True),
+    (1000, 136, 1096, 8, 3, 200, 1, True, "f16", "gelu_tanh", False, "own", True, "rows", True),
+    (300, 64, 2056, 4, 2, 0, 64, False, "bf16", "gelu", True, "own", False, "rows", False),
+    (700, 8, 2600, 2, 1, 0, 1, False, "bf16", "none", False, None, True, None, True),
+    (60, 136, 5000, 2, 2, 0, 1, False, "f16", "silu", True, "f32", False, "tokens", True),
+    (40, 72, 4096, 64, 8, 0, 1, False, "bf16", "relu", False, "own", True, "tokens", True),  # five rows an expert
+]
+
+
+@pytest.mark.parametrize("case", WIDE, ids=[f"{c[0]}-{c[1]}-{c[2]}-{c[3]}-{c[9]}" for c in WIDE])
+def test_wide_products_match_the_oracle(case):
+    test_matches_the_oracle(case)
+
+
+@pytest.mark.parametrize("rows", ROWS)
+def test_every_tile_height_of_wide_products(rows):
+    """As many columns as make 64-row pieces too many for the form of short segments."""
+    announce("expert act wide height", rows)
+    n = 32 * -(-449 // (rows // 64 + 1)) + 8
+    run_case(np.zeros((rows, 1), np.int32), 72, n, 1, 0, 1, False, "bf16", "silu", True, "own", True, "tokens", True, rows)
+
+
+def test_uneven_segments_of_wide_products():
+    announce("expert act wide uneven")
+    idx = np.repeat(np.arange(6), [1, 30, 33, 0, 700, 64]).astype(np.int32)
+    idx = idx[np.random.default_rng(1).permutation(len(idx))][:, None]
+    for gated in (False, True):
+        run_case(idx, 200, 1608, 6, 0, 1, False, "f16", "gelu_tanh", gated, "own", True, "rows", True, 5)
+
+
+@pytest.mark.parametrize("n", [72, 1512])
 @pytest.mark.parametrize("s,e,k", [(40, 8, 4), (300, 64, 4), (1500, 3, 2)])
 @pytest.mark.parametrize("dtype", ["bf16", "f16"])
-def test_whole_numbers_are_exact(s, e, k, dtype):
+def test_whole_numbers_are_exact(s, e, k, n, dtype):
     """Products of small whole numbers have exact sums in any order: all forms agree bit for bit."""
-    announce("expert act integers", s, e, k, dtype)
+    announce("expert act integers", s, e, k, n, dtype)
     rng = np.random.default_rng(s)
-    m, n = 120, 72
+    m = 120
     idx = W.random_idx(rng, s, e, k)
     L = oracle.dispatch_layout(idx, e, 0)
     Lg = M.moe_dispatch_layout(to_dev(idx), e, 0)
@@ -264,8 +296,8 @@ def test_nan_and_inf_stay_where_they_are():
     also through the K tail and the rows a tile repeats."""
     announce("expert act nan")
     rng = np.random.default_rng(4)
-    for s, e, k in ((12, 8, 2), (700, 3, 2)):
-        m, n = 72, 136
+    m = 72
+    for s, e, k, n in ((12, 8, 2, 136), (700, 3, 2, 136), (700, 3, 2, 1608)):
         idx = W.random_idx(rng, s, e, k)
         idx[0], idx[1] = [0, 1], [1, 2]
         Lg = M.moe_dispatch_layout(to_dev(idx), e, 0)
@@ -350,11 +382,11 @@ def test_empty_batches():
         assert got[0].shape == pre.shape and not got[0].any() and not got[1].any() and got[2].shape == (0, 2) and not got[3].any()
 
 
-@pytest.mark.parametrize("s", [24, 900])
-def test_replays_from_a_graph_and_runs_beside_another_stream(s):
-    announce("expert act graph", s)
+@pytest.mark.parametrize("s,n", [(24, 104), (900, 104), (900, 1000)])
+def test_replays_from_a_graph_and_runs_beside_another_stream(s, n):
+    announce("expert act graph", s, n)
     rng = np.random.default_rng(6)
-    m, n, e, k = 136, 104, 8, 2
+    m, e, k = 136, 8, 2
     idx = to_dev(W.random_idx(rng, s, e, k))
     x, wts = to_dev(rand(rng, (s, m), "bf16"), "bf16"), to_dev(W.expert_weights(2, e, 2 * n, m, "bf16"), "bf16")
     bias, w = to_dev(rand(rng, (e, 2 * n), "bf16"), "bf16"), to_dev(W.random_weights(rng, s, k))
