@@ -574,10 +574,12 @@ moe_status_t moe_expert_gemm_act(const moe_layout_t* layout, const void* a, int3
   const size_t eb = elem_bytes(dtype);
   const size_t a_bytes = a_rows * m * eb, res_bytes = res_rows * n * eb;
   const size_t out_bytes = v.rows * n * eb, pre_bytes = static_cast<size_t>(v.rows) * nz * eb;
+  const size_t w_bytes = static_cast<size_t>(v.e) * nz * m * eb;
   if (overlap(out, out_bytes, a, a_bytes) || overlap(out, out_bytes, ep.residual, res_bytes) ||
       overlap(ep.preact, pre_bytes, a, a_bytes) || overlap(ep.preact, pre_bytes, ep.residual, res_bytes) ||
+      overlap(out, out_bytes, weights, w_bytes) || overlap(ep.preact, pre_bytes, weights, w_bytes) ||
       overlap(out, out_bytes, ep.preact, pre_bytes))
-    return fail(MOE_ERR_INVALID_ARG, "out and preact may not overlap each other, a or residual");
+    return fail(MOE_ERR_INVALID_ARG, "out and preact may not overlap each other, a, weights or residual");
   moe::ExpertAct p{};
   p.a = a;
   p.w = weights;
@@ -622,8 +624,10 @@ moe_status_t moe_expert_act_dgrad(const moe_layout_t* layout, const void* grad_p
   MOE_TRY(check_array(weights, v.s > 0 ? v.e : 0, "weights", true));
   MOE_TRY(check_array(grad_a, v.rows, "grad_a", true));
   const size_t eb = elem_bytes(dtype);
-  if (overlap(grad_a, static_cast<size_t>(v.rows) * m * eb, grad_preact, static_cast<size_t>(v.rows) * nz * eb))
-    return fail(MOE_ERR_INVALID_ARG, "grad_preact and grad_a may not overlap");
+  const size_t a_bytes = static_cast<size_t>(v.rows) * m * eb;
+  if (overlap(grad_a, a_bytes, grad_preact, static_cast<size_t>(v.rows) * nz * eb) ||
+      overlap(grad_a, a_bytes, weights, static_cast<size_t>(v.e) * nz * m * eb))
+    return fail(MOE_ERR_INVALID_ARG, "grad_a may not overlap grad_preact or weights");
   moe::ExpertAct p{};
   p.a = grad_preact;
   p.w = weights;

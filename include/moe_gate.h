@@ -391,7 +391,8 @@ moe_status_t moe_expert_gemm(const moe_layout_t* layout, const void* a, int32_t 
  *               rows no route fills are zero
  *   a, gather, weights [e, nz, m], m, n, dtype, out [rows, n]: as in moe_expert_gemm; m and n
  *   multiples of 8; every pointer to element rows and the bias 16-byte aligned. out and
- *   preact may not overlap each other, a or residual. A NULL epilogue means all defaults.
+ *   preact may not overlap each other, a, weights or residual. A NULL epilogue means all
+ *   defaults.
  * Sums are float32 (order unspecified, one order per sizes: the results are reproducible);
  * weights, activation and residual are float32 operations, each rounded.
  */
@@ -455,7 +456,7 @@ moe_status_t moe_expert_act_backward(const moe_layout_t* layout, const void* gra
  * for the placed rows r of expert x, rows no route fills zero: moe_expert_gemm_dgrad's
  * product on the tiles of moe_expert_gemm_act (whose heights follow the segments), summed in
  * another order. The gradient of gathered token rows is moe_dispatch_backward of grad_a.
- * Arguments as in moe_expert_gemm_dgrad, with n = nz.
+ * Arguments as in moe_expert_gemm_dgrad, with n = nz; grad_a may not overlap weights either.
  */
 moe_status_t moe_expert_act_dgrad(const moe_layout_t* layout, const void* grad_preact,
                                   const void* weights, int32_t m, int32_t nz, moe_dtype_t dtype,
@@ -523,7 +524,7 @@ moe_status_t moe_expert_gemm_wgrad(const moe_layout_t* layout, const void* a, in
  * loss and z float64, rounded once. A token whose logits are all -inf has no distribution:
  * it counts among the tokens, its routes are counted, and it adds 0 to probs and z. NaN or
  * +inf in an unpadded token's logits makes probs, loss and z of its group NaN, no other's.
- * One launch for a single group of up to 16384 logits, else two.
+ * One launch for a single group of up to 16384 logits and 1024 tokens, else two.
  */
 size_t moe_balance_workspace_bytes(int32_t s, int32_t e, int32_t g);
 moe_status_t moe_balance_loss(const float* logits, const int32_t* topk_idx,

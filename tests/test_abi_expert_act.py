@@ -51,6 +51,7 @@ def test_forward_argument_checks(lib):
     assert call(bias=at(3).value, bias_dtype=2) == 2  # f16 bias of bf16 weights
     assert call(bias=at(3, 4).value) == 5 and call(residual=at(4, 8).value) == 5 and call(preact=at(5, 8).value) == 5
     for clash in (dict(out=at(0, 256)), dict(residual=at(2, 64).value), dict(preact=at(2, 1024).value),
+                  dict(out=at(1, 64)), dict(preact=at(1, 65520).value),  # the last of the weights' 65536 bytes
                   dict(preact=at(0, 16).value), dict(preact=at(6).value, residual=at(6, 32).value)):
         assert call(**clash) == 1, clash
         assert "overlap" in lib.moe_last_error().decode()
@@ -92,7 +93,8 @@ def test_input_gradient_argument_checks(lib):
     assert call(dtype=0) == 2 and call(nz=4) == 5 and call(m=12) == 5 and call(m=0) == 1
     assert call(g=None) == 1 and call(w=None) == 1 and call(out=None) == 1
     assert call(out=at(2, 8)) == 5 and call(layout=M.LayoutStruct()) == 4
-    assert call(out=at(0, 512)) == 1 and "overlap" in lib.moe_last_error().decode()
+    for out in (at(0, 512), at(1, 65520)):
+        assert call(out=out) == 1 and "overlap" in lib.moe_last_error().decode()
 
 
 def test_binding_refuses_mismatched_tensors(monkeypatch):

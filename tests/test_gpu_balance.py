@@ -243,6 +243,38 @@ def test_replays_from_a_graph(s, e, groups):
         assert all(torch.equal(a, b) for a, b in zip(outs, want)), f"replay {rep}"
 
 
+def test_two_graphs_share_a_workspace():
+    """Replayed in turn on one stream, as two captured parts of one program are."""
+    announce("balance two graphs")
+    rng = np.random.default_rng(21)
+    parts, workspace = [], None
+    for s, e, groups in ((6000, 40, None), (3000, 72, [0, 100, 100, 3000])):
+        logits = torch.from_numpy(rng.standard_normal((s, e)).astype(np.float32)).cuda()
+        idx = torch.from_numpy(W.random_idx(rng, s, e, 3)).cuda()
+        gd = None if groups is None else torch.tensor(groups, dtype=torch.int32, device="cuda")
+        parts.append((logits, idx, gd))
+    need = [M.lib().moe_balance_workspace_bytes(p[0].shape[0], p[0].shape[1], 1 if p[2] is None else len(p[2]) - 1) for p in parts]
+    assert min(need) > 0
+    workspace = torch.full((max(need),), 0xA5, dtype=torch.uint8, device="cuda")
+    run = lambda p, ws: M.moe_balance_loss(p[0], p[1], groups=p[2], workspace=ws)  # noqa: E731
+    graphs, outs = [], []
+    for p in parts:
+        run(p, workspace)
+        torch.cuda.synchronize()
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            outs.append(run(p, workspace))
+    for rep in range(3):
+        for p in parts:
+            p[0].copy_(torch.from_numpy(rng.standard_normal(tuple(p[0].shape)).astype(np.float32)))
+        want = [run(p, None) for p in parts]
+        for g in (graphs if rep % 2 == 0 else graphs[::-1]):
+            g.replay()
+        torch.cuda.synchronize()
+        for o, v in zip(outs, want):
+            assert all(torch.equal(a, b) for a, b in zip(o, v)), f"replay {rep}"
+
+
 def test_autograd_gives_the_gradient():
     announce("balance autograd")
     rng = np.random.default_rng(10)

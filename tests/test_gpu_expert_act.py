@@ -555,6 +555,49 @@ def test_a_layer_of_all_the_pieces():
         assert abs(got - want) <= 5 * 2.0 ** -11 * 8 * size + 1e-4, (i, got, want, size)
 
 
+def test_a_captured_training_step_replays():
+    """Router, both losses, a gated and a weighted projection and their backward in one graph:
+    each replay gives the eager step's bits, also between eager steps on other leaves."""
+    announce("captured step")
+    rng = np.random.default_rng(31)
+    s, m, n, e, k = 300, 72, 136, 8, 2
+    data = [to_dev(t, "bf16" if t.dtype != np.float32 else None) for t in (
+        rng.standard_normal((s, e)).astype(np.float32), rand(rng, (s, m), "bf16"), W.expert_weights(1, e, 2 * n, m, "bf16"),
+        W.expert_weights(2, e, m, n, "bf16"), rand(rng, (e, m), "bf16"))]
+    gy = to_dev(rand(rng, (s, m), "bf16"), "bf16")
+
+    def step(values):
+        leaves = [t.detach().requires_grad_() for t in values]  # new leaves: none is shared with another graph
+        logits, x, up, down, bias = leaves
+        idx, w = A.route(logits, k)
+        loss, z, _ = A.balance_loss(logits, idx)
+        L, _ = A.layout(idx, e)
+        h = A.expert_linear(x, up, L, act="silu", gated=True)
+        y = A.combine(A.expert_linear(h, down, L, bias=bias, w=w, gather=False), None, L)
+        return (y.detach(), *torch.autograd.grad([y, loss.sum() + 0.5 * z.sum()], leaves, [gy, torch.ones((), device="cuda")]))
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step(data)
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        outs = step(data)
+    for rep in range(3):
+        data[0].copy_(torch.from_numpy(rng.standard_normal((s, e)).astype(np.float32)))
+        data[1].copy_(to_dev(rand(rng, (s, m), "bf16"), "bf16"))
+        want = [t.clone() for t in step(data)]
+        torch.cuda.synchronize()
+        for t in outs:
+            t.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        for i, (a, b) in enumerate(zip(outs, want)):
+            assert torch.equal(a, b), f"replay {rep}, output {i}"
+
+
 def test_refusals():
     announce("expert act refusals")
     idx = to_dev(W.random_idx(np.random.default_rng(1), 20, 4, 2))
@@ -566,6 +609,8 @@ def test_refusals():
     with pytest.raises(M.MoeError, match="overlap"):
         buf = torch.zeros((40, 64), dtype=torch.bfloat16, device="cuda")
         M.moe_expert_gemm_act(L, x, w, residual=buf, out=buf)
+    with pytest.raises(M.MoeError, match="overlap"):
+        M.moe_expert_gemm_act(L, x, w, out=w.view(-1, 64)[:40])
     with pytest.raises(M.MoeError, match="MISALIGNED"):
         M.moe_expert_gemm_act(L, x, torch.zeros((4, 60, 64), dtype=torch.bfloat16, device="cuda"))
     with pytest.raises(M.MoeError, match="MISALIGNED"):
