@@ -21,7 +21,8 @@
 namespace moe {
 
 constexpr int kBwdThreads = 256, kBwdWaves = kBwdThreads / kWave;
-constexpr int kBwdRows = 64;    // rows of a tile
+constexpr int kBwdRows = 64;    // most rows of a tile
+constexpr int64_t kBwdFewTiles = 512;  // under so many tiles of 64 rows they have 16
 constexpr int kBwdCols = 512;   // output features per workgroup
 constexpr int kBwdZero = 64;    // workgroups that clear rows no route fills
 
@@ -58,7 +59,7 @@ __device__ __forceinline__ void act_and_slope(float z, float* f, float* d) {
 
 template <int DT, int ACT, bool GATED>
 __global__ __launch_bounds__(kBwdThreads) void expert_act_backward_kernel(ExpertActBackward p, int col_blocks,
-                                                                          int tile_grid, float* __restrict__ bias_part,
+                                                                          int shift, int tile_grid, float* __restrict__ bias_part,
                                                                           double* __restrict__ dot_part) {
   constexpr int H = GATED ? 2 : 1;  // halves of z
   __shared__ float row_w[kBwdRows];
@@ -86,12 +87,12 @@ __global__ __launch_bounds__(kBwdThreads) void expert_act_backward_kernel(Expert
     return;
   }
   const SegmentTile tc =
-      segment_tile(blockIdx.x, p.e, p.kept, p.offsets, col_blocks, 8, [](int r) { return (r + kBwdRows - 1) / kBwdRows; });
+      segment_tile(blockIdx.x, p.e, p.kept, p.offsets, col_blocks, 8, [shift](int r) { return (r + (1 << shift) - 1) >> shift; });
   const int x = tc.expert;
   if (x < 0) return;
-  const int row0 = tc.offset + tc.rb * kBwdRows;
-  const int rem = tc.rows - tc.rb * kBwdRows;
-  const int nrows = rem < kBwdRows ? rem : kBwdRows;
+  const int row0 = tc.offset + (tc.rb << shift);
+  const int rem = tc.rows - (tc.rb << shift);
+  const int nrows = rem < 1 << shift ? rem : 1 << shift;
   const int c = tc.cb * kBwdCols + 8 * lane;
   const bool in = c < p.n;
   if (p.route_w != nullptr) {
@@ -173,9 +174,9 @@ __global__ __launch_bounds__(kBwdThreads) void expert_act_backward_kernel(Expert
     }
   }
   if (p.grad_bias == nullptr) return;
-  // Tile rb of expert x owns partial row offsets[x] / kBwdRows + x + rb: as floor(a + b) >=
+  // Tile rb of expert x owns partial row (offsets[x] >> shift) + x + rb: as floor(a + b) >=
   // floor(a) + ceil(b) - 1, the next expert's first is past this one's last.
-  const size_t slot = static_cast<size_t>(tc.offset / kBwdRows) + x + tc.rb;
+  const size_t slot = static_cast<size_t>(tc.offset >> shift) + x + tc.rb;
 #pragma unroll
   for (int h = 0; h < H; ++h) {
     __syncthreads();
@@ -198,7 +199,7 @@ __global__ __launch_bounds__(kBwdThreads) void expert_act_backward_kernel(Expert
 // lanes of four by 16 partial rows at a time, summed in float64, then in order. The others
 // take a route per thread.
 template <int DT>
-__global__ __launch_bounds__(kBwdThreads) void expert_act_backward_sums_kernel(ExpertActBackward p, int col_blocks,
+__global__ __launch_bounds__(kBwdThreads) void expert_act_backward_sums_kernel(ExpertActBackward p, int col_blocks, int shift,
                                                                                int bias_blocks, int64_t bias_grid,
                                                                                const float* __restrict__ bias_part,
                                                                                const double* __restrict__ dot_part) {
@@ -206,8 +207,8 @@ __global__ __launch_bounds__(kBwdThreads) void expert_act_backward_sums_kernel(E
   const int tid = threadIdx.x;
   if (static_cast<int64_t>(blockIdx.x) < bias_grid) {
     const int x = blockIdx.x / bias_blocks, c0 = blockIdx.x % bias_blocks * 64;
-    const int tiles = (p.kept[x] + kBwdRows - 1) / kBwdRows;
-    const size_t slot = static_cast<size_t>(p.offsets[x] / kBwdRows) + x;
+    const int tiles = (p.kept[x] + (1 << shift) - 1) >> shift;
+    const size_t slot = static_cast<size_t>(p.offsets[x] >> shift) + x;
     const int c = c0 + 4 * (tid % 16);
     double s[4] = {0.0, 0.0, 0.0, 0.0};
     if (c < p.nz) {  // nz is a multiple of 8
@@ -243,10 +244,14 @@ ExpertActBackwardPlan expert_act_backward_plan(const LayoutView& L, int n, bool 
   ExpertActBackwardPlan p{};
   const int nz = gated ? 2 * n : n;
   p.col_blocks = (n + kBwdCols - 1) / kBwdCols;
-  p.slots = L.rows / kBwdRows + L.e + 1;
   const int64_t routes = static_cast<int64_t>(L.s) * L.k;
   const int64_t placed = routes < L.rows ? routes : L.rows;
-  const int64_t tiles = L.s == 0 ? 0 : (placed / kBwdRows + (placed < L.e ? placed : L.e)) * p.col_blocks;
+  auto tiles_of = [&](int shift) {
+    return L.s == 0 ? 0 : ((placed >> shift) + (placed < L.e ? placed : L.e)) * p.col_blocks;
+  };
+  p.shift = tiles_of(6) < kBwdFewTiles ? 4 : 6;
+  const int64_t tiles = tiles_of(p.shift);
+  p.slots = (L.rows >> p.shift) + L.e + 1;
   p.grid = (tiles + kXcds - 1) / kXcds * kXcds;
   p.off_bias = 0;
   p.off_dots = (static_cast<size_t>(p.slots) * nz * 4 + 255) / 256 * 256;
@@ -260,10 +265,10 @@ static void launch_first(const ExpertActBackward& p, const ExpertActBackwardPlan
   const unsigned grid = static_cast<unsigned>(plan.grid + kBwdZero);
   const int tile_grid = static_cast<int>(plan.grid);
   if (p.gated)
-    expert_act_backward_kernel<DT, ACT, true><<<grid, kBwdThreads, 0, stream>>>(p, plan.col_blocks, tile_grid, bias_part,
+    expert_act_backward_kernel<DT, ACT, true><<<grid, kBwdThreads, 0, stream>>>(p, plan.col_blocks, plan.shift, tile_grid, bias_part,
                                                                              dot_part);
   else
-    expert_act_backward_kernel<DT, ACT, false><<<grid, kBwdThreads, 0, stream>>>(p, plan.col_blocks, tile_grid,
+    expert_act_backward_kernel<DT, ACT, false><<<grid, kBwdThreads, 0, stream>>>(p, plan.col_blocks, plan.shift, tile_grid,
                                                                               bias_part, dot_part);
 }
 
@@ -287,7 +292,7 @@ static hipError_t launch_dt(const ExpertActBackward& p, const ExpertActBackwardP
   const int64_t grid = bias_grid + (p.grad_w != nullptr ? (routes + kBwdThreads - 1) / kBwdThreads : 0);
   if (grid == 0) return hipSuccess;
   expert_act_backward_sums_kernel<DT><<<static_cast<unsigned>(grid), kBwdThreads, 0, stream>>>(
-      p, plan.col_blocks, bias_blocks, bias_grid, bias_part, dot_part);
+      p, plan.col_blocks, plan.shift, bias_blocks, bias_grid, bias_part, dot_part);
   return hipGetLastError();
 }
 

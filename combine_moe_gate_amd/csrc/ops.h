@@ -81,6 +81,7 @@ struct ExpertActBackward {
 // The workspace: a partial bias row per row tile, a partial dot per row and column block.
 struct ExpertActBackwardPlan {
   int32_t col_blocks;
+  int32_t shift;  // a tile has 1 << shift rows
   int64_t slots, grid;
   size_t off_bias, off_dots, bytes;
 };
