@@ -27,6 +27,10 @@ routing it was built from. A layout replayed for routing that did not come from
 the recorder's gate is verified on the GPU against the recorded routing, and the
 backward of that dispatch raises if they differ: a mis-route fails loudly
 instead of silently. A recompute that outruns its log builds afresh.
+
+To capture a backward pass into a HIP graph, give it leaves that no live eager graph shares
+(`t.detach().requires_grad_()`): for a shared leaf autograd waits on the eager graph's stream
+inside the capture, which can end the process.
 """
 from __future__ import annotations
 
