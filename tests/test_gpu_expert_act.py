@@ -197,6 +197,8 @@ CASES = [
     (4000, 72, 136, 4, 2, 600, 1, False, "bf16", "none", True, "own", True, "tokens", False),
     (700, 8, 520, 2, 1, 0, 1, False, "bf16", "gelu", False, None, True, None, True),     # one K chunk
     (900, 128, 8, 3, 3, 0, 1, False, "f16", "silu", True, "own", False, "rows", True),   # one column chunk
+    (20, 136, 72, 1024, 4, 0, 1, False, "bf16", "silu", True, "own", True, "tokens", True),  # few of many experts
+    (20, 72, 264, 700, 8, 3, 1, False, "f16", "gelu", False, "f32", True, "rows", False),    # capacity, mostly empty
 ]
 
 
@@ -449,6 +451,29 @@ def test_more_values_than_32_bits_count():
     dots = (g * z * sg).sum(1)
     last = (L.dst.flatten()[:, None] == torch.arange(L.rows - 50, L.rows, device="cuda")).int().argmax(0)
     assert ((gw.flatten()[last].double() - dots).abs() <= 1e-5 * (g * z * sg).abs().sum(1)).all()
+
+
+@pytest.mark.parametrize("s", [4, 300])
+def test_weights_past_4_gib(s):
+    """Both ends of 4.8 GB of weights, forward and input gradient."""
+    announce("expert act weights past 4 GiB", s)
+    e, n, m = 36, 8192, 8192
+    wts = torch.zeros((e, n, m), dtype=torch.bfloat16, device="cuda")
+    gen = torch.Generator("cuda").manual_seed(8)
+    for x in (0, e - 1):
+        wts[x] = (torch.randn((n, m), generator=gen, device="cuda") / 8).to(torch.bfloat16)
+    idx = torch.where(torch.arange(s, device="cuda") % 2 == 0, 0, e - 1).int()[:, None].contiguous()
+    L = M.moe_dispatch_layout(idx, e, 0)
+    a = torch.randn((s, m), generator=gen, device="cuda").to(torch.bfloat16)
+    out = M.moe_expert_gemm_act(L, a, wts, act="relu")
+    g = torch.randn((s, n), generator=gen, device="cuda").to(torch.bfloat16)
+    ga = M.moe_expert_act_dgrad(L, g, wts)
+    for x, rows in ((0, slice(0, (s + 1) // 2)), (e - 1, slice((s + 1) // 2, s))):
+        w64, a64, g64 = wts[x].double(), a[L.src[rows].long()].double(), g[rows].double()
+        want, mag = (a64 @ w64.t()).clamp(min=0), a64.abs() @ w64.t().abs()
+        assert ((out[rows].double() - want).abs() <= 2.0 ** -8 * want.abs() + (m + 3) * 2 * U * mag).all()
+        want, mag = g64 @ w64, g64.abs() @ w64.abs()
+        assert ((ga[rows].double() - want).abs() <= 2.0 ** -8 * want.abs() + (n + 3) * 2 * U * mag).all()
 
 
 GRADS = [("silu", True, True, False, "own", None, "bf16"), ("gelu", False, False, True, "f32", "rows", "bf16"),
