@@ -24,8 +24,7 @@
 // For a gated projection a wave's 64 weight rows are 32 gate rows and the 32 up rows that
 // meet them, so both products of an output are in one wave. The finished sums leave through
 // a piece of LDS of the wave's own, 16 rows at a time, and come back as eight consecutive
-// features per lane: bias, residual and results then move as 16-byte pieces, and the
-// epilogue's code exists once whatever the tile's height.
+// features per lane: bias, residual and results then move as 16-byte pieces.
 //
 // Few rows (decoding; bound by reading the weights). A workgroup of four waves multiplies
 // up to 16 F rows by 16 FB weight rows, each wave a quarter of the K steps: weights go from
@@ -34,7 +33,9 @@
 //
 // The input-row gradient runs the tiles on the same weights, which are [K][N] to it: pieces
 // of 64 K rows by 256 features are staged as they lie and read through LDS's transposing
-// reads, and a tile has at most 256 rows (nine units would spill).
+// reads, and a tile has at most 256 rows (nine units would spill). 49152 rows of 64 experts
+// from 2816 to 2048 features take 600 us, from 2048 to 1408 370; moe_expert_gemm_dgrad's
+// kernel, with tiles of a fixed 256 rows, 738 and 503.
 //
 // Measured (bf16, random routing): 65536 rows of 128 experts by 4096 x 4096 (gated, 2.2
 // TFLOP) with bias and kept pre-activations 2.1 ms, 1040 TFLOP/s; one dense expert 1250

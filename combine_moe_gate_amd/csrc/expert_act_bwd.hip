@@ -6,7 +6,7 @@
 //     grad_b[x] = sum_r grad_z[r],   grad_w(route at r) = <grad_out[r], u(z[r])>
 // The products' own gradients are grouped GEMMs of grad_z and need nothing from here.
 //
-// One pass over grad_out and z, bound by its traffic. A workgroup takes up to kBwdRows rows
+// One pass over grad_out and z, bound by its traffic. A workgroup takes 64 rows (16 of few)
 // of one expert by 512 output features: a wave a row at a time, a lane eight features as
 // 16-byte pieces (gated: of both halves), so the bias sums of its features stay in a lane's
 // registers over the rows. The waves' sums meet in LDS in order and go out as one partial
@@ -22,7 +22,11 @@ namespace moe {
 
 constexpr int kBwdThreads = 256, kBwdWaves = kBwdThreads / kWave;
 constexpr int kBwdRows = 64;    // most rows of a tile
-constexpr int64_t kBwdFewTiles = 512;  // under so many tiles of 64 rows they have 16
+// Under so many tiles of 64 rows (two per CU) tiles have 16. Microseconds with 16 and with 64,
+// by tiles of 64: 16 experts, 264 gated features: 47 tiles 9.3 and 16.0, 266 18.5 and 23.8, 516
+// 31.2 and 25.7, 1016 47.9 and 38.1; 128 experts, 512 features: 253 11.7 and 15.0, 628 29.2
+// and 26.8; 8 experts, 4096 gated features: 312 22.5 and 25.3, 1064 76.4 and 72.8.
+constexpr int64_t kBwdFewTiles = 512;
 constexpr int kBwdCols = 512;   // output features per workgroup
 constexpr int kBwdZero = 64;    // workgroups that clear rows no route fills
 
