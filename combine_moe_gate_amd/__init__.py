@@ -120,10 +120,14 @@ _SIGNATURES = {
     "moe_layout_read": (ctypes.c_int, [ctypes.POINTER(LayoutStruct), _P, _P, _P]),
     "moe_expert_gemm_act": (ctypes.c_int, [ctypes.POINTER(LayoutStruct), _P, _I, _P, _I, _I, ctypes.c_int,
                                            ctypes.POINTER(Epilogue), _P, _P]),
+    "moe_expert_gemm_act_ex": (ctypes.c_int, [ctypes.POINTER(LayoutStruct), _P, _I, _P, _I, _I, ctypes.c_int,
+                                              ctypes.POINTER(Epilogue), ctypes.c_int, _P, _P]),
     "moe_expert_act_dgrad": (ctypes.c_int, [ctypes.POINTER(LayoutStruct), _P, _P, _I, _I, ctypes.c_int, _P, _P]),
     "moe_expert_act_backward_workspace_bytes": (ctypes.c_size_t, [ctypes.POINTER(LayoutStruct), _I, _I]),
     "moe_expert_act_backward": (ctypes.c_int, [ctypes.POINTER(LayoutStruct), _P, _P, _I, ctypes.c_int, _I, _I, _P, _P,
                                                ctypes.c_int, _P, _P, _P, _P, ctypes.c_size_t, _P]),
+    "moe_expert_act_backward_ex": (ctypes.c_int, [ctypes.POINTER(LayoutStruct), _P, _P, ctypes.c_int, _I, ctypes.c_int,
+                                                  _I, _I, _P, _P, ctypes.c_int, _P, _P, _P, _P, ctypes.c_size_t, _P]),
     "moe_balance_workspace_bytes": (ctypes.c_size_t, [_I, _I, _I]),
     "moe_balance_loss": (ctypes.c_int, [_P, _P, _P, _P, _I, _I, _I, _I, _P, _P, _P, _P, _P, _P, ctypes.c_size_t,
                                         _P]),
@@ -507,7 +511,7 @@ _GEMM_DTYPES = (torch.bfloat16, torch.float16)
 
 def moe_expert_gemm_act(layout: Layout, a: torch.Tensor, weights: torch.Tensor, gather: bool = True, bias=None,
                         act: str = "none", gated: bool = False, w=None, residual=None, residual_gather: bool = False,
-                        save_preact: bool = False, out=None, preact=None):
+                        save_preact: bool = False, out=None, preact=None, preact_dtype=None):
     """Grouped expert product with an epilogue: for each placed row r of expert x, with
     z = A(r) @ weights[x]^T + bias[x],
         out[r] = w_r u + res(r),   u = act(z), or gated: u = act(z[:n]) * z[n:]
@@ -517,8 +521,9 @@ def moe_expert_gemm_act(layout: Layout, a: torch.Tensor, weights: torch.Tensor, 
     rows first. bias [e, weight rows] float32 or a's dtype; act none, relu, gelu (exact),
     gelu_tanh or silu; w [s, k] float32 scales a row by its route's weight; residual [rows,
     n], or token rows [s, n] with residual_gather, is added last. With save_preact (or
-    preact given) returns (out, preact): z rounded, [rows, weight rows], for
-    moe_expert_act_backward.
+    preact given) returns (out, preact): z, [rows, weight rows], for moe_expert_act_backward,
+    in preact_dtype: a's dtype (None, or preact's: z rounded) or float32 (twice the memory, the
+    gradient of the z the forward used).
     """
     _expect(a, "a", (layout.s if gather else layout.rows, None), _GEMM_DTYPES)
     m = a.shape[1]
@@ -532,18 +537,22 @@ def moe_expert_gemm_act(layout: Layout, a: torch.Tensor, weights: torch.Tensor, 
     _expect(w, "w", (layout.s, layout.k), torch.float32)
     _expect(residual, "residual", (layout.s if residual_gather else layout.rows, n), a.dtype)
     _expect(out, "out", (layout.rows, n), a.dtype)
-    _expect(preact, "preact", (layout.rows, nz), a.dtype)
+    if preact_dtype is None:
+        preact_dtype = a.dtype if preact is None else (a.dtype, torch.float32)
+    elif preact_dtype not in (a.dtype, torch.float32):
+        raise ValueError(f"preact_dtype must be float32 or {a.dtype}, got {preact_dtype}")
+    _expect(preact, "preact", (layout.rows, nz), preact_dtype)
     _same_device(layout, a, weights, bias, w, residual, out, preact)
     if out is None:
         out = torch.empty((layout.rows, n), dtype=a.dtype, device=a.device)
     if save_preact and preact is None:
-        preact = torch.empty((layout.rows, nz), dtype=a.dtype, device=a.device)
+        preact = torch.empty((layout.rows, nz), dtype=preact_dtype, device=a.device)
     ep = Epilogue(code, int(bool(gated)), bias.data_ptr() if bias is not None else None,
                   _DTYPE_CODE[bias.dtype] if bias is not None else MOE_F32, int(bool(residual_gather)),
                   w.data_ptr() if w is not None else None, residual.data_ptr() if residual is not None else None,
                   preact.data_ptr() if preact is not None else None)
-    _launch(a, lib().moe_expert_gemm_act, layout.byref(), _ptr(a), int(bool(gather)), _ptr(weights), m, n,
-            _DTYPE_CODE[a.dtype], ctypes.byref(ep), _ptr(out))
+    _launch(a, lib().moe_expert_gemm_act_ex, layout.byref(), _ptr(a), int(bool(gather)), _ptr(weights), m, n,
+            _DTYPE_CODE[a.dtype], ctypes.byref(ep), _DTYPE_CODE[a.dtype if preact is None else preact.dtype], _ptr(out))
     return out if preact is None else (out, preact)
 
 
@@ -553,8 +562,8 @@ def moe_expert_act_backward(layout: Layout, grad_out: torch.Tensor, preact=None,
     """Backward of moe_expert_gemm_act's epilogue: (grad_preact, grad_bias, grad_w,
     grad_residual), None where not asked for.
 
-    grad_out [rows, n]; preact as the forward kept it (not needed for act none, not gated,
-    without need_w). grad_preact [rows, weight rows]; grad_bias [e, weight rows] of
+    grad_out [rows, n]; preact as the forward kept it, in grad_out's dtype or float32 (not
+    needed for act none, not gated, without need_w). grad_preact [rows, weight rows]; grad_bias [e, weight rows] of
     bias_dtype (float32 or grad_out's dtype; None: not wanted); grad_w [s, k] float32 (needs
     w); grad_residual [rows, n], for a residual of buffer rows. The gradients of a and
     weights are moe_expert_act_dgrad and moe_expert_gemm_wgrad of grad_preact.
@@ -570,7 +579,7 @@ def moe_expert_act_backward(layout: Layout, grad_out: torch.Tensor, preact=None,
         raise ValueError("need_w: w is required")
     if preact is None and (code != 0 or gated or need_w):
         raise ValueError("preact is required (the values the forward kept)")
-    _expect(preact, "preact", (layout.rows, nz), dt)
+    _expect(preact, "preact", (layout.rows, nz), (dt, torch.float32))
     _expect(workspace, "workspace", (None,), torch.uint8)
     _same_device(layout, grad_out, preact, w, workspace)
     dev = grad_out.device
@@ -581,9 +590,9 @@ def moe_expert_act_backward(layout: Layout, grad_out: torch.Tensor, preact=None,
     if workspace is None and (gb is not None or gw is not None):
         workspace = torch.empty(lib().moe_expert_act_backward_workspace_bytes(layout.byref(), n, int(bool(gated))),
                                 dtype=torch.uint8, device=dev)
-    _launch(grad_out, lib().moe_expert_act_backward, layout.byref(), _ptr(grad_out), _ptr(preact), n, _DTYPE_CODE[dt],
-            code, int(bool(gated)), _ptr(w), _ptr(gz), _DTYPE_CODE[bias_dtype] if gb is not None else MOE_F32, _ptr(gb),
-            _ptr(gw), _ptr(gr), _ptr(workspace), workspace.numel() if workspace is not None else 0)
+    _launch(grad_out, lib().moe_expert_act_backward_ex, layout.byref(), _ptr(grad_out), _ptr(preact),
+            _DTYPE_CODE[dt if preact is None else preact.dtype], n, _DTYPE_CODE[dt], code, int(bool(gated)), _ptr(w), _ptr(gz),
+            _DTYPE_CODE[bias_dtype] if gb is not None else MOE_F32, _ptr(gb), _ptr(gw), _ptr(gr), _ptr(workspace), workspace.numel() if workspace is not None else 0)
     return gz, gb, gw, gr
 
 

@@ -224,13 +224,14 @@ class _ExpertAct(torch.autograd.Function):
     """One projection per expert with its epilogue; a gathered from token rows or a buffer."""
 
     @staticmethod
-    def forward(ctx, a, weights, bias, w, residual, layout, act, gated, gather, residual_gather):
+    def forward(ctx, a, weights, bias, w, residual, layout, act, gated, gather, residual_gather, preact_dtype):
         a, weights = a.contiguous(), weights.contiguous()
         bias, w, residual = (None if t is None else t.contiguous() for t in (bias, w, residual))
         bent = act != "none" or gated
         keep = (bent and any(ctx.needs_input_grad[:4])) or (w is not None and ctx.needs_input_grad[3])
         got = moe_expert_gemm_act(layout, a, weights, gather=gather, bias=bias, act=act, gated=gated, w=w,
-                                  residual=residual, residual_gather=residual_gather, save_preact=keep)
+                                  residual=residual, residual_gather=residual_gather, save_preact=keep,
+                                  preact_dtype=preact_dtype)
         out, preact = got if keep else (got, None)
         ctx.save_for_backward(a, weights, w, preact)
         ctx.layout, ctx.act, ctx.gated, ctx.bent = layout, act, gated, bent
@@ -261,7 +262,7 @@ class _ExpertAct(torch.autograd.Function):
             g_weights = moe_expert_gemm_wgrad(L, a, g_z, gather=ctx.gather, out_dtype=weights.dtype)
         if need_res and ctx.residual_gather:
             g_res = moe_dispatch_backward(L, g_out)
-        return g_a, g_weights, g_bias, g_w, g_res, None, None, None, None, None
+        return g_a, g_weights, g_bias, g_w, g_res, None, None, None, None, None, None
 
 
 class LayoutRecorder:
@@ -411,7 +412,8 @@ def combine(expert_out: torch.Tensor, w: torch.Tensor | None, layout: Layout):
 
 def expert_linear(x: torch.Tensor, weights: torch.Tensor, layout: Layout, bias: torch.Tensor | None = None,
                   act: str = "none", gated: bool = False, w: torch.Tensor | None = None,
-                  residual: torch.Tensor | None = None, residual_gather: bool = False, gather: bool = True):
+                  residual: torch.Tensor | None = None, residual_gather: bool = False, gather: bool = True,
+                  preact_dtype: torch.dtype | None = None):
     """Each placed row r of expert x: x[src[r]] @ weights[x]^T, the dispatch fused into the
     grouped GEMM's operand loads (forward, input-row gradient and weight gradient all run
     on the layout). weights [e, n, m]; returns [rows, n] for combine().
@@ -420,10 +422,14 @@ def expert_linear(x: torch.Tensor, weights: torch.Tensor, layout: Layout, bias: 
     u = act(z), or, gated, act(z[:n]) * z[n:] with weights [e, 2n, m]: act none, relu, gelu,
     gelu_tanh or silu, w [s, k] the route weights, residual a row for each buffer row or,
     with residual_gather, for each token. gather=False takes x as a buffer [rows, m] (the
-    rows an earlier projection left). Gradients reach x, weights, bias, w and residual."""
+    rows an earlier projection left). Gradients reach x, weights, bias, w and residual.
+
+    The backward starts from the z that the forward kept: rounded to x's dtype, or with
+    preact_dtype=torch.float32 as it was, in twice the memory. Its own gradient is rounded to
+    x's dtype once, before the products that lead to x and weights (what matrix cores take)."""
     if gather and bias is None and act == "none" and not gated and w is None and residual is None:
         return _ExpertLinear.apply(x, weights, layout)
-    return _ExpertAct.apply(x, weights, bias, w, residual, layout, act, gated, gather, residual_gather)
+    return _ExpertAct.apply(x, weights, bias, w, residual, layout, act, gated, gather, residual_gather, preact_dtype)
 
 
 def renormalize(w: torch.Tensor, layout: Layout):

@@ -535,9 +535,9 @@ static moe_status_t check_act(int32_t activation, int32_t gated, int32_t n) {
   return MOE_OK;
 }
 
-static moe_status_t check_bias_dtype(int32_t bias_dtype, moe_dtype_t dtype) {
-  if (bias_dtype != MOE_F32 && bias_dtype != dtype)
-    return fail(MOE_ERR_UNSUPPORTED, "bias_dtype must be float32 or dtype (got %d, dtype %d)", bias_dtype,
+static moe_status_t check_wide(const char* name, int32_t type, moe_dtype_t dtype) {
+  if (type != MOE_F32 && type != dtype)
+    return fail(MOE_ERR_UNSUPPORTED, "%s must be float32 or dtype (got %d, dtype %d)", name, type,
                 static_cast<int>(dtype));
   return MOE_OK;
 }
@@ -545,6 +545,13 @@ static moe_status_t check_bias_dtype(int32_t bias_dtype, moe_dtype_t dtype) {
 moe_status_t moe_expert_gemm_act(const moe_layout_t* layout, const void* a, int32_t gather,
                                  const void* weights, int32_t m, int32_t n, moe_dtype_t dtype,
                                  const moe_expert_epilogue_t* epilogue, void* out, void* stream) {
+  return moe_expert_gemm_act_ex(layout, a, gather, weights, m, n, dtype, epilogue, dtype, out, stream);
+}
+
+moe_status_t moe_expert_gemm_act_ex(const moe_layout_t* layout, const void* a, int32_t gather,
+                                    const void* weights, int32_t m, int32_t n, moe_dtype_t dtype,
+                                    const moe_expert_epilogue_t* epilogue, moe_dtype_t preact_dtype,
+                                    void* out, void* stream) {
   moe::LayoutView v;
   MOE_TRY(view_of(layout, &v));
   if (dtype != MOE_BF16 && dtype != MOE_F16)
@@ -558,7 +565,8 @@ moe_status_t moe_expert_gemm_act(const moe_layout_t* layout, const void* a, int3
   MOE_TRY(check_rows(m, dtype, &rc_in));
   MOE_TRY(check_rows(n, dtype, &rc_out));
   MOE_TRY(check_act(ep.activation, ep.gated, n));
-  if (ep.bias != nullptr) MOE_TRY(check_bias_dtype(ep.bias_dtype, dtype));
+  if (ep.bias != nullptr) MOE_TRY(check_wide("bias_dtype", ep.bias_dtype, dtype));
+  if (ep.preact != nullptr) MOE_TRY(check_wide("preact_dtype", preact_dtype, dtype));
   if (ep.residual_gather != 0 && ep.residual_gather != 1)
     return fail(MOE_ERR_INVALID_ARG, "residual_gather must be 0 or 1 (got %d)", ep.residual_gather);
   const int32_t nz = ep.gated ? 2 * n : n;
@@ -573,7 +581,7 @@ moe_status_t moe_expert_gemm_act(const moe_layout_t* layout, const void* a, int3
   if (ep.preact != nullptr) MOE_TRY(check_array(ep.preact, 1, "preact", true));
   const size_t eb = elem_bytes(dtype);
   const size_t a_bytes = a_rows * m * eb, res_bytes = res_rows * n * eb;
-  const size_t out_bytes = v.rows * n * eb, pre_bytes = static_cast<size_t>(v.rows) * nz * eb;
+  const size_t out_bytes = v.rows * n * eb, pre_bytes = static_cast<size_t>(v.rows) * nz * elem_bytes(preact_dtype);
   const size_t w_bytes = static_cast<size_t>(v.e) * nz * m * eb;
   if (overlap(out, out_bytes, a, a_bytes) || overlap(out, out_bytes, ep.residual, res_bytes) ||
       overlap(ep.preact, pre_bytes, a, a_bytes) || overlap(ep.preact, pre_bytes, ep.residual, res_bytes) ||
@@ -603,6 +611,7 @@ moe_status_t moe_expert_gemm_act(const moe_layout_t* layout, const void* a, int3
   p.gated = ep.gated != 0;
   p.bias_f32 = ep.bias_dtype == MOE_F32;
   p.residual_gather = ep.residual_gather != 0;
+  p.preact_f32 = preact_dtype == MOE_F32;
   return hip_status(moe::launch_expert_act(v, p, static_cast<int>(dtype), static_cast<hipStream_t>(stream)),
                     "moe_expert_gemm_act");
 }
@@ -662,6 +671,17 @@ moe_status_t moe_expert_act_backward(const moe_layout_t* layout, const void* gra
                                      void* grad_preact, moe_dtype_t bias_dtype, void* grad_bias,
                                      float* grad_topk_w, void* grad_residual, void* workspace,
                                      size_t workspace_bytes, void* stream) {
+  return moe_expert_act_backward_ex(layout, grad_out, preact, dtype, n, dtype, activation, gated, topk_w, grad_preact,
+                                    bias_dtype, grad_bias, grad_topk_w, grad_residual, workspace, workspace_bytes,
+                                    stream);
+}
+
+moe_status_t moe_expert_act_backward_ex(const moe_layout_t* layout, const void* grad_out,
+                                        const void* preact, moe_dtype_t preact_dtype, int32_t n,
+                                        moe_dtype_t dtype, int32_t activation, int32_t gated,
+                                        const float* topk_w, void* grad_preact, moe_dtype_t bias_dtype,
+                                        void* grad_bias, float* grad_topk_w, void* grad_residual,
+                                        void* workspace, size_t workspace_bytes, void* stream) {
   moe::LayoutView v;
   MOE_TRY(view_of(layout, &v));
   if (dtype != MOE_BF16 && dtype != MOE_F16)
@@ -670,10 +690,11 @@ moe_status_t moe_expert_act_backward(const moe_layout_t* layout, const void* gra
   int64_t rc = 0;
   MOE_TRY(check_rows(n, dtype, &rc));
   MOE_TRY(check_act(activation, gated, n));
-  if (grad_bias != nullptr) MOE_TRY(check_bias_dtype(bias_dtype, dtype));
+  if (grad_bias != nullptr) MOE_TRY(check_wide("bias_dtype", bias_dtype, dtype));
   if (grad_topk_w != nullptr && topk_w == nullptr && v.s > 0)
     return fail(MOE_ERR_INVALID_ARG, "grad_topk_w needs topk_w");
   const bool needs_z = activation != MOE_ACT_NONE || gated != 0 || grad_topk_w != nullptr;
+  if (needs_z) MOE_TRY(check_wide("preact_dtype", preact_dtype, dtype));
   const int64_t rows = v.s > 0 ? v.rows : 0;
   MOE_TRY(check_array(grad_out, rows, "grad_out", true));
   if (needs_z) MOE_TRY(check_array(preact, rows, "preact", true));
@@ -693,10 +714,11 @@ moe_status_t moe_expert_act_backward(const moe_layout_t* layout, const void* gra
                   plan.bytes);
   }
   const size_t eb = elem_bytes(dtype);
-  const size_t n_bytes = v.rows * n * eb, z_bytes = static_cast<size_t>(v.rows) * nz * eb;
-  if (overlap(grad_preact, z_bytes, grad_out, n_bytes) || overlap(grad_preact, z_bytes, preact, z_bytes) ||
+  const size_t n_bytes = v.rows * n * eb, gz_bytes = static_cast<size_t>(v.rows) * nz * eb;
+  const size_t z_bytes = static_cast<size_t>(v.rows) * nz * elem_bytes(preact_dtype);
+  if (overlap(grad_preact, gz_bytes, grad_out, n_bytes) || overlap(grad_preact, gz_bytes, preact, z_bytes) ||
       overlap(grad_residual, n_bytes, grad_out, n_bytes) || overlap(grad_residual, n_bytes, preact, z_bytes) ||
-      overlap(grad_preact, z_bytes, grad_residual, n_bytes))
+      overlap(grad_preact, gz_bytes, grad_residual, n_bytes))
     return fail(MOE_ERR_INVALID_ARG, "grad_preact and grad_residual may not overlap each other, grad_out or preact");
   moe::ExpertActBackward p{};
   p.grad_out = grad_out;
@@ -719,6 +741,7 @@ moe_status_t moe_expert_act_backward(const moe_layout_t* layout, const void* gra
   p.rows = v.rows;
   p.gated = gated != 0;
   p.bias_f32 = bias_dtype == MOE_F32;
+  p.preact_f32 = needs_z && preact_dtype == MOE_F32;
   return hip_status(moe::launch_expert_act_backward(v, p, plan, static_cast<char*>(workspace), static_cast<int>(dtype),
                                                     static_cast<hipStream_t>(stream)),
                     "moe_expert_act_backward");

@@ -63,6 +63,20 @@ __device__ __forceinline__ void load8(const void* p, size_t at, bool f32, float 
   }
 }
 
+// Eight elements of a row of kept values: float32, or rounded to the element type.
+template <int DT>
+__device__ __forceinline__ void store8(void* p, size_t at, bool f32, const float (&f)[8]) {
+  if (f32) {
+    chunk_t* q = reinterpret_cast<chunk_t*>(static_cast<float*>(p) + at);
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+      q[h] = chunk_t{__float_as_uint(f[4 * h]), __float_as_uint(f[4 * h + 1]), __float_as_uint(f[4 * h + 2]),
+                     __float_as_uint(f[4 * h + 3])};
+  } else {
+    *reinterpret_cast<chunk_t*>(static_cast<uint16_t*>(p) + at) = pack<DT>(f);
+  }
+}
+
 // The route weight of buffer row r (token t): that of the route placed there.
 __device__ __forceinline__ float route_weight(const ExpertAct& p, int r, int t) {
   float w = 1.0f;
@@ -89,9 +103,9 @@ __device__ __forceinline__ void finish8(const ExpertAct& p, int x, int r, int t,
     }
   }
   if (p.preact != nullptr) {
-    uint16_t* row = static_cast<uint16_t*>(p.preact) + static_cast<size_t>(r) * p.nz + c;
-    *reinterpret_cast<chunk_t*>(row) = pack<DT>(v);
-    if (p.gated) *reinterpret_cast<chunk_t*>(row + p.n) = pack<DT>(u);
+    const size_t at = static_cast<size_t>(r) * p.nz + c;
+    store8<DT>(p.preact, at, p.preact_f32, v);
+    if (p.gated) store8<DT>(p.preact, at + p.n, p.preact_f32, u);
   }
   switch (p.act) {  // uniform
 #define MOE_ACT_CASE(A)                                         \
@@ -134,8 +148,9 @@ __device__ __forceinline__ void zero_unfilled(const ExpertAct& p, int b, int nb)
     chunk_t* o = reinterpret_cast<chunk_t*>(static_cast<uint16_t*>(p.out) + static_cast<size_t>(r) * p.n);
     for (int c = lane; c < p.n / 8; c += kWave) o[c] = z;
     if (p.preact != nullptr) {
-      chunk_t* q = reinterpret_cast<chunk_t*>(static_cast<uint16_t*>(p.preact) + static_cast<size_t>(r) * p.nz);
-      for (int c = lane; c < p.nz / 8; c += kWave) q[c] = z;
+      const size_t chunks = p.preact_f32 ? p.nz / 4 : p.nz / 8;
+      chunk_t* q = static_cast<chunk_t*>(p.preact) + static_cast<size_t>(r) * chunks;
+      for (size_t c = lane; c < chunks; c += kWave) q[c] = z;
     }
   };
   const int per = waves > p.e ? waves / p.e : 1;  // waves that share an expert's tail

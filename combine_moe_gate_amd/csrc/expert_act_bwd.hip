@@ -4,7 +4,10 @@
 // grad_out[r], for each placed row r of expert x:
 //     grad_z[r] = g act'(z)      (gated: g z_up act'(z_gate), and g act(z_gate))
 //     grad_b[x] = sum_r grad_z[r],   grad_w(route at r) = <grad_out[r], u(z[r])>
-// The products' own gradients are grouped GEMMs of grad_z and need nothing from here.
+// The products' own gradients are grouped GEMMs of grad_z, which is rounded to the element type
+// for them, once: what the matrix cores take (grad_b sums the unrounded values). z is read as
+// the forward kept it, rounded to the element type or in float32 (Z32): whichever the caller
+// keeps memory for.
 //
 // One pass over grad_out and z, bound by its traffic. A workgroup takes 64 rows (16 of few)
 // of one expert by 512 output features: a wave a row at a time, a lane eight features as
@@ -14,8 +17,11 @@
 // second launch adds both up in a fixed order. No floating-point atomics. Four rows per wave
 // are in flight, since a row's loads alone would leave memory idle while it is finished.
 //
-// Measured: 49152 rows of 1408 gated features (0.69 GB) 134 us, 5.2 TB/s; 2000 rows of 264
+// Measured: 49152 rows of 1408 gated features (0.69 GB) 134 us, 5.2 TB/s; the same with float32
+// z (0.97 GB) 196 us against 145 in calls one after the other, 4.9 TB/s; 2000 rows of 264
 // gated features with bias 9.5 us and 3 us for the sums.
+#include <type_traits>
+
 #include "expert_act.h"
 
 namespace moe {
@@ -61,11 +67,12 @@ __device__ __forceinline__ void act_and_slope(float z, float* f, float* d) {
   }
 }
 
-template <int DT, int ACT, bool GATED>
+template <int DT, int ACT, bool GATED, bool Z32>
 __global__ __launch_bounds__(kBwdThreads) void expert_act_backward_kernel(ExpertActBackward p, int col_blocks,
                                                                           int shift, int tile_grid, float* __restrict__ bias_part,
                                                                           double* __restrict__ dot_part) {
   constexpr int H = GATED ? 2 : 1;  // halves of z
+  constexpr int C = Z32 ? 2 : 1;    // 16-byte pieces of eight of its values
   __shared__ float row_w[kBwdRows];
   __shared__ float sums[kBwdWaves][kBwdCols];
   const int tid = threadIdx.x, lane = lane_id(), wv = wave_in_block();
@@ -115,24 +122,33 @@ __global__ __launch_bounds__(kBwdThreads) void expert_act_backward_kernel(Expert
 #pragma unroll
     for (int q = 0; q < 8; ++q) acc[h][q] = 0.0f;
   const uint16_t* gout = static_cast<const uint16_t*>(p.grad_out) + c;
-  const uint16_t* zin = static_cast<const uint16_t*>(p.preact) + c;
-  // kDepth rows of a wave in flight: each is loaded that many rows before it is worked on
+  const chunk_t* zin = static_cast<const chunk_t*>(p.preact);
+  // kDepth rows of a wave in flight: each is loaded that many rows before it is worked on (with
+  // float32 z two measure the same)
   constexpr int kDepth = 4;
-  chunk_t gv[kDepth], zv[kDepth][H];
+  chunk_t gv[kDepth], zv[kDepth][H][C];
   auto load = [&](int i, int b) __attribute__((always_inline)) {
     const chunk_t none = {0u, 0u, 0u, 0u};
     const size_t r = static_cast<size_t>(row0 + i);
     gv[b] = in ? *reinterpret_cast<const chunk_t*>(gout + r * p.n) : none;
 #pragma unroll
     for (int h = 0; h < H; ++h)
-      zv[b][h] = in && p.preact != nullptr ? *reinterpret_cast<const chunk_t*>(zin + r * p.nz + h * p.n) : none;
+#pragma unroll
+      for (int q = 0; q < C; ++q) zv[b][h][q] = in && p.preact != nullptr ? zin[(r * p.nz + h * p.n + c) / 8 * C + q] : none;
   };
   auto work = [&](int i, int b) __attribute__((always_inline)) {
     const int r = row0 + i;
     float g[8], z[H][8], d[H][8];
     unpack<DT>(gv[b], g);
 #pragma unroll
-    for (int h = 0; h < H; ++h) unpack<DT>(zv[b][h], z[h]);
+    for (int h = 0; h < H; ++h) {
+      if constexpr (Z32) {
+#pragma unroll
+        for (int q = 0; q < 8; ++q) z[h][q] = __uint_as_float(zv[b][h][q / 4][q % 4]);
+      } else {
+        unpack<DT>(zv[b][h][0], z[h]);
+      }
+    }
     const float w = p.route_w != nullptr ? row_w[i] : 1.0f;
     float dot = 0.0f;
 #pragma unroll
@@ -268,12 +284,13 @@ static void launch_first(const ExpertActBackward& p, const ExpertActBackwardPlan
                          double* dot_part, hipStream_t stream) {
   const unsigned grid = static_cast<unsigned>(plan.grid + kBwdZero);
   const int tile_grid = static_cast<int>(plan.grid);
-  if (p.gated)
-    expert_act_backward_kernel<DT, ACT, true><<<grid, kBwdThreads, 0, stream>>>(p, plan.col_blocks, plan.shift, tile_grid, bias_part,
-                                                                             dot_part);
-  else
-    expert_act_backward_kernel<DT, ACT, false><<<grid, kBwdThreads, 0, stream>>>(p, plan.col_blocks, plan.shift, tile_grid,
-                                                                              bias_part, dot_part);
+  auto go = [&](auto gated, auto z32) {
+    expert_act_backward_kernel<DT, ACT, decltype(gated)::value, decltype(z32)::value>
+        <<<grid, kBwdThreads, 0, stream>>>(p, plan.col_blocks, plan.shift, tile_grid, bias_part, dot_part);
+  };
+  using std::true_type, std::false_type;
+  if (p.gated) p.preact_f32 ? go(true_type{}, true_type{}) : go(true_type{}, false_type{});
+  else p.preact_f32 ? go(false_type{}, true_type{}) : go(false_type{}, false_type{});
 }
 
 template <int DT>

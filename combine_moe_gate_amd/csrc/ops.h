@@ -50,12 +50,12 @@ struct ExpertAct {
   const void* bias;         // [e, nz] (float32 if bias_f32), or null
   const float* route_w;     // [s, k], or null
   const void* residual;     // [s, n] if residual_gather, else [rows, n], or null
-  void* preact;             // [rows, nz], or null
+  void* preact;             // [rows, nz] (float32 if preact_f32), or null
   void* out;                // [rows, n]
   const int32_t *dst, *src, *kept, *offsets;
   int32_t e, k, m, n, nz, act;
   int64_t rows;
-  bool gather, gated, bias_f32, residual_gather;
+  bool gather, gated, bias_f32, residual_gather, preact_f32;
 };
 hipError_t launch_expert_act(const LayoutView& L, const ExpertAct& p, int dtype, hipStream_t stream);
 int64_t expert_act_grid(const LayoutView& L, int n, bool gated);  // its workgroups
@@ -67,7 +67,7 @@ int64_t expert_act_dgrad_grid(const LayoutView& L, int n);
 // Its epilogue's backward (n, nz as above).
 struct ExpertActBackward {
   const void* grad_out;     // [rows, n]
-  const void* preact;       // [rows, nz], or null where nothing needs it
+  const void* preact;       // [rows, nz] (float32 if preact_f32), or null where nothing needs it
   const float* route_w;     // [s, k], or null
   void* grad_preact;        // [rows, nz], or null
   void* grad_bias;          // [e, nz] (float32 if bias_f32), or null
@@ -76,7 +76,7 @@ struct ExpertActBackward {
   const int32_t *dst, *src, *kept, *offsets;
   int32_t s, e, k, n, nz, act;
   int64_t rows;
-  bool gated, bias_f32;
+  bool gated, bias_f32, preact_f32;
 };
 // The workspace: a partial bias row per row tile, a partial dot per row and column block.
 struct ExpertActBackwardPlan {

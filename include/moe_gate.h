@@ -387,8 +387,10 @@ moe_status_t moe_expert_gemm(const moe_layout_t* layout, const void* a, int32_t 
  *   topk_w      [s, k] float32, w_r the weight of the route placed at r, or NULL (1)
  *   residual    [rows, n], res(r) = residual[r], or with residual_gather [s, n], res(r) =
  *               residual[src[r]]; of dtype; or NULL (0)
- *   preact      [rows, nz] of dtype out: z rounded, for moe_expert_act_backward, or NULL;
- *               rows no route fills are zero
+ *   preact      [rows, nz] out: z, for moe_expert_act_backward, or NULL; rows no route fills
+ *               are zero. moe_expert_gemm_act keeps it rounded to dtype, moe_expert_gemm_act_ex
+ *               in preact_dtype (MOE_F32 or dtype): float32 is twice the memory, and a gradient
+ *               from the z the forward used
  *   a, gather, weights [e, nz, m], m, n, dtype, out [rows, n]: as in moe_expert_gemm; m and n
  *   multiples of 8; every pointer to element rows and the bias 16-byte aligned. out and
  *   preact may not overlap each other, a, weights or residual. A NULL epilogue means all
@@ -418,6 +420,10 @@ typedef struct moe_expert_epilogue {
 moe_status_t moe_expert_gemm_act(const moe_layout_t* layout, const void* a, int32_t gather,
                                  const void* weights, int32_t m, int32_t n, moe_dtype_t dtype,
                                  const moe_expert_epilogue_t* epilogue, void* out, void* stream);
+moe_status_t moe_expert_gemm_act_ex(const moe_layout_t* layout, const void* a, int32_t gather,
+                                    const void* weights, int32_t m, int32_t n, moe_dtype_t dtype,
+                                    const moe_expert_epilogue_t* epilogue, moe_dtype_t preact_dtype,
+                                    void* out, void* stream);
 
 /*
  * Backward of moe_expert_gemm_act's epilogue, from the kept z: with g = w_r grad_out[r] for
@@ -432,7 +438,8 @@ moe_status_t moe_expert_gemm_act(const moe_layout_t* layout, const void* a, int3
  * moe_expert_gemm_dgrad) and moe_expert_gemm_wgrad of grad_preact (with n = nz); that of a
  * gathered residual is moe_dispatch_backward of grad_out.
  *   grad_out [rows, n]; preact [rows, nz] as kept by the forward (NULL allowed for
- *   MOE_ACT_NONE, not gated and without grad_topk_w: nothing needs it); both of dtype.
+ *   MOE_ACT_NONE, not gated and without grad_topk_w: nothing needs it); both of dtype, with
+ *   moe_expert_act_backward_ex preact of preact_dtype (MOE_F32 or dtype).
  *   topk_w [s, k] or NULL as in the forward; grad_preact [rows, nz] of dtype, grad_bias
  *   [e, nz] of bias_dtype (MOE_F32 or dtype), grad_topk_w [s, k] float32 (needs topk_w),
  *   grad_residual [rows, n] of dtype: each may be NULL (not wanted). The outputs of rows may
@@ -449,6 +456,12 @@ moe_status_t moe_expert_act_backward(const moe_layout_t* layout, const void* gra
                                      void* grad_preact, moe_dtype_t bias_dtype, void* grad_bias,
                                      float* grad_topk_w, void* grad_residual, void* workspace,
                                      size_t workspace_bytes, void* stream);
+moe_status_t moe_expert_act_backward_ex(const moe_layout_t* layout, const void* grad_out,
+                                        const void* preact, moe_dtype_t preact_dtype, int32_t n,
+                                        moe_dtype_t dtype, int32_t activation, int32_t gated,
+                                        const float* topk_w, void* grad_preact, moe_dtype_t bias_dtype,
+                                        void* grad_bias, float* grad_topk_w, void* grad_residual,
+                                        void* workspace, size_t workspace_bytes, void* stream);
 
 /*
  * Input-row gradient of moe_expert_gemm_act, from its epilogue's grad_preact [rows, nz]:
