@@ -345,7 +345,8 @@ def _own_gemm(st):
 def _own_ffn(st):
     import combine_moe_gate_amd.autograd as A
     c, L = st["case"], st["layout"]
-    h = A.expert_linear(st["x"], st["up"], L, bias=st["up_bias"], act=c["act"], gated=True)
+    # the gradient of the z that the forward used, in 32 bits as inside any operator here
+    h = A.expert_linear(st["x"], st["up"], L, bias=st["up_bias"], act=c["act"], gated=True, preact_dtype=torch.float32)
     o = A.expert_linear(h, st["down"], L, bias=st["down_bias"], gather=False)
     return _with_grads(st, A.combine(o, st["w"].float(), L))
 
