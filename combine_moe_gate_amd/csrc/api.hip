@@ -570,7 +570,7 @@ moe_status_t moe_expert_gemm_act_ex(const moe_layout_t* layout, const void* a, i
   if (ep.residual_gather != 0 && ep.residual_gather != 1)
     return fail(MOE_ERR_INVALID_ARG, "residual_gather must be 0 or 1 (got %d)", ep.residual_gather);
   const int32_t nz = ep.gated ? 2 * n : n;
-  if (moe::expert_act_grid(v, n, ep.gated != 0) > INT32_MAX)
+  if (!moe::expert_act_fits(v, n, ep.gated != 0))
     return fail(MOE_ERR_UNSUPPORTED, "rows x n too large for one grouped GEMM launch");
   const int64_t a_rows = gather ? v.s : v.rows, res_rows = ep.residual_gather ? v.s : v.rows;
   MOE_TRY(check_array(a, v.s > 0 ? a_rows : 0, "a", true));
@@ -627,7 +627,7 @@ moe_status_t moe_expert_act_dgrad(const moe_layout_t* layout, const void* grad_p
   int64_t rc_in = 0, rc_out = 0;
   MOE_TRY(check_rows(nz, dtype, &rc_in));
   MOE_TRY(check_rows(m, dtype, &rc_out));
-  if (moe::expert_act_dgrad_grid(v, m) > INT32_MAX)
+  if (!moe::expert_act_dgrad_fits(v, m))
     return fail(MOE_ERR_UNSUPPORTED, "rows x m too large for one input-gradient launch");
   MOE_TRY(check_array(grad_preact, v.s > 0 ? v.rows : 0, "grad_preact", true));
   MOE_TRY(check_array(weights, v.s > 0 ? v.e : 0, "weights", true));
@@ -702,8 +702,7 @@ moe_status_t moe_expert_act_backward_ex(const moe_layout_t* layout, const void* 
   if (grad_residual != nullptr) MOE_TRY(check_array(grad_residual, 1, "grad_residual", true));
   const moe::ExpertActBackwardPlan plan = moe::expert_act_backward_plan(v, n, gated != 0);
   const int32_t nz = gated ? 2 * n : n;
-  const int64_t sums = static_cast<int64_t>(v.e) * ((nz + 63) / 64) + static_cast<int64_t>(v.s) * v.k / 256 + 1;
-  if (plan.grid > INT32_MAX - 65536 || sums > INT32_MAX)
+  if (!moe::expert_act_backward_fits(v, plan, nz, grad_bias != nullptr, grad_topk_w != nullptr))
     return fail(MOE_ERR_UNSUPPORTED, "rows x n too large for one launch");
   if (grad_bias != nullptr || grad_topk_w != nullptr) {
     if (workspace == nullptr) return fail(MOE_ERR_INVALID_ARG, "workspace is NULL");

@@ -348,20 +348,20 @@ __global__ __launch_bounds__(kBalBlock) void balance_tile_kernel(BalanceArgs a, 
   }
 }
 
-// Forward, second launch: workgroup (chunk, group) adds the group's partial rows over
+// Forward, second launch: workgroup (chunk, group - group0) adds the group's partial rows over
 // kBalChunk experts: 4 lanes of four experts by 64 rows at a time, in float64, then the 64 in
 // order. One workgroup alone draws the partial rows, which other XCDs wrote, at some 40 GB/s:
 // 512 rows of 128 experts in one workgroup took 15 us, in eight they take 7, most of it the
 // launch and two rounds of loads. The chunks' shares of the loss go to the group's last workgroup to arrive (counted on `arrived`, which
 // the first launch clears), which adds them in chunk order.
-__global__ __launch_bounds__(kBalReduce) void balance_reduce_kernel(BalanceArgs a, int tile, int pitch, int chunks,
-                                                                    BalancePartials part, BalanceOut out) {
+__global__ __launch_bounds__(kBalReduce) void balance_reduce_kernel(BalanceArgs a, int group0, int tile, int pitch,
+                                                                    int chunks, BalancePartials part, BalanceOut out) {
   constexpr int kRows = kBalReduce / 4;
   __shared__ double psum[kRows][kBalChunk];
   __shared__ int32_t csum[kRows][kBalChunk];
   __shared__ double red_z[kBalReduce / kWave];
   __shared__ int32_t red_n[kBalReduce / kWave];
-  const int tid = threadIdx.x, chunk = blockIdx.x % chunks, j = blockIdx.x / chunks;
+  const int tid = threadIdx.x, chunk = blockIdx.x % chunks, j = group0 + blockIdx.x / chunks;
   int lo = 0, hi = a.s;
   if (a.groups != nullptr) {
     lo = a.groups[j] > 0 ? a.groups[j] : 0;
@@ -561,9 +561,15 @@ hipError_t launch_balance_loss(const BalanceArgs& a, const BalancePlan& p, char*
   });
   hipError_t err = hipGetLastError();
   if (err != hipSuccess || single) return err;
-  balance_reduce_kernel<<<static_cast<unsigned>(a.g) * p.chunks, kBalReduce, 0, stream>>>(a, p.tile, p.pitch, p.chunks,
-                                                                                        part, out);
-  return hipGetLastError();
+  // as many groups at a time as one launch takes: all of them, short of 262144 (at 1024 experts)
+  const int most = static_cast<int>(most_workgroups(kBalReduce) / p.chunks);
+  for (int64_t g0 = 0; g0 < a.g && err == hipSuccess; g0 += most) {
+    const unsigned groups = static_cast<unsigned>(a.g - g0 < most ? a.g - g0 : most);
+    balance_reduce_kernel<<<groups * p.chunks, kBalReduce, 0, stream>>>(a, static_cast<int>(g0), p.tile, p.pitch, p.chunks,
+                                                                        part, out);
+    err = hipGetLastError();
+  }
+  return err;
 }
 
 hipError_t launch_balance_loss_backward(const BalanceArgs& a, const int32_t* counts, const int32_t* tokens,

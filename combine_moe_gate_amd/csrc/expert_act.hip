@@ -627,13 +627,13 @@ static ActShape act_shape(const LayoutView& L, int n, bool gated, bool kn) {
   return fits ? small : large;
 }
 
-int64_t expert_act_grid(const LayoutView& L, int n, bool gated) {
-  return (act_shape(L, n, gated, false).tiles + kXcds - 1) / kXcds * kXcds + kZeroBlocks;
-}
+static int64_t act_grid(const ActShape& a) { return (a.tiles + kXcds - 1) / kXcds * kXcds + kZeroBlocks; }
 
-int64_t expert_act_dgrad_grid(const LayoutView& L, int m) {
-  return (act_shape(L, m, false, true).tiles + kXcds - 1) / kXcds * kXcds + kZeroBlocks;
-}
+static bool act_fits(const ActShape& a) { return act_grid(a) <= most_workgroups(a.few ? kFewThreads : kActThreads); }
+
+bool expert_act_fits(const LayoutView& L, int n, bool gated) { return act_fits(act_shape(L, n, gated, false)); }
+
+bool expert_act_dgrad_fits(const LayoutView& L, int m) { return act_fits(act_shape(L, m, false, true)); }
 
 // Dynamic LDS above the 64 KiB default needs the kernel's limit raised, once per device.
 static hipError_t allow_lds(const void* kernel, int bytes, std::atomic<uint64_t>& done) {
@@ -674,7 +674,7 @@ static hipError_t launch_tiles(const ExpertAct& p, int col_blocks, int64_t grid,
 template <int DT>
 static hipError_t launch_dt(const LayoutView& L, const ExpertAct& p, hipStream_t stream) {
   const ActShape a = act_shape(L, p.n, p.gated, false);
-  const int64_t grid = expert_act_grid(L, p.n, p.gated);
+  const int64_t grid = act_grid(a);
   const int col_blocks = static_cast<int>(a.col_blocks);
   if (a.few == 1) return launch_few<DT, 1, 2>(p, col_blocks, grid, stream);
   if (a.few == 4) return launch_few<DT, 4, 4>(p, col_blocks, grid, stream);
@@ -688,8 +688,9 @@ hipError_t launch_expert_act(const LayoutView& L, const ExpertAct& p, int dtype,
 
 hipError_t launch_expert_act_dgrad(const LayoutView& L, const ExpertAct& p, int dtype, hipStream_t stream) {
   if (p.rows == 0) return hipSuccess;
-  const int64_t grid = expert_act_dgrad_grid(L, p.n);
-  const int col_blocks = static_cast<int>(act_shape(L, p.n, false, true).col_blocks);
+  const ActShape a = act_shape(L, p.n, false, true);
+  const int64_t grid = act_grid(a);
+  const int col_blocks = static_cast<int>(a.col_blocks);
   return dtype == kBF16 ? launch_tiles<kBF16, true>(p, col_blocks, grid, stream)
                         : launch_tiles<kF16, true>(p, col_blocks, grid, stream);
 }

@@ -279,6 +279,18 @@ ExpertActBackwardPlan expert_act_backward_plan(const LayoutView& L, int n, bool 
   return p;
 }
 
+// The second launch's workgroups: those of the bias sums, and all.
+static void sums_grid(int64_t s, int k, int e, int nz, bool bias, bool weights, int64_t* bias_grid, int64_t* grid) {
+  *bias_grid = bias ? static_cast<int64_t>(e) * ((nz + 63) / 64) : 0;
+  *grid = *bias_grid + (weights ? (s * k + kBwdThreads - 1) / kBwdThreads : 0);
+}
+
+bool expert_act_backward_fits(const LayoutView& L, const ExpertActBackwardPlan& plan, int nz, bool bias, bool weights) {
+  int64_t bias_grid = 0, grid = 0;
+  sums_grid(L.s, L.k, L.e, nz, bias, weights, &bias_grid, &grid);
+  return plan.grid + kBwdZero <= most_workgroups(kBwdThreads) && grid <= most_workgroups(kBwdThreads);
+}
+
 template <int DT, int ACT>
 static void launch_first(const ExpertActBackward& p, const ExpertActBackwardPlan& plan, float* bias_part,
                          double* dot_part, hipStream_t stream) {
@@ -308,9 +320,8 @@ static hipError_t launch_dt(const ExpertActBackward& p, const ExpertActBackwardP
   const hipError_t err = hipGetLastError();
   if (err != hipSuccess || (p.grad_bias == nullptr && p.grad_w == nullptr)) return err;
   const int bias_blocks = (p.nz + 63) / 64;
-  const int64_t bias_grid = p.grad_bias != nullptr ? static_cast<int64_t>(p.e) * bias_blocks : 0;
-  const int64_t routes = static_cast<int64_t>(p.s) * p.k;
-  const int64_t grid = bias_grid + (p.grad_w != nullptr ? (routes + kBwdThreads - 1) / kBwdThreads : 0);
+  int64_t bias_grid = 0, grid = 0;
+  sums_grid(p.s, p.k, p.e, p.nz, p.grad_bias != nullptr, p.grad_w != nullptr, &bias_grid, &grid);
   if (grid == 0) return hipSuccess;
   expert_act_backward_sums_kernel<DT><<<static_cast<unsigned>(grid), kBwdThreads, 0, stream>>>(
       p, plan.col_blocks, plan.shift, bias_blocks, bias_grid, bias_part, dot_part);

@@ -10,6 +10,9 @@
 
 namespace moe {
 
+// Most workgroups of so many threads in one launch: a grid is counted in 32-bit work items.
+constexpr int64_t most_workgroups(int threads) { return UINT32_MAX / threads; }
+
 // ---------------------------------------------------------------------------------
 // balance loss
 
@@ -58,11 +61,11 @@ struct ExpertAct {
   bool gather, gated, bias_f32, residual_gather, preact_f32;
 };
 hipError_t launch_expert_act(const LayoutView& L, const ExpertAct& p, int dtype, hipStream_t stream);
-int64_t expert_act_grid(const LayoutView& L, int n, bool gated);  // its workgroups
+bool expert_act_fits(const LayoutView& L, int n, bool gated);  // whether one launch takes its workgroups
 // Its input gradient: out[r] = a[r] @ W[x] with W [e, m, n] (m weight rows, n inputs): the
 // struct's a = the gradient rows [rows, m], out [rows, n], nz = n; no epilogue.
 hipError_t launch_expert_act_dgrad(const LayoutView& L, const ExpertAct& p, int dtype, hipStream_t stream);
-int64_t expert_act_dgrad_grid(const LayoutView& L, int n);
+bool expert_act_dgrad_fits(const LayoutView& L, int n);
 
 // Its epilogue's backward (n, nz as above).
 struct ExpertActBackward {
@@ -86,6 +89,8 @@ struct ExpertActBackwardPlan {
   size_t off_bias, off_dots, bytes;
 };
 ExpertActBackwardPlan expert_act_backward_plan(const LayoutView& L, int n, bool gated);
+// Whether its launches, the second with the sums of a bias and of route weights, take their workgroups.
+bool expert_act_backward_fits(const LayoutView& L, const ExpertActBackwardPlan& plan, int nz, bool bias, bool weights);
 hipError_t launch_expert_act_backward(const LayoutView& L, const ExpertActBackward& p,
                                       const ExpertActBackwardPlan& plan, char* ws, int dtype, hipStream_t stream);
 
