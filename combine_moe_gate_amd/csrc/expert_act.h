@@ -68,7 +68,9 @@ __device__ __forceinline__ void load8(const void* p, size_t at, bool f32, float 
   }
 }
 
-// Eight elements of a row of kept values: float32, or rounded to the element type.
+// Eight elements of a row of kept values: float32, or rounded to the element type. A finite value
+// past f16's largest is kept as that: as an infinity it would meet a slope or an activation of 0
+// in the backward, where the forward had a finite product.
 template <int DT>
 __device__ __forceinline__ void store8(void* p, size_t at, bool f32, const float (&f)[8]) {
   if (f32) {
@@ -78,7 +80,11 @@ __device__ __forceinline__ void store8(void* p, size_t at, bool f32, const float
       q[h] = chunk_t{__float_as_uint(f[4 * h]), __float_as_uint(f[4 * h + 1]), __float_as_uint(f[4 * h + 2]),
                      __float_as_uint(f[4 * h + 3])};
   } else {
-    *reinterpret_cast<chunk_t*>(static_cast<uint16_t*>(p) + at) = pack<DT>(f);
+    float g[8];
+#pragma unroll
+    for (int u = 0; u < 8; ++u)
+      g[u] = DT == kF16 && __builtin_fabsf(f[u]) < INFINITY ? fminf(fmaxf(f[u], -65504.0f), 65504.0f) : f[u];
+    *reinterpret_cast<chunk_t*>(static_cast<uint16_t*>(p) + at) = pack<DT>(g);
   }
 }
 

@@ -388,9 +388,9 @@ moe_status_t moe_expert_gemm(const moe_layout_t* layout, const void* a, int32_t 
  *   residual    [rows, n], res(r) = residual[r], or with residual_gather [s, n], res(r) =
  *               residual[src[r]]; of dtype; or NULL (0)
  *   preact      [rows, nz] out: z, for moe_expert_act_backward, or NULL; rows no route fills
- *               are zero. moe_expert_gemm_act keeps it rounded to dtype, moe_expert_gemm_act_ex
- *               in preact_dtype (MOE_F32 or dtype): float32 is twice the memory, and a gradient
- *               from the z the forward used
+ *               are zero. moe_expert_gemm_act keeps it rounded to dtype (a finite z past f16's
+ *               largest value as that), moe_expert_gemm_act_ex in preact_dtype (MOE_F32 or
+ *               dtype): float32 is twice the memory, and a gradient from the z the forward used
  *   a, gather, weights [e, nz, m], m, n, dtype, out [rows, n]: as in moe_expert_gemm; m and n
  *   multiples of 8; every pointer to element rows and the bias 16-byte aligned. out and
  *   preact may not overlap each other, a, weights or residual. A NULL epilogue means all

@@ -165,6 +165,33 @@ def test_replays_from_a_graph():
         assert all(torch.equal(p, q) for p, q in zip(outs, want)), f"replay {rep}"
 
 
+@pytest.mark.parametrize("n", [8, 4104])
+@pytest.mark.parametrize("name", E.ACTS)
+def test_values_past_f16_stay_finite(name, n):
+    """z = -70000 and -200 in the gate, 70000 in the up half: every activation but none makes 0 of
+    them, so the output, the gradients and the route weight's are 0 and not NaN. An infinite z
+    stays infinite."""
+    announce("kept values past f16", name, n)
+    s = 300
+    L = M.moe_dispatch_layout(torch.zeros((s, 1), dtype=torch.int32, device="cuda"), 1, 0)
+    x = torch.zeros((s, 8), dtype=torch.float16, device="cuda")
+    x[:, 0], x[:, 1] = 200, 1
+    wts = torch.zeros((1, 2 * n, 8), dtype=torch.float16, device="cuda")
+    wts[0, :n:2, 0], wts[0, 1:n:2, 1], wts[0, n:, 0] = -350, -200, 350
+    w = torch.ones((s, 1), device="cuda")
+    kw = dict(act=name, gated=True, w=w)
+    out, pre = M.moe_expert_gemm_act(L, x, wts, save_preact=True, **kw)
+    want = torch.full((n,), -65504.0)
+    want[1::2] = -200
+    assert torch.equal(pre.cpu().float(), torch.cat([want, torch.full((n,), 65504.0)]).expand(s, -1))
+    gz, gb, gw, _ = M.moe_expert_act_backward(L, torch.ones_like(out), pre, need_w=True, bias_dtype=torch.float32, **kw)
+    if name != "none":
+        assert not out.any() and not gz.any() and not gb.any() and not gw.any()
+    x[:, 0] = float("inf")
+    _, pre = M.moe_expert_gemm_act(L, x, wts, save_preact=True, **kw)
+    assert torch.isneginf(pre[:, :n:2]).all() and torch.isposinf(pre[:, n:]).all()
+
+
 def test_empty_batch_and_capacity_rows():
     announce("kept float32 empty")
     idx = torch.empty((0, 2), dtype=torch.int32, device="cuda")
