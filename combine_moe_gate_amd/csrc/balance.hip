@@ -42,7 +42,8 @@ constexpr int kBalMinTile = 32;
 constexpr int kBalChunk = 16;  // experts per workgroup of the second launch
 constexpr int kBalReduce = 256;  // its threads
 // Batches of up to this many logits and tokens are one tile, finished by the first launch
-// alone. One launch against two, microseconds: 8 experts 8192 logits 8.5 to 8.7, 16384 12.2 to
+// alone (and those of up to kBalMinTile tokens, which are one tile at any width: up to 32768
+// logits). One launch against two, microseconds: 8 experts 8192 logits 8.5 to 8.7, 16384 12.2 to
 // 9.3; 64 experts 16384 9.1 to 10.2, 32768 13.7 to 10.1; 256 experts 16384 8.4 to 10.8, 32768
 // 12.6 to 11.0.
 constexpr int64_t kBalSingle = 16384;

@@ -537,8 +537,9 @@ moe_status_t moe_expert_gemm_wgrad(const moe_layout_t* layout, const void* a, in
  * loss and z float64, rounded once. A token whose logits are all -inf has no distribution:
  * it counts among the tokens, its routes are counted, and it adds 0 to probs and z. NaN or
  * +inf in an unpadded token's logits makes probs, loss and z of its group NaN, no other's.
- * One launch for a single group of up to 16384 logits and 1024 tokens, else two (a further
- * one for each 262143 groups at 1024 experts, 16.7 million at 16).
+ * One launch (and no workspace) for a single group of up to 32 tokens, or of up to 1024 tokens
+ * and 16384 logits, else two (a further one for each 262143 groups at 1024 experts, 16.7
+ * million at 16).
  */
 size_t moe_balance_workspace_bytes(int32_t s, int32_t e, int32_t g);
 moe_status_t moe_balance_loss(const float* logits, const int32_t* topk_idx,

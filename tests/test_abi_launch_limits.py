@@ -62,3 +62,12 @@ def test_balance_loss_of_many_groups(lib):
     g = 300000
     args = [at(0), at(1), None, at(2), g, E, 1, g, at(3), at(4), at(5), at(6), None, at(7), 1 << 40, None]
     assert lib.moe_balance_loss(*args) == 1 and "z is NULL" in lib.moe_last_error().decode()
+
+
+def test_balance_loss_in_one_launch(lib):
+    """No workspace where the header says that one launch does."""
+    f = lib.moe_balance_workspace_bytes
+    for s, e, one in ((32, 1024, True), (33, 1024, False), (1024, 16, True), (1024, 17, False), (1025, 15, False),
+                      (33, 496, True), (33, 497, False)):
+        assert (f(s, e, 1) == 0) == one, (s, e)
+        assert f(s, e, 2) > 0
