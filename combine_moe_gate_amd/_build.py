@@ -3,7 +3,8 @@
     python -m combine_moe_gate_amd._build
 
 hipcc cross-compiles for gfx950 without a GPU present. The same build compiles
-tests/c_abi_check, a C++ program that drives the library through its C ABI alone.
+tests/c_abi_check and tests/c_abi_ops_check, C++ programs that drive the library through its
+C ABI alone.
 """
 from __future__ import annotations
 
@@ -45,21 +46,20 @@ def hipcc() -> str:
     return path
 
 
-C_CHECK_SRC = os.path.join(ROOT, "tests", "c_abi_check.cpp")
-C_CHECK_BIN = os.path.join(ROOT, "tests", "c_abi_check")
+C_CHECKS = [os.path.join(ROOT, "tests", name) for name in ("c_abi_check", "c_abi_ops_check")]
 
 
-def build_c_check(verbose: bool = False) -> str:
-    """Compile the C++ program that drives the library through its C ABI alone (a GPU
-    test runs it). It links LIB_PATH, found next to the binary through its run path."""
-    cmd = [hipcc(), "-O2", "-std=c++17", "-Wall", "-I", os.path.join(ROOT, "include"), C_CHECK_SRC,
-           "-L", HERE, "-lmoe_gate", "-Wl,-rpath,$ORIGIN/../combine_moe_gate_amd", "-o", C_CHECK_BIN]
-    if verbose:
-        print(" ".join(cmd), flush=True)
-    res = subprocess.run(cmd, capture_output=True, text=True)
-    if res.returncode != 0:
-        raise RuntimeError(f"hipcc failed ({res.returncode}):\n{res.stdout}\n{res.stderr}")
-    return C_CHECK_BIN
+def build_c_checks(verbose: bool = False) -> None:
+    """Compile the C++ programs that drive the library through its C ABI alone (GPU tests
+    run them). They link LIB_PATH, found next to the binary through its run path."""
+    for path in C_CHECKS:
+        cmd = [hipcc(), "-O2", "-std=c++17", "-Wall", "-I", os.path.join(ROOT, "include"), path + ".cpp",
+               "-L", HERE, "-lmoe_gate", "-Wl,-rpath,$ORIGIN/../combine_moe_gate_amd", "-o", path]
+        if verbose:
+            print(" ".join(cmd), flush=True)
+        res = subprocess.run(cmd, capture_output=True, text=True)
+        if res.returncode != 0:
+            raise RuntimeError(f"hipcc failed ({res.returncode}):\n{res.stdout}\n{res.stderr}")
 
 
 def build(verbose: bool = False) -> str:
@@ -74,7 +74,7 @@ def build(verbose: bool = False) -> str:
     if verbose and res.stderr.strip():
         print(res.stderr, file=sys.stderr)
     os.replace(tmp, LIB_PATH)
-    build_c_check(verbose)
+    build_c_checks(verbose)
     return LIB_PATH
 
 
