@@ -224,11 +224,13 @@ class _ExpertAct(torch.autograd.Function):
     """One projection per expert with its epilogue; a gathered from token rows or a buffer."""
 
     @staticmethod
-    def forward(ctx, a, weights, bias, w, residual, layout, act, gated, gather, residual_gather, preact_dtype):
+    def forward(ctx, a, weights, bias, w, residual, layout, act, gated, gather, residual_gather, preact_dtype,
+                backward):
         a, weights = a.contiguous(), weights.contiguous()
         bias, w, residual = (None if t is None else t.contiguous() for t in (bias, w, residual))
         bent = act != "none" or gated
-        keep = (bent and any(ctx.needs_input_grad[:4])) or (w is not None and ctx.needs_input_grad[3])
+        # needs_input_grad says what the inputs ask for, also where no backward follows
+        keep = backward and ((bent and any(ctx.needs_input_grad[:4])) or (w is not None and ctx.needs_input_grad[3]))
         got = moe_expert_gemm_act(layout, a, weights, gather=gather, bias=bias, act=act, gated=gated, w=w,
                                   residual=residual, residual_gather=residual_gather, save_preact=keep,
                                   preact_dtype=preact_dtype)
@@ -262,7 +264,7 @@ class _ExpertAct(torch.autograd.Function):
             g_weights = moe_expert_gemm_wgrad(L, a, g_z, gather=ctx.gather, out_dtype=weights.dtype)
         if need_res and ctx.residual_gather:
             g_res = moe_dispatch_backward(L, g_out)
-        return g_a, g_weights, g_bias, g_w, g_res, None, None, None, None, None, None
+        return g_a, g_weights, g_bias, g_w, g_res, None, None, None, None, None, None, None
 
 
 class LayoutRecorder:
@@ -429,7 +431,8 @@ def expert_linear(x: torch.Tensor, weights: torch.Tensor, layout: Layout, bias: 
     x's dtype once, before the products that lead to x and weights (what matrix cores take)."""
     if gather and bias is None and act == "none" and not gated and w is None and residual is None:
         return _ExpertLinear.apply(x, weights, layout)
-    return _ExpertAct.apply(x, weights, bias, w, residual, layout, act, gated, gather, residual_gather, preact_dtype)
+    return _ExpertAct.apply(x, weights, bias, w, residual, layout, act, gated, gather, residual_gather, preact_dtype,
+                            torch.is_grad_enabled())
 
 
 def renormalize(w: torch.Tensor, layout: Layout):
