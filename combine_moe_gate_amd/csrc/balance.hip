@@ -24,10 +24,12 @@
 // Nothing depends on an order of arrival: sums are taken in a fixed order, and the only
 // atomics are integer counts.
 //
-// Measured: 65536 tokens, 512 experts, 10 routes: forward 35-43 us and 7 us for the partial
-// rows, 137 MB read, 3.2-3.9 TB/s; backward 45 us, 268 MB, 6.0 TB/s. 32768 tokens, 128 experts,
-// 8 routes: 10 + 7 us and 10 us, mostly the time of a launch and a tile's first loads. One
-// tile, 256 tokens, 8 experts: 5 us and 3 us.
+// Measured: 65536 tokens, 512 experts, 10 routes: forward 43 us (35 after a pause) and 7 us for
+// the partial rows, 137 MB read, 3.2 TB/s where loads alone reach 6.8; backward 46 us, 268 MB,
+// 5.9 TB/s, its reads partly from the Infinity Cache. 32768 tokens, 128 experts, 8 routes: 9 + 7
+// us and 10 us for 18 and 34 MB, 16381 of 60 experts in 29 groups 12 + 7 us and 7 us for 4 and 8
+// MB: not bandwidth but loads that wait for each other (the group's offsets, then rows, routes
+// and partial rows), with a tile or two per CU. One tile, 256 tokens, 8 experts: 5 us and 3 us.
 #include <type_traits>
 
 #include "moe_device.h"
@@ -352,9 +354,9 @@ __global__ __launch_bounds__(kBalBlock) void balance_tile_kernel(BalanceArgs a, 
 // Forward, second launch: workgroup (chunk, group - group0) adds the group's partial rows over
 // kBalChunk experts: 4 lanes of four experts by 64 rows at a time, in float64, then the 64 in
 // order. One workgroup alone draws the partial rows, which other XCDs wrote, at some 40 GB/s:
-// 512 rows of 128 experts in one workgroup took 15 us, in eight they take 7, most of it the
-// launch and two rounds of loads. The chunks' shares of the loss go to the group's last workgroup to arrive (counted on `arrived`, which
-// the first launch clears), which adds them in chunk order.
+// 512 rows of 128 experts in one workgroup took 15 us, in eight they take 7 (for 1.2 MB). The
+// chunks' shares of the loss go to the group's last workgroup to arrive (counted on `arrived`,
+// which the first launch clears), which adds them in chunk order.
 __global__ __launch_bounds__(kBalReduce) void balance_reduce_kernel(BalanceArgs a, int group0, int tile, int pitch,
                                                                     int chunks, BalancePartials part, BalanceOut out) {
   constexpr int kRows = kBalReduce / 4;
