@@ -203,3 +203,28 @@ def test_empty_batch_and_capacity_rows():
         assert pre.dtype == torch.float32 and not pre.any() and not out.any()
         gz, gb, _, _ = M.moe_expert_act_backward(L, out, pre, act="silu", gated=True, bias_dtype=torch.float32)
         assert gz.shape == pre.shape and gz.dtype == torch.bfloat16 and not gz.any() and not gb.any()
+
+
+def test_more_bytes_than_32_bits_count():
+    """9.2 GB of kept values, 2.3e9 of them: both ends, forward and backward."""
+    announce("kept float32 9.2 GB")
+    s, m, n, e, k = 70000, 64, 4096, 8, 8
+    gen = torch.Generator("cuda").manual_seed(3)
+    idx = torch.rand((s, e), generator=gen, device="cuda").argsort(1).int()
+    x = torch.randn((s, m), generator=gen, device="cuda").to(torch.bfloat16)
+    wts = (torch.randn((e, n, m), generator=gen, device="cuda") / 8).to(torch.bfloat16)
+    L = M.moe_dispatch_layout(idx, e, 0)
+    out, pre = M.moe_expert_gemm_act(L, x, wts, act="silu", save_preact=True, preact_dtype=torch.float32)
+    gz, gb, _, _ = M.moe_expert_act_backward(L, out, pre, act="silu", bias_dtype=torch.float32)
+    for rows in (slice(0, 50), slice(L.rows - 50, L.rows)):
+        r = torch.arange(L.rows, device="cuda")[rows]
+        ex = torch.searchsorted(L.offsets[1:].long(), r, right=True)
+        p = x[L.src[rows].long()].double()[:, None, :] * wts[ex].double()
+        assert ((pre[rows].double() - p.sum(2)).abs() <= (m + 3) * 2 * U * p.abs().sum(2)).all()
+        z, g = pre[rows].double(), out[rows].double()
+        sg = torch.sigmoid(z)
+        want = g * sg * (1 + z * (1 - sg))
+        # act_err's slope error, and half a step of bf16
+        eps = U * (16 + 8 * z.abs() * (1 - sg)) * (1 + 2 * z.abs()) + 8 * U * (1 + z.abs())
+        assert ((gz[rows].double() - want).abs() <= 2.0 ** -8 * want.abs() + g.abs() * sg * eps + 1e-30).all()
+    assert torch.isfinite(gb).all()
