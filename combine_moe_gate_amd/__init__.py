@@ -18,6 +18,10 @@ function names are those of the C ABI in include/moe_gate.h:
     ga      = moe_expert_act_dgrad(layout, gz, weights)    # rows' gradient; weights': moe_expert_gemm_wgrad
     counts, tokens, probs, loss, z = moe_balance_loss(logits, idx, mask, groups)
     gl      = moe_balance_loss_backward(logits, counts, tokens, k, grad_loss, grad_z, mask, groups)
+    q       = moe_mx4_quantize(x)                          # (codes, scales): 4-bit rows, blocks of 32
+    x       = moe_mx4_dequantize(*q, dtype)
+    h       = moe_mx4_expert_gemm(layout, q, up, act="silu", gated=True, quantize_out=True)  # 4-bit weights
+    ga      = moe_mx4_expert_dgrad(layout, gz, up)
 
 There is no CPU fallback: without the built library, or without a GPU, every
 call raises.
@@ -132,6 +136,11 @@ _SIGNATURES = {
     "moe_balance_loss": (ctypes.c_int, [_P, _P, _P, _P, _I, _I, _I, _I, _P, _P, _P, _P, _P, _P, ctypes.c_size_t,
                                         _P]),
     "moe_balance_loss_backward": (ctypes.c_int, [_P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _P, _P]),
+    "moe_mx4_quantize": (ctypes.c_int, [_P, ctypes.c_int64, _I, ctypes.c_int, _P, _P, _P]),
+    "moe_mx4_dequantize": (ctypes.c_int, [_P, _P, ctypes.c_int64, _I, ctypes.c_int, _P, _P]),
+    "moe_mx4_expert_gemm": (ctypes.c_int, [ctypes.POINTER(LayoutStruct), _P, _P, _I, _P, _P, _I, _I, ctypes.c_int,
+                                           ctypes.POINTER(Epilogue), ctypes.c_int, _P, _P, _P]),
+    "moe_mx4_expert_dgrad": (ctypes.c_int, [ctypes.POINTER(LayoutStruct), _P, _P, _P, _I, _I, ctypes.c_int, _P, _P]),
     "moe_dispatch_layout_static_scratch": (ctypes.c_int, [_P, _I, _I, _I, _I, ctypes.POINTER(LayoutOptions), _P,
                                                           ctypes.c_size_t, ctypes.POINTER(LayoutStruct), _P]),
 }
@@ -613,6 +622,159 @@ def moe_expert_act_dgrad(layout: Layout, grad_preact: torch.Tensor, weights: tor
     return out
 
 
+_MX4_BLOCK = 32
+
+
+def _expect_mx4(pair, name: str, shape) -> None:
+    """Check a (codes, scales) pair that stands for values of `shape` (None matches any size)."""
+    if not isinstance(pair, (tuple, list)) or len(pair) != 2:
+        raise TypeError(f"{name} must be a (codes, scales) pair, as moe_mx4_quantize returns")
+    codes, scales = pair
+    for t, part in ((codes, "codes"), (scales, "scales")):
+        if t is None:
+            raise TypeError(f"{name}: {part} must be a torch.Tensor, got None")
+    m = shape[-1]
+    _expect(codes, f"{name}: codes", (*shape[:-1], None if m is None else m // 2), torch.uint8)
+    if codes.shape[-1] % (_MX4_BLOCK // 2):
+        raise ValueError(f"{name}: codes must have whole blocks of {_MX4_BLOCK // 2} bytes a row, got {codes.shape[-1]}")
+    _expect(scales, f"{name}: scales", (*codes.shape[:-1], codes.shape[-1] // (_MX4_BLOCK // 2)), torch.uint8)
+
+
+def moe_mx4_quantize(x: torch.Tensor, codes=None, scales=None):
+    """Rows in microscaled 4-bit floating point: (codes [..., m / 2], scales [..., m / 32]) uint8 of
+    x [..., m] float32, bfloat16 or float16, m a multiple of 32.
+
+    Each block of 32 values has a scale byte E, 2^(E - 127), from its largest magnitude, and
+    each value a sign and one of 0, 0.5, 1, 1.5, 2, 3, 4, 6 in four bits (two to a byte, the first in
+    the low half), the nearest to value / scale, ties to the even code, at most 6. A block with an
+    infinity or NaN gets scale 255 and reads back as NaN. codes, scales: tensors to write to."""
+    if not isinstance(x, torch.Tensor):
+        raise TypeError(f"x must be a torch.Tensor, got {type(x).__name__}")
+    if x.dim() < 1 or x.shape[-1] % _MX4_BLOCK or x.shape[-1] == 0:
+        raise ValueError(f"x must have rows of whole blocks of {_MX4_BLOCK} values, got shape {list(x.shape)}")
+    lead, m = x.shape[:-1], x.shape[-1]
+    _expect(x, "x", x.shape, _ROW_DTYPES)
+    _expect(codes, "codes", (*lead, m // 2), torch.uint8)
+    _expect(scales, "scales", (*lead, m // _MX4_BLOCK), torch.uint8)
+    _one_device(x, codes, scales)
+    if codes is None:
+        codes = torch.empty((*lead, m // 2), dtype=torch.uint8, device=x.device)
+    if scales is None:
+        scales = torch.empty((*lead, m // _MX4_BLOCK), dtype=torch.uint8, device=x.device)
+    _launch(x, lib().moe_mx4_quantize, x.data_ptr(), x.numel() // m, m, _DTYPE_CODE[x.dtype], codes.data_ptr(), scales.data_ptr())
+    return codes, scales
+
+
+def moe_mx4_dequantize(codes: torch.Tensor, scales: torch.Tensor, dtype: torch.dtype = torch.bfloat16, out=None):
+    """The values [..., m] that codes [..., m / 2] and scales [..., m / 32] stand for (see
+    moe_mx4_quantize), in dtype (or out's): exact in float32 and bfloat16, rounded once in float16."""
+    if not isinstance(codes, torch.Tensor):
+        raise TypeError(f"codes must be a torch.Tensor, got {type(codes).__name__}")
+    if codes.dim() < 1 or codes.shape[-1] == 0:
+        raise ValueError(f"codes must have rows of whole blocks, got shape {list(codes.shape)}")
+    _expect_mx4((codes, scales), "codes", codes.shape[:-1] + (2 * codes.shape[-1],))
+    m = 2 * codes.shape[-1]
+    if out is not None:
+        dtype = out.dtype if isinstance(out, torch.Tensor) else dtype
+    if dtype not in _DTYPE_CODE:
+        raise ValueError(f"unsupported element type {dtype}")
+    _expect(out, "out", (*codes.shape[:-1], m), dtype)
+    _one_device(codes, scales, out)
+    if out is None:
+        out = torch.empty((*codes.shape[:-1], m), dtype=dtype, device=codes.device)
+    _launch(codes, lib().moe_mx4_dequantize, codes.data_ptr(), scales.data_ptr(), out.numel() // m, m, _DTYPE_CODE[dtype],
+            out.data_ptr())
+    return out
+
+
+def moe_mx4_expert_gemm(layout: Layout, a, weights, gather: bool = True, bias=None, act: str = "none", gated: bool = False,
+                        w=None, residual=None, residual_gather: bool = False, save_preact: bool = False, dtype=None,
+                        quantize_out: bool = False, out=None, preact=None, preact_dtype=None):
+    """moe_expert_gemm_act with 4-bit weights: weights is the pair (codes [e, n, m / 2], scales [e, n,
+    m / 32]) of moe_mx4_quantize ([e, 2n, ..] gated).
+
+    a: rows in bfloat16 or float16, or a (codes, scales) pair of 4-bit rows ([s, ..] with gather, else
+    [rows, ..]); dtype: with 4-bit rows, the element type of bias, residual and results (bfloat16 unless
+    given; with 16-bit rows it is theirs). quantize_out: the result is a (codes, scales) pair, the float32
+    results rounded once to 4 bits (n a multiple of 32), for a next product; out is then such a pair.
+    Everything else as in moe_expert_gemm_act; with save_preact (or preact given) returns (out, preact)."""
+    rows = layout.s if gather else layout.rows
+    pair = isinstance(a, (tuple, list))
+    if pair:
+        _expect_mx4(a, "a", (rows, None))
+        codes, a_scales = a
+        m = 2 * codes.shape[1]
+        dtype = torch.bfloat16 if dtype is None else dtype
+        if dtype not in _GEMM_DTYPES:
+            raise ValueError(f"dtype must be bfloat16 or float16, got {dtype}")
+    elif a is None:
+        raise TypeError("a must be a torch.Tensor or a (codes, scales) pair, got None")
+    else:
+        _expect(a, "a", (rows, None), _GEMM_DTYPES)
+        codes, a_scales, m = a, None, a.shape[1]
+        if dtype not in (None, a.dtype):
+            raise ValueError(f"dtype must be that of the rows, {a.dtype}, got {dtype}")
+        dtype = a.dtype
+    if m == 0 or m % _MX4_BLOCK:
+        raise ValueError(f"rows must be whole blocks of {_MX4_BLOCK} values, got {m}")
+    _expect_mx4(weights, "weights", (layout.e, None, m))
+    nz = weights[0].shape[1]
+    if gated and nz % 2:
+        raise ValueError(f"gated weights must have an even number of rows, got {nz}")
+    n = nz // 2 if gated else nz
+    _expect(bias, "bias", (layout.e, nz), (torch.float32, dtype))
+    code = _activation(act)
+    _expect(w, "w", (layout.s, layout.k), torch.float32)
+    _expect(residual, "residual", (layout.s if residual_gather else layout.rows, n), dtype)
+    if quantize_out and n % _MX4_BLOCK:
+        raise ValueError(f"quantize_out: the {n} results of a row must be whole blocks of {_MX4_BLOCK}")
+    if quantize_out:
+        if out is not None:
+            _expect_mx4(out, "out", (layout.rows, n))
+        out_codes, out_scales = (None, None) if out is None else out
+    else:
+        _expect(out, "out", (layout.rows, n), dtype)
+        out_codes, out_scales = out, None
+    if preact_dtype is None:
+        preact_dtype = dtype if preact is None else (dtype, torch.float32)
+    elif preact_dtype not in (dtype, torch.float32):
+        raise ValueError(f"preact_dtype must be float32 or {dtype}, got {preact_dtype}")
+    _expect(preact, "preact", (layout.rows, nz), preact_dtype)
+    _same_device(layout, codes, a_scales, weights[0], weights[1], bias, w, residual, out_codes, out_scales, preact)
+    if out_codes is None:
+        if quantize_out:
+            out_codes = torch.empty((layout.rows, n // 2), dtype=torch.uint8, device=codes.device)
+            out_scales = torch.empty((layout.rows, n // _MX4_BLOCK), dtype=torch.uint8, device=codes.device)
+        else:
+            out_codes = torch.empty((layout.rows, n), dtype=dtype, device=codes.device)
+    if save_preact and preact is None:
+        preact = torch.empty((layout.rows, nz), dtype=preact_dtype, device=codes.device)
+    ep = Epilogue(code, int(bool(gated)), _ptr(bias), _DTYPE_CODE[bias.dtype] if bias is not None else MOE_F32,
+                  int(bool(residual_gather)), _ptr(w), _ptr(residual), _ptr(preact))
+    _launch(codes, lib().moe_mx4_expert_gemm, layout.byref(), _ptr(codes), _ptr(a_scales), int(bool(gather)), _ptr(weights[0]),
+            _ptr(weights[1]), m, n, _DTYPE_CODE[dtype], ctypes.byref(ep), _DTYPE_CODE[dtype if preact is None else preact.dtype],
+            _ptr(out_codes), _ptr(out_scales))
+    result = (out_codes, out_scales) if quantize_out else out_codes
+    return result if preact is None else (result, preact)
+
+
+def moe_mx4_expert_dgrad(layout: Layout, grad_preact: torch.Tensor, weights, out=None):
+    """Input-row gradient of moe_mx4_expert_gemm: grad_a[r] = grad_preact[r] @ W[x], W the values of
+    the pair weights, for the placed rows of expert x, [rows, m] (zero rows where no route is placed).
+    grad_preact is moe_expert_act_backward's (the epilogue is the same); the token gradient of a
+    gathered forward is moe_dispatch_backward(layout, grad_a)."""
+    _expect(grad_preact, "grad_preact", (layout.rows, None), _GEMM_DTYPES)
+    nz = grad_preact.shape[1]
+    _expect_mx4(weights, "weights", (layout.e, nz, None))
+    m = 2 * weights[0].shape[2]
+    _expect(out, "out", (layout.rows, m), grad_preact.dtype)
+    _same_device(layout, grad_preact, weights[0], weights[1], out)
+    out = out if out is not None else torch.empty((layout.rows, m), dtype=grad_preact.dtype, device=grad_preact.device)
+    _launch(grad_preact, lib().moe_mx4_expert_dgrad, layout.byref(), _ptr(grad_preact), _ptr(weights[0]), _ptr(weights[1]), m, nz,
+            _DTYPE_CODE[grad_preact.dtype], _ptr(out))
+    return out
+
+
 def moe_renormalize_kept(layout: Layout, w: torch.Tensor, out=None):
     _expect(w, "w", (layout.s, layout.k), torch.float32)
     _expect(out, "out", (layout.s, layout.k), torch.float32)
@@ -733,6 +895,7 @@ __all__ = [
     "moe_layout_read", "moe_dispatch_weighted", "moe_dispatch_weighted_backward",
     "moe_renormalize_kept", "moe_renormalize_kept_backward", "moe_expert_gemm", "moe_expert_gemm_wgrad", "moe_expert_gemm_dgrad",
     "moe_expert_gemm_act", "moe_expert_act_backward", "moe_expert_act_dgrad", "ACTIVATIONS",
-    "moe_balance_loss", "moe_balance_loss_backward", "workspace_bytes", "Layout",
+    "moe_balance_loss", "moe_balance_loss_backward", "moe_mx4_quantize", "moe_mx4_dequantize",
+    "moe_mx4_expert_gemm", "moe_mx4_expert_dgrad", "workspace_bytes", "Layout",
     "LayoutOptions", "MoeError", "lib", "EXPORTS",
 ]

@@ -43,7 +43,8 @@ from . import (FLAG_REPLAY_MISMATCH, Layout, moe_balance_loss, moe_balance_loss_
                moe_dispatch_replay, moe_dispatch_weighted, moe_dispatch_weighted_backward,
                moe_expert_act_backward, moe_expert_act_dgrad, moe_expert_gemm, moe_expert_gemm_act,
                moe_expert_gemm_dgrad, moe_expert_gemm_wgrad, moe_gate_topk, moe_gate_topk_backward,
-               moe_layout_read, moe_renormalize_kept, moe_renormalize_kept_backward)
+               moe_layout_read, moe_mx4_expert_dgrad, moe_mx4_expert_gemm, moe_mx4_quantize,
+               moe_renormalize_kept, moe_renormalize_kept_backward)
 
 
 class _Gate(torch.autograd.Function):
@@ -267,6 +268,52 @@ class _ExpertAct(torch.autograd.Function):
         return g_a, g_weights, g_bias, g_w, g_res, None, None, None, None, None, None, None
 
 
+class _ExpertMx4(torch.autograd.Function):
+    """One projection per expert on frozen 4-bit weights, with its epilogue; a gathered from token rows
+    or a buffer, quantised first with quantize_rows (the gradient passes through as it is)."""
+
+    @staticmethod
+    def forward(ctx, a, bias, w, residual, codes, scales, layout, act, gated, gather, residual_gather, quantize_rows,
+                preact_dtype, backward):
+        a, codes, scales = a.contiguous(), codes.contiguous(), scales.contiguous()
+        bias, w, residual = (None if t is None else t.contiguous() for t in (bias, w, residual))
+        bent = act != "none" or gated
+        keep = backward and ((bent and any(ctx.needs_input_grad[:3])) or (w is not None and ctx.needs_input_grad[2]))
+        got = moe_mx4_expert_gemm(layout, moe_mx4_quantize(a) if quantize_rows else a, (codes, scales), gather=gather,
+                                  bias=bias, act=act, gated=gated, w=w, residual=residual,
+                                  residual_gather=residual_gather, save_preact=keep, dtype=a.dtype,
+                                  preact_dtype=preact_dtype)
+        out, preact = got if keep else (got, None)
+        ctx.save_for_backward(codes, scales, w, preact)
+        ctx.layout, ctx.act, ctx.gated, ctx.bent = layout, act, gated, bent
+        ctx.gather, ctx.residual_gather = gather, residual_gather
+        ctx.bias_dtype = None if bias is None else bias.dtype
+        return out
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, g_out):
+        codes, scales, w, preact = ctx.saved_tensors
+        need_a, need_bias, need_w, need_res = ctx.needs_input_grad[:4]
+        L, g_out = ctx.layout, g_out.contiguous()
+        g_a = g_bias = g_w = g_res = None
+        g_z = g_out  # neither bent nor weighted: the product's own gradient
+        need_z = need_a and (ctx.bent or w is not None)
+        rows_res = need_res and not ctx.residual_gather
+        if need_z or need_bias or need_w or rows_res:
+            gz, g_bias, g_w, g_res = moe_expert_act_backward(
+                L, g_out, preact, ctx.act, ctx.gated, w, need_preact=need_z,
+                bias_dtype=ctx.bias_dtype if need_bias else None, need_w=need_w, need_residual=rows_res)
+            g_z = gz if need_z else g_out
+        if need_a:
+            g_a = moe_mx4_expert_dgrad(L, g_z, (codes, scales))
+            if ctx.gather:
+                g_a = moe_dispatch_backward(L, g_a)
+        if need_res and ctx.residual_gather:
+            g_res = moe_dispatch_backward(L, g_out)
+        return g_a, g_bias, g_w, g_res, None, None, None, None, None, None, None, None, None, None
+
+
 class LayoutRecorder:
     """Routing and layouts of one checkpointed call, recorded on its forward, replayed on
     its recompute.
@@ -435,6 +482,19 @@ def expert_linear(x: torch.Tensor, weights: torch.Tensor, layout: Layout, bias: 
                             torch.is_grad_enabled())
 
 
+def expert_linear_mx4(x: torch.Tensor, weights, layout: Layout, bias: torch.Tensor | None = None, act: str = "none",
+                      gated: bool = False, w: torch.Tensor | None = None, residual: torch.Tensor | None = None,
+                      residual_gather: bool = False, gather: bool = True, quantize_rows: bool = False,
+                      preact_dtype: torch.dtype | None = None):
+    """expert_linear on frozen 4-bit weights, the pair (codes [e, n, m / 2], scales [e, n, m / 32]) of
+    moe_mx4_quantize (gated: [e, 2n, ..]): gradients reach x, bias, w and residual, for tuning what stands
+    around the experts. quantize_rows: x is rounded to 4 bits before the product as well, and the gradient
+    passes through that rounding as it is. The other arguments as in expert_linear."""
+    codes, scales = weights
+    return _ExpertMx4.apply(x, bias, w, residual, codes, scales, layout, act, gated, gather, residual_gather,
+                            quantize_rows, preact_dtype, torch.is_grad_enabled())
+
+
 def renormalize(w: torch.Tensor, layout: Layout):
     """Weights renormalised over each token's kept routes (after the capacity drop)."""
     return _Renormalize.apply(w, layout)
@@ -452,5 +512,5 @@ def checkpoint(fn, *args, verify: bool = True, **kwargs):
     return out, rec
 
 
-__all__ = ["route", "balance_loss", "layout", "dispatch", "dispatch_on", "combine", "renormalize", "expert_linear", "checkpoint",
+__all__ = ["route", "balance_loss", "layout", "dispatch", "dispatch_on", "combine", "renormalize", "expert_linear", "expert_linear_mx4", "checkpoint",
            "LayoutRecorder"]

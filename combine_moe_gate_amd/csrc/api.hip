@@ -655,6 +655,181 @@ moe_status_t moe_expert_act_dgrad(const moe_layout_t* layout, const void* grad_p
                     "moe_expert_act_dgrad");
 }
 
+// ---------------------------------------------------------------------------------
+// microscaled 4-bit floating point
+
+// Rows of 4-bit values are whole blocks of 32.
+static moe_status_t check_mx4_rows(const char* name, int32_t m) {
+  if (m < 1) return fail(MOE_ERR_INVALID_ARG, "%s must be >= 1 (got %d)", name, m);
+  if (m % 32 != 0) return fail(MOE_ERR_MISALIGNED, "%s=%d is not a multiple of 32 (rows of 4-bit values are whole blocks)", name, m);
+  return MOE_OK;
+}
+
+static moe_status_t check_mx4_flat(const void* wide, const char* name, int64_t rows, int32_t m, moe_dtype_t dtype,
+                                   const void* codes, const void* scales, int64_t* blocks) {
+  if (elem_bytes(dtype) == 0) return fail(MOE_ERR_INVALID_ARG, "unknown dtype %d", static_cast<int>(dtype));
+  if (rows < 0) return fail(MOE_ERR_INVALID_ARG, "rows must be >= 0 (got %lld)", static_cast<long long>(rows));
+  MOE_TRY(check_mx4_rows("m", m));
+  *blocks = 0;
+  if (rows == 0) return MOE_OK;
+  if (rows > INT64_MAX / 8 / m)
+    return fail(MOE_ERR_UNSUPPORTED, "rows=%lld of m=%d are more than fit memory", static_cast<long long>(rows), m);
+  MOE_TRY(check_array(wide, rows, name, true));
+  MOE_TRY(check_array(codes, rows, "codes", true));
+  MOE_TRY(check_array(scales, rows, "scales", false));
+  *blocks = rows * (m / 32);
+  const size_t n = static_cast<size_t>(*blocks);
+  if (overlap(wide, n * 32 * elem_bytes(dtype), codes, n * 16) || overlap(wide, n * 32 * elem_bytes(dtype), scales, n) ||
+      overlap(codes, n * 16, scales, n))
+    return fail(MOE_ERR_INVALID_ARG, "%s, codes and scales may not overlap", name);
+  return MOE_OK;
+}
+
+moe_status_t moe_mx4_quantize(const void* x, int64_t rows, int32_t m, moe_dtype_t dtype, void* codes,
+                              uint8_t* scales, void* stream) {
+  int64_t blocks = 0;
+  MOE_TRY(check_mx4_flat(x, "x", rows, m, dtype, codes, scales, &blocks));
+  return hip_status(moe::launch_mx4_quantize(x, blocks, static_cast<int>(dtype), codes, scales,
+                                             static_cast<hipStream_t>(stream)),
+                    "moe_mx4_quantize");
+}
+
+moe_status_t moe_mx4_dequantize(const void* codes, const uint8_t* scales, int64_t rows, int32_t m,
+                                moe_dtype_t dtype, void* out, void* stream) {
+  int64_t blocks = 0;
+  MOE_TRY(check_mx4_flat(out, "out", rows, m, dtype, codes, scales, &blocks));
+  return hip_status(moe::launch_mx4_dequantize(codes, scales, blocks, static_cast<int>(dtype), out,
+                                               static_cast<hipStream_t>(stream)),
+                    "moe_mx4_dequantize");
+}
+
+moe_status_t moe_mx4_expert_gemm(const moe_layout_t* layout, const void* a, const uint8_t* a_scales,
+                                 int32_t gather, const void* w_codes, const uint8_t* w_scales,
+                                 int32_t m, int32_t n, moe_dtype_t dtype,
+                                 const moe_expert_epilogue_t* epilogue, moe_dtype_t preact_dtype,
+                                 void* out, uint8_t* out_scales, void* stream) {
+  moe::LayoutView v;
+  MOE_TRY(view_of(layout, &v));
+  if (dtype != MOE_BF16 && dtype != MOE_F16)
+    return fail(MOE_ERR_UNSUPPORTED, "moe_mx4_expert_gemm supports bf16 and f16 only (got dtype %d)",
+                static_cast<int>(dtype));
+  if (gather != 0 && gather != 1)
+    return fail(MOE_ERR_INVALID_ARG, "gather must be 0 or 1 (got %d)", gather);
+  const moe_expert_epilogue_t none{};
+  const moe_expert_epilogue_t& ep = epilogue != nullptr ? *epilogue : none;
+  int64_t rc_out = 0;
+  MOE_TRY(check_mx4_rows("m", m));
+  MOE_TRY(check_rows(n, dtype, &rc_out));
+  if (out_scales != nullptr) MOE_TRY(check_mx4_rows("n", n));
+  MOE_TRY(check_act(ep.activation, ep.gated, n));
+  if (ep.bias != nullptr) MOE_TRY(check_wide("bias_dtype", ep.bias_dtype, dtype));
+  if (ep.preact != nullptr) MOE_TRY(check_wide("preact_dtype", preact_dtype, dtype));
+  if (ep.residual_gather != 0 && ep.residual_gather != 1)
+    return fail(MOE_ERR_INVALID_ARG, "residual_gather must be 0 or 1 (got %d)", ep.residual_gather);
+  const int32_t nz = ep.gated ? 2 * n : n;
+  const int64_t a_rows = gather ? v.s : v.rows, res_rows = ep.residual_gather ? v.s : v.rows;
+  MOE_TRY(check_array(a, v.s > 0 ? a_rows : 0, "a", true));
+  MOE_TRY(check_array(w_codes, v.s > 0 ? v.e : 0, "w_codes", true));
+  MOE_TRY(check_array(w_scales, v.s > 0 ? v.e : 0, "w_scales", false));
+  MOE_TRY(check_array(out, v.rows, "out", true));
+  if (ep.bias != nullptr) MOE_TRY(check_array(ep.bias, 1, "bias", true));
+  if (ep.residual != nullptr) MOE_TRY(check_array(ep.residual, 1, "residual", true));
+  if (ep.preact != nullptr) MOE_TRY(check_array(ep.preact, 1, "preact", true));
+  moe::Mx4Act p{};
+  p.a = a;
+  p.w = w_codes;
+  p.bias = ep.bias;
+  p.route_w = ep.topk_w;
+  p.residual = ep.residual;
+  p.preact = ep.preact;
+  p.out = out;
+  p.dst = v.dst;
+  p.src = v.src;
+  p.kept = v.kept;
+  p.offsets = v.offsets;
+  p.e = v.e;
+  p.k = v.k;
+  p.m = m;
+  p.n = n;
+  p.nz = nz;
+  p.act = ep.activation;
+  p.rows = v.rows;
+  p.gather = gather != 0;
+  p.gated = ep.gated != 0;
+  p.bias_f32 = ep.bias_dtype == MOE_F32;
+  p.residual_gather = ep.residual_gather != 0;
+  p.preact_f32 = preact_dtype == MOE_F32;
+  p.a_scales = a_scales;
+  p.w_scales = w_scales;
+  p.out_scales = out_scales;
+  if (!moe::mx4_act_fits(v, p, static_cast<int>(dtype)))
+    return fail(MOE_ERR_UNSUPPORTED, "rows x n too large for one grouped GEMM launch");
+  // what the call writes may overlap neither what it reads nor one another
+  const size_t eb = elem_bytes(dtype), rows = static_cast<size_t>(v.rows), blocks = static_cast<size_t>(m) / 32;
+  struct Span {
+    const void* p;
+    size_t bytes;
+  };
+  const Span writes[3] = {{out, out_scales != nullptr ? rows * n / 2 : rows * n * eb},
+                          {out_scales, rows * n / 32},
+                          {ep.preact, rows * nz * elem_bytes(preact_dtype)}};
+  const Span reads[5] = {{a, a_rows * (a_scales != nullptr ? blocks * 16 : m * eb)},
+                         {a_scales, a_rows * blocks},
+                         {w_codes, static_cast<size_t>(v.e) * nz * blocks * 16},
+                         {w_scales, static_cast<size_t>(v.e) * nz * blocks},
+                         {ep.residual, res_rows * n * eb}};
+  for (int i = 0; i < 3; ++i) {
+    bool clash = false;
+    for (const Span& r : reads) clash = clash || overlap(writes[i].p, writes[i].bytes, r.p, r.bytes);
+    for (int j = 0; j < i; ++j) clash = clash || overlap(writes[i].p, writes[i].bytes, writes[j].p, writes[j].bytes);
+    if (clash)
+      return fail(MOE_ERR_INVALID_ARG, "out, out_scales and preact may not overlap each other, a, the weights or residual");
+  }
+  return hip_status(moe::launch_mx4_act(v, p, static_cast<int>(dtype), static_cast<hipStream_t>(stream)),
+                    "moe_mx4_expert_gemm");
+}
+
+moe_status_t moe_mx4_expert_dgrad(const moe_layout_t* layout, const void* grad_preact, const void* w_codes,
+                                  const uint8_t* w_scales, int32_t m, int32_t nz, moe_dtype_t dtype,
+                                  void* grad_a, void* stream) {
+  moe::LayoutView v;
+  MOE_TRY(view_of(layout, &v));
+  if (dtype != MOE_BF16 && dtype != MOE_F16)
+    return fail(MOE_ERR_UNSUPPORTED, "moe_mx4_expert_dgrad supports bf16 and f16 only (got dtype %d)",
+                static_cast<int>(dtype));
+  int64_t rc_in = 0;
+  MOE_TRY(check_rows(nz, dtype, &rc_in));
+  MOE_TRY(check_mx4_rows("m", m));
+  if (!moe::mx4_dgrad_fits(v, m))
+    return fail(MOE_ERR_UNSUPPORTED, "rows x m too large for one input-gradient launch");
+  MOE_TRY(check_array(grad_preact, v.s > 0 ? v.rows : 0, "grad_preact", true));
+  MOE_TRY(check_array(w_codes, v.s > 0 ? v.e : 0, "w_codes", true));
+  MOE_TRY(check_array(w_scales, v.s > 0 ? v.e : 0, "w_scales", false));
+  MOE_TRY(check_array(grad_a, v.rows, "grad_a", true));
+  const size_t eb = elem_bytes(dtype), blocks = static_cast<size_t>(v.e) * nz * (m / 32);
+  const size_t a_bytes = static_cast<size_t>(v.rows) * m * eb;
+  if (overlap(grad_a, a_bytes, grad_preact, static_cast<size_t>(v.rows) * nz * eb) ||
+      overlap(grad_a, a_bytes, w_codes, blocks * 16) || overlap(grad_a, a_bytes, w_scales, blocks))
+    return fail(MOE_ERR_INVALID_ARG, "grad_a may not overlap grad_preact or the weights");
+  moe::Mx4Act p{};
+  p.a = grad_preact;
+  p.w = w_codes;
+  p.w_scales = w_scales;
+  p.out = grad_a;
+  p.dst = v.dst;
+  p.src = v.src;
+  p.kept = v.kept;
+  p.offsets = v.offsets;
+  p.e = v.e;
+  p.k = v.k;
+  p.m = nz;
+  p.n = p.nz = m;
+  p.act = MOE_ACT_NONE;
+  p.rows = v.rows;
+  return hip_status(moe::launch_mx4_dgrad(v, p, static_cast<int>(dtype), static_cast<hipStream_t>(stream)),
+                    "moe_mx4_expert_dgrad");
+}
+
 size_t moe_expert_act_backward_workspace_bytes(const moe_layout_t* layout, int32_t n, int32_t gated) {
   const std::string saved = g_last_error;
   moe::LayoutView v;

@@ -96,12 +96,12 @@ __device__ __forceinline__ float route_weight(const ExpertAct& p, int r, int t) 
   return w;
 }
 
-// Eight output features c .. c + 7 of buffer row r of expert x, from the float32 products
-// v (gated: of the gate rows, u those of the up rows): bias, activation, route weight w,
-// residual, one rounding, whole 16-byte stores. c + 8 <= n.
+// Eight output features c .. c + 7 of buffer row r of expert x, unrounded in v, from the float32
+// products v (gated: of the gate rows, u those of the up rows): bias, activation, route weight
+// w, residual. c + 8 <= n.
 template <int DT>
-__device__ __forceinline__ void finish8(const ExpertAct& p, int x, int r, int t, float w, int c, float (&v)[8],
-                                        float (&u)[8]) {
+__device__ __forceinline__ void epilogue8(const ExpertAct& p, int x, int r, int t, float w, int c, float (&v)[8],
+                                          float (&u)[8]) {
   if (p.bias != nullptr) {
     float b[8];
     load8<DT>(p.bias, static_cast<size_t>(x) * p.nz + c, p.bias_f32, b);
@@ -146,30 +146,45 @@ __device__ __forceinline__ void finish8(const ExpertAct& p, int x, int r, int t,
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[i] += b[i];
   }
+}
+
+// The same, rounded once and stored as a whole 16 bytes.
+template <int DT>
+__device__ __forceinline__ void finish8(const ExpertAct& p, int x, int r, int t, float w, int c, float (&v)[8],
+                                        float (&u)[8]) {
+  epilogue8<DT>(p, x, r, t, w, c, v, u);
   *reinterpret_cast<chunk_t*>(static_cast<uint16_t*>(p.out) + static_cast<size_t>(r) * p.n + c) = pack<DT>(v);
 }
 
-// Zero the rows of the output (and of the kept values) that no route fills: block b of nb,
-// a row per wave at a time.
-__device__ __forceinline__ void zero_unfilled(const ExpertAct& p, int b, int nb) {
-  const int lane = lane_id(), wpb = blockDim.x / kWave;
+// clear(r) by a whole wave for every row that no route fills: block b of nb, a row per wave at a
+// time.
+template <class Clear>
+__device__ __forceinline__ void each_unfilled(const ExpertAct& p, int b, int nb, Clear clear) {
+  const int wpb = blockDim.x / kWave;
   const int wave = b * wpb + wave_in_block(), waves = nb * wpb;
-  const chunk_t z = {0u, 0u, 0u, 0u};
-  auto clear = [&](int r) {
-    chunk_t* o = reinterpret_cast<chunk_t*>(static_cast<uint16_t*>(p.out) + static_cast<size_t>(r) * p.n);
-    for (int c = lane; c < p.n / 8; c += kWave) o[c] = z;
-    if (p.preact != nullptr) {
-      const size_t chunks = p.preact_f32 ? p.nz / 4 : p.nz / 8;
-      chunk_t* q = static_cast<chunk_t*>(p.preact) + static_cast<size_t>(r) * chunks;
-      for (size_t c = lane; c < chunks; c += kWave) q[c] = z;
-    }
-  };
   const int per = waves > p.e ? waves / p.e : 1;  // waves that share an expert's tail
   for (int64_t item = wave; item < static_cast<int64_t>(p.e) * per; item += waves) {
     const int x = static_cast<int>(item % p.e), sub = static_cast<int>(item / p.e);
     for (int r = p.offsets[x] + p.kept[x] + sub; r < p.offsets[x + 1]; r += per) clear(r);
   }
   for (int64_t r = static_cast<int64_t>(p.offsets[p.e]) + wave; r < p.rows; r += waves) clear(static_cast<int>(r));
+}
+
+// Zero row r of the kept values, if there are any.
+__device__ __forceinline__ void clear_preact(const ExpertAct& p, int r) {
+  if (p.preact == nullptr) return;
+  const size_t chunks = p.preact_f32 ? p.nz / 4 : p.nz / 8;
+  chunk_t* q = static_cast<chunk_t*>(p.preact) + static_cast<size_t>(r) * chunks;
+  for (size_t c = lane_id(); c < chunks; c += kWave) q[c] = chunk_t{0u, 0u, 0u, 0u};
+}
+
+// Zero the rows of the output (and of the kept values) that no route fills.
+__device__ __forceinline__ void zero_unfilled(const ExpertAct& p, int b, int nb) {
+  each_unfilled(p, b, nb, [&](int r) {
+    chunk_t* o = reinterpret_cast<chunk_t*>(static_cast<uint16_t*>(p.out) + static_cast<size_t>(r) * p.n);
+    for (int c = lane_id(); c < p.n / 8; c += kWave) o[c] = chunk_t{0u, 0u, 0u, 0u};
+    clear_preact(p, r);
+  });
 }
 
 // Inclusive sum over the wave's lanes, by DPP moves alone: shifts by 1, 2, 4, 8 within each

@@ -569,11 +569,7 @@ __global__ __launch_bounds__(kFewThreads, F == 4 ? 2 : 4) void expert_act_few_ke
 // ---------------------------------------------------------------------------------
 // launches
 
-constexpr int kZeroBlocks = 64;  // workgroups that clear rows no route fills
-
-// At most this many row tiles of a height, known without reading the layout: a segment of R
-// rows has fewer than R / height + 1.
-static int64_t row_tiles(const LayoutView& L, int height) {
+int64_t row_tiles(const LayoutView& L, int height) {
   const int64_t routes = static_cast<int64_t>(L.s) * L.k;
   const int64_t with_rows = routes < L.e ? routes : L.e;
   if (L.capacity > 0) {
@@ -636,8 +632,7 @@ bool expert_act_fits(const LayoutView& L, int n, bool gated) { return act_fits(a
 
 bool expert_act_dgrad_fits(const LayoutView& L, int m) { return act_fits(act_shape(L, m, false, true)); }
 
-// Dynamic LDS above the 64 KiB default needs the kernel's limit raised, once per device.
-static hipError_t allow_lds(const void* kernel, int bytes, std::atomic<uint64_t>& done) {
+hipError_t allow_lds(const void* kernel, int bytes, std::atomic<uint64_t>& done) {
   int dev = 0;
   hipError_t err = hipGetDevice(&dev);
   if (err != hipSuccess) return err;

@@ -6,6 +6,8 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "internal.h"
 
 namespace moe {
@@ -42,6 +44,15 @@ hipError_t launch_balance_loss_backward(const BalanceArgs& a, const int32_t* cou
 
 // ---------------------------------------------------------------------------------
 // expert products with an epilogue
+
+constexpr int kZeroBlocks = 64;  // workgroups that clear rows no route fills
+
+// At most this many row tiles of a height, known without reading the layout: a segment of R
+// rows has fewer than R / height + 1.
+int64_t row_tiles(const LayoutView& L, int height);
+
+// Dynamic LDS above the 64 KiB default needs the kernel's limit raised, once per device.
+hipError_t allow_lds(const void* kernel, int bytes, std::atomic<uint64_t>& done);
 
 enum Act : int { kActNone = 0, kActRelu = 1, kActGelu = 2, kActGeluTanh = 3, kActSilu = 4 };
 
@@ -93,5 +104,27 @@ ExpertActBackwardPlan expert_act_backward_plan(const LayoutView& L, int n, bool 
 bool expert_act_backward_fits(const LayoutView& L, const ExpertActBackwardPlan& plan, int nz, bool bias, bool weights);
 hipError_t launch_expert_act_backward(const LayoutView& L, const ExpertActBackward& p,
                                       const ExpertActBackwardPlan& plan, char* ws, int dtype, hipStream_t stream);
+
+// ---------------------------------------------------------------------------------
+// microscaled 4-bit floating point (the format stands in mx4.h)
+
+// `blocks` blocks of 32 values: to 16 bytes of codes and a scale byte each, and back.
+hipError_t launch_mx4_quantize(const void* x, int64_t blocks, int dtype, void* codes, void* scales, hipStream_t stream);
+hipError_t launch_mx4_dequantize(const void* codes, const void* scales, int64_t blocks, int dtype, void* out,
+                                 hipStream_t stream);
+
+// An expert product whose weights are 4-bit: w holds codes [e, nz, m / 2]. With a_scales the rows
+// are 4-bit as well (a: codes [.., m / 2]), with out_scales the results (out: codes [rows, n / 2]).
+struct Mx4Act : ExpertAct {
+  const uint8_t* a_scales;  // [s or rows, m / 32], or null
+  const uint8_t* w_scales;  // [e, nz, m / 32]
+  uint8_t* out_scales;      // [rows, n / 32], or null
+};
+hipError_t launch_mx4_act(const LayoutView& L, const Mx4Act& p, int dtype, hipStream_t stream);
+bool mx4_act_fits(const LayoutView& L, const Mx4Act& p, int dtype);
+// Its input gradient: out[r] = a[r] @ W[x] with W [e, m, n] (m weight rows, n inputs): the struct's
+// a = the gradient rows [rows, m], out [rows, n], nz = n; no epilogue.
+hipError_t launch_mx4_dgrad(const LayoutView& L, const Mx4Act& p, int dtype, hipStream_t stream);
+bool mx4_dgrad_fits(const LayoutView& L, int n);
 
 }  // namespace moe

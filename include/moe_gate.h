@@ -476,6 +476,65 @@ moe_status_t moe_expert_act_dgrad(const moe_layout_t* layout, const void* grad_p
                                   void* grad_a, void* stream);
 
 /*
+ * Microscaled 4-bit floating point. A row is cut into blocks of 32 values. A block has a scale
+ * byte E, standing for 2^(E - 127), 255 for "not a number"; a value has four bits: a sign (8)
+ * and one of 0, 0.5, 1, 1.5, 2, 3, 4, 6 (0 to 7). It stands for their product as a float32: a
+ * power of two past float32's range (E = 254 with codes above 1) is infinite.
+ *   codes  [rows, m / 2] bytes, two values to a byte, the first in the low half; 16-byte aligned
+ *   scales [rows, m / 32] bytes, any alignment
+ * m is a multiple of 32 (MOE_ERR_MISALIGNED otherwise).
+ *
+ * moe_mx4_quantize: E = floor(log2 top) - 2 + 127 for the block's largest magnitude `top`, at
+ * least 0; values over the scale rounded to the nearest code, half-way cases to the even one,
+ * past 6 to 6; a zero keeps its sign. A block with an infinity or NaN gets E = 255 and codes 0,
+ * a block of zeros E = 0. x [rows, m] of dtype MOE_F32, MOE_BF16 or MOE_F16, 16-byte aligned.
+ *
+ * moe_mx4_dequantize: out [rows, m] of dtype, each value rounded once (exact in float32 and
+ * bf16; f16 rounds below 2^-14 and is infinite past 65504; NaN in a block with E = 255).
+ *
+ * rows >= 0; x or out, codes and scales may not overlap.
+ */
+moe_status_t moe_mx4_quantize(const void* x, int64_t rows, int32_t m, moe_dtype_t dtype,
+                              void* codes, uint8_t* scales, void* stream);
+moe_status_t moe_mx4_dequantize(const void* codes, const uint8_t* scales, int64_t rows, int32_t m,
+                                moe_dtype_t dtype, void* out, void* stream);
+
+/*
+ * moe_expert_gemm_act with 4-bit weights, and 4-bit rows and results where wanted:
+ *   out[r] = w_r u + res(r),  u = act(z) or act(z[0:n]) * z[n:2n],  z = A(r) @ W[x]^T + bias[x]
+ * with W the values that w_codes [e, nz, m / 2] and w_scales [e, nz, m / 32] stand for.
+ *   a_scales    NULL: a holds rows of dtype ([s, m] if gather, else [rows, m]); otherwise a holds
+ *               codes [.., m / 2] and a_scales their scales [.., m / 32], as moe_mx4_quantize
+ *               writes them (row by row: the dispatch is fused into the loads here too)
+ *   out_scales  NULL: out [rows, n] of dtype; otherwise the float32 results are quantised as in
+ *               moe_mx4_quantize: out holds codes [rows, n / 2], out_scales [rows, n / 32] (n a
+ *               multiple of 32); rows no route fills get zero codes and scales
+ *   epilogue, preact_dtype, gather, dtype (bf16 or f16: rows, bias, residual and results): as in
+ *               moe_expert_gemm_act_ex. m a multiple of 32, n of 8.
+ * Products are exact and summed in float32 (order unspecified, one order per sizes). A block with
+ * scale 255 makes the sums it enters NaN. out, out_scales and preact may not overlap each other
+ * or anything read. codes, rows, bias, residual, preact and out 16-byte aligned.
+ */
+moe_status_t moe_mx4_expert_gemm(const moe_layout_t* layout, const void* a, const uint8_t* a_scales,
+                                 int32_t gather, const void* w_codes, const uint8_t* w_scales,
+                                 int32_t m, int32_t n, moe_dtype_t dtype,
+                                 const moe_expert_epilogue_t* epilogue, moe_dtype_t preact_dtype,
+                                 void* out, uint8_t* out_scales, void* stream);
+
+/*
+ * Input-row gradient of moe_mx4_expert_gemm, from its epilogue's grad_preact [rows, nz]
+ * (moe_expert_act_backward computes it: the epilogue is the same):
+ *   grad_a[r, :] = grad_preact[r, :] @ W[x]       (W [e, nz, m] in 4 bits, grad_a [rows, m])
+ * for the placed rows r of expert x; rows no route fills zero. Through the rounding of rows to 4
+ * bits the gradient is taken to pass unchanged. grad_preact and grad_a of dtype (bf16 or f16),
+ * m a multiple of 32, nz of 8; grad_a may not overlap grad_preact or the weights. The gradient of
+ * gathered token rows is moe_dispatch_backward of grad_a.
+ */
+moe_status_t moe_mx4_expert_dgrad(const moe_layout_t* layout, const void* grad_preact,
+                                  const void* w_codes, const uint8_t* w_scales, int32_t m,
+                                  int32_t nz, moe_dtype_t dtype, void* grad_a, void* stream);
+
+/*
  * Input-row gradient of moe_expert_gemm ([DS-8213] first commit: the backward replays the
  * forward's grouping on the same handle; review-fix commit: the groups are the offsets'
  * segments). For expert x and each row r in [offsets[x], offsets[x] + kept[x]):

@@ -57,3 +57,4 @@ from .moe import (  # noqa: F401
 )
 from .router import Balance, balance_loss, balance_loss_backward  # noqa: F401
 from .epilogue import expert_act_backward, expert_gemm_act  # noqa: F401
+from . import mx4  # noqa: F401
