@@ -12,13 +12,16 @@ import os
 import shutil
 import subprocess
 import sys
+import tempfile
+from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 LIB_NAME = "libmoe_gate.so"
 LIB_PATH = os.path.join(HERE, LIB_NAME)
 SOURCES = [os.path.join(HERE, "csrc", f) for f in ("api.hip", "gate.hip", "layout.hip", "rows.hip", "gemm.hip", "gemm_bwd.hip",
-                                                     "balance.hip", "expert_act.hip", "expert_act_bwd.hip", "mx4.hip", "mx4_act.hip", "mx4_dgrad.hip")]
+                                                     "balance.hip", "expert_act.hip", "expert_act_bwd.hip", "mx4.hip", "mx4_act.hip", "mx4_tile.hip",
+                                                     "mx4_dgrad.hip")]
 HEADERS = [os.path.join(HERE, "csrc", f) for f in ("internal.h", "moe_device.h", "gemm_common.h", "ops.h", "expert_act.h", "mx4.h",
                                                      "mx4_product.h")] + [
     os.path.join(ROOT, "include", "moe_gate.h")]
@@ -64,16 +67,24 @@ def build_c_checks(verbose: bool = False) -> None:
 
 
 def build(verbose: bool = False) -> str:
-    """Compile every HIP source into LIB_PATH (always recompiles). Returns the path."""
+    """Compile every HIP source, several at a time, into LIB_PATH (always recompiles). Returns the path."""
     tmp = LIB_PATH + ".tmp"
-    cmd = [hipcc(), *FLAGS, "-I", os.path.join(ROOT, "include"), *SOURCES, "-o", tmp]
-    if verbose:
-        print(" ".join(cmd), flush=True)
-    res = subprocess.run(cmd, capture_output=True, text=True)
-    if res.returncode != 0:
-        raise RuntimeError(f"hipcc failed ({res.returncode}):\n{res.stdout}\n{res.stderr}")
-    if verbose and res.stderr.strip():
-        print(res.stderr, file=sys.stderr)
+    compile_flags = [f for f in FLAGS if f != "-shared"]
+
+    def run(cmd):
+        if verbose:
+            print(" ".join(cmd), flush=True)
+        res = subprocess.run(cmd, capture_output=True, text=True)
+        if res.returncode != 0:
+            raise RuntimeError(f"hipcc failed ({res.returncode}):\n{res.stdout}\n{res.stderr}")
+        if verbose and res.stderr.strip():
+            print(res.stderr, file=sys.stderr)
+
+    with tempfile.TemporaryDirectory() as objects, ThreadPoolExecutor(min(8, os.cpu_count() or 1)) as pool:
+        objs = [os.path.join(objects, os.path.basename(s) + ".o") for s in SOURCES]
+        list(pool.map(run, [[hipcc(), *compile_flags, "-c", "-I", os.path.join(ROOT, "include"), s, "-o", o]
+                            for s, o in zip(SOURCES, objs)]))
+        run([hipcc(), *FLAGS, *objs, "-o", tmp])
     os.replace(tmp, LIB_PATH)
     build_c_checks(verbose)
     return LIB_PATH

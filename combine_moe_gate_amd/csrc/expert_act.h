@@ -1,6 +1,8 @@
 // Activations and the epilogue shared by the kernels of the expert products.
 #pragma once
 
+#include <utility>
+
 #include "gemm_common.h"
 #include "ops.h"
 
@@ -271,6 +273,35 @@ __device__ __forceinline__ SegmentTile segment_tile(int b, int e, const int32_t*
   tc.cb = __builtin_amdgcn_readfirstlane(v / in_band);  // uniform as they are: kept in scalar registers
   tc.rb = __builtin_amdgcn_readfirstlane(bd * band + v % in_band);
   return tc;
+}
+
+// Row-blocks of a segment of `rows` rows: as few of at most Units 32-row units as hold it, of
+// nearly equal height.
+template <int Units>
+__device__ __forceinline__ int unit_blocks(int rows) {
+  const int units = (rows + 31) / 32;
+  return (units + Units - 1) / Units;
+}
+
+struct UnitTile {
+  int expert, unit0, units, cb, rows, offset;  // expert (-1: none), first 32-row unit, units, column-block
+};
+
+template <int Units>
+__device__ __forceinline__ UnitTile unit_tile(int b, int e, const int32_t* __restrict__ kept,
+                                              const int32_t* __restrict__ offsets, int col_blocks, int band) {
+  const SegmentTile s = segment_tile(b, e, kept, offsets, col_blocks, band, [](int r) { return unit_blocks<Units>(r); });
+  if (s.expert < 0) return UnitTile{-1, 0, 0, 0, 0, 0};
+  const int units = (s.rows + 31) / 32;
+  const int base = units / s.blocks, extra = units % s.blocks;  // the first `extra` blocks are a unit taller
+  return UnitTile{s.expert, s.rb * base + (s.rb < extra ? s.rb : extra), base + (s.rb < extra), s.cb, s.rows,
+                  s.offset};
+}
+
+// f(0), f(1), ... with compile-time arguments.
+template <int... I, class F>
+__device__ __forceinline__ void static_for(std::integer_sequence<int, I...>, F f) {
+  (f(std::integral_constant<int, I>{}), ...);
 }
 
 }  // namespace moe

@@ -44,7 +44,6 @@
 // of 2.3 GB read: 0.57 ms, 4.2 TB/s, 45%. One token, 8 experts of 128, 201 MB of weights: 41 us,
 // 4.9 TB/s of them, where loads alone reach 6.8.
 #include <atomic>
-#include <utility>
 
 #include "expert_act.h"
 
@@ -81,28 +80,6 @@ static_assert(8 * 2 * 16 * kSlabPitch <= 2 * kActStage, "the slabs reuse the sta
 template <bool KN>
 constexpr int act_units = KN ? kActUnits - 1 : kActUnits;
 
-// Row-blocks of a segment of `rows` rows: as few as hold it, of nearly equal height.
-template <bool KN>
-__device__ __forceinline__ int act_blocks(int rows) {
-  const int units = (rows + 31) / 32;
-  return (units + act_units<KN> - 1) / act_units<KN>;
-}
-
-struct ActTile {
-  int expert, unit0, units, cb, rows, offset;  // expert (-1: none), first 32-row unit, units, column-block
-};
-
-template <bool KN>
-__device__ __forceinline__ ActTile act_tile(int b, int e, const int32_t* __restrict__ kept,
-                                            const int32_t* __restrict__ offsets, int col_blocks) {
-  const SegmentTile s = segment_tile(b, e, kept, offsets, col_blocks, kActBand, [](int r) { return act_blocks<KN>(r); });
-  if (s.expert < 0) return ActTile{-1, 0, 0, 0, 0, 0};
-  const int units = (s.rows + 31) / 32;
-  const int base = units / s.blocks, extra = units % s.blocks;  // the first `extra` blocks are a unit taller
-  return ActTile{s.expert, s.rb * base + (s.rb < extra ? s.rb : extra), base + (s.rb < extra), s.cb, s.rows,
-                 s.offset};
-}
-
 // Four weight fragments of a [K][N] stage: for tile j two transposing reads at at[j] and 4 K
 // rows (2048 bytes) on. They are written out with their wait because the compiler lets no
 // transposing read it knows start while direct-to-LDS loads are in flight, and those are in
@@ -126,16 +103,10 @@ __device__ __forceinline__ void read_tr16(const uint32_t (&at)[4], chunk_t (&b)[
   for (int j = 0; j < 4; ++j) b[j] = chunk_t{lo[j].x, lo[j].y, hi[j].x, hi[j].y};
 }
 
-// f(0), f(1), ... with compile-time arguments.
-template <int... I, class F>
-__device__ __forceinline__ void static_for(std::integer_sequence<int, I...>, F f) {
-  (f(std::integral_constant<int, I>{}), ...);
-}
-
 // The tile's products and its epilogue, for a height of 32 FM rows. KN: weights stored
 // [K][N] per expert (the input gradient).
 template <int DT, bool KN, int FM>
-__device__ __forceinline__ void act_tile_body(const ExpertAct& p, const ActTile& tc, char* lds) {
+__device__ __forceinline__ void act_tile_body(const ExpertAct& p, const UnitTile& tc, char* lds) {
   constexpr int FN = 4;
   // A K step's products in order: (k32 half, row tile), 2 FM slots of FN MFMAs, cut into
   // groups of up to four slots whose fragments are read together; the last group lies in
@@ -410,7 +381,7 @@ __global__ __launch_bounds__(kActThreads) __attribute__((amdgpu_waves_per_eu(2, 
     zero_unfilled(p, blockIdx.x - tile_grid, gridDim.x - tile_grid);
     return;
   }
-  const ActTile tc = act_tile<KN>(blockIdx.x, p.e, p.kept, p.offsets, col_blocks);
+  const UnitTile tc = unit_tile<act_units<KN>>(blockIdx.x, p.e, p.kept, p.offsets, col_blocks, kActBand);
   if (tc.expert < 0) return;
   switch (tc.units) {
     case 1: act_tile_body<DT, KN, 1>(p, tc, lds); break;

@@ -11,56 +11,15 @@
 // weights have in earnest); elsewhere each row value is split into two bf16 values, the upper 8
 // bits of its 11 and the rest, both products exact again.
 //
-// Few rows: a workgroup of four waves multiplies up to 16 F rows by 16 FB weight rows, each wave a
+// Two kernels, chosen by the rows an expert has on average: the tiles of mx4_tile.hip, and few rows:
+// a workgroup of four waves multiplies up to 16 F rows by 16 FB weight rows, each wave a
 // quarter of the K steps of four blocks: codes, scales and rows go from memory straight to the
 // registers, several steps ahead, and the four partial sums meet in LDS.
-#include "expert_act.h"
+#include <atomic>
+
 #include "mx4_product.h"
 
 namespace moe {
-
-typedef int i32x8_t __attribute__((ext_vector_type(8)));
-
-// A block of 4-bit codes per lane on each side, lane l's of row l % 16 and K block l / 16, with the
-// scale bytes in the low bytes of sa and sb.
-__device__ __forceinline__ f32x4_t mfma_mx4(const chunk_t& a, uint32_t sa, const chunk_t& b, uint32_t sb, f32x4_t c) {
-  const i32x8_t va = {static_cast<int>(a.x), static_cast<int>(a.y), static_cast<int>(a.z), static_cast<int>(a.w), 0, 0, 0, 0};
-  const i32x8_t vb = {static_cast<int>(b.x), static_cast<int>(b.y), static_cast<int>(b.z), static_cast<int>(b.w), 0, 0, 0, 0};
-  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(va, vb, c, 4, 4, 0, static_cast<int>(sa), 0, static_cast<int>(sb));
-}
-
-// Eight output features, finished and stored: rounded to 16 bits, or to 4 with the block's other
-// 24 in the lane's group of four (lanes 4 i .. 4 i + 3 hold features c - c % 32 .. + 31 of a row).
-template <int DT>
-__device__ __forceinline__ void finish8_mx4(const Mx4Act& p, int x, int r, int t, float w, int c, float (&v)[8],
-                                            float (&u)[8]) {
-  epilogue8<DT>(p, x, r, t, w, c, v, u);
-  const size_t at = static_cast<size_t>(r) * p.n + c;
-  if (p.out_scales != nullptr) {
-    uint32_t E;
-    static_cast<uint32_t*>(p.out)[at / 8] = mx4_quantize8(v, &E);
-    if (c % 32 == 0) p.out_scales[at / 32] = static_cast<uint8_t>(E);
-  } else {
-    *reinterpret_cast<chunk_t*>(static_cast<uint16_t*>(p.out) + at) = pack<DT>(v);
-  }
-}
-
-__device__ __forceinline__ void zero_unfilled_mx4(const Mx4Act& p, int b, int nb) {
-  if (p.out_scales == nullptr) {
-    zero_unfilled(p, b, nb);
-    return;
-  }
-  each_unfilled(p, b, nb, [&](int r) {
-    const int blocks = p.n / kMx4Block;
-    chunk_t* o = static_cast<chunk_t*>(p.out) + static_cast<size_t>(r) * blocks;
-    uint8_t* s = p.out_scales + static_cast<size_t>(r) * blocks;
-    for (int c = lane_id(); c < blocks; c += kWave) {
-      o[c] = chunk_t{0u, 0u, 0u, 0u};
-      s[c] = 0;
-    }
-    clear_preact(p, r);
-  });
-}
 
 // ---------------------------------------------------------------------------------
 // few rows
@@ -252,38 +211,53 @@ __global__ __launch_bounds__(kMxFewThreads, 2) void mx4_few_kernel(Mx4Act p, int
 // ---------------------------------------------------------------------------------
 // launches
 
+// How a launch is shaped: F of its row tiles (16 F rows; 0: the large tiles), the weight rows
+// per workgroup, and its workgroups.
 struct Mx4Shape {
-  int few, cols;       // F of its row tiles (16 F rows), weight rows per workgroup
+  int few, cols;
   int64_t col_blocks, tiles;
 };
 
 static Mx4Shape mx4_shape(const LayoutView& L, const Mx4Act& p) {
-  // 64 weight rows, so that a 4-bit block of 32 gated results lies in one workgroup
-  Mx4Shape a{1, 64, 0, 0};
-  a.col_blocks = (static_cast<int64_t>(p.nz) + a.cols - 1) / a.cols;
-  a.tiles = L.s == 0 ? 0 : row_tiles(L, 16 * a.few) * a.col_blocks;
-  return a;
+  auto shape = [&](int few) {
+    // 64 weight rows, so that a 4-bit block of 32 gated results lies in one workgroup
+    Mx4Shape a{few, few ? 64 : 256, 0, 0};
+    a.col_blocks = (static_cast<int64_t>(p.nz) + a.cols - 1) / a.cols;
+    a.tiles = L.s == 0 ? 0 : row_tiles(L, few ? 16 * few : mx4_tile_rows()) * a.col_blocks;
+    return a;
+  };
+  const int64_t routes = static_cast<int64_t>(L.s) * L.k;
+  int64_t mean = (routes + L.e - 1) / L.e;
+  if (L.capacity > 0 && mean > L.capacity) mean = L.capacity;
+  return shape(mean <= 16 ? 1 : 0);
 }
 
 static int64_t mx4_grid(const Mx4Shape& a) { return (a.tiles + kXcds - 1) / kXcds * kXcds + kZeroBlocks; }
 
 bool mx4_act_fits(const LayoutView& L, const Mx4Act& p, int) {
-  return mx4_grid(mx4_shape(L, p)) <= most_workgroups(kMxFewThreads);
+  const Mx4Shape a = mx4_shape(L, p);
+  return mx4_grid(a) <= most_workgroups(a.few ? kMxFewThreads : kMx4TileThreads);
 }
 
 template <int RT, int DT, int F, int FB>
 static hipError_t launch_few(const Mx4Act& p, int col_blocks, int64_t grid, hipStream_t stream) {
+  static std::atomic<uint64_t> done{0};
   constexpr int kBytes = kMxFewWaves * 16 * F * (16 * FB * 4 + 16);
-  static_assert(kBytes <= 65536);
-  mx4_few_kernel<RT, DT, F, FB><<<static_cast<unsigned>(grid), kMxFewThreads, kBytes, stream>>>(
-      p, col_blocks, static_cast<int>(grid) - kZeroBlocks);
+  auto kern = mx4_few_kernel<RT, DT, F, FB>;
+  if (kBytes > 65536) {
+    const hipError_t err = allow_lds(reinterpret_cast<const void*>(kern), kBytes, done);
+    if (err != hipSuccess) return err;
+  }
+  kern<<<static_cast<unsigned>(grid), kMxFewThreads, kBytes, stream>>>(p, col_blocks, static_cast<int>(grid) - kZeroBlocks);
   return hipGetLastError();
 }
 
 template <int RT, int DT>
 static hipError_t launch_rt(const LayoutView& L, const Mx4Act& p, hipStream_t stream) {
   const Mx4Shape a = mx4_shape(L, p);
-  return launch_few<RT, DT, 1, 4>(p, static_cast<int>(a.col_blocks), mx4_grid(a), stream);
+  const int col_blocks = static_cast<int>(a.col_blocks);
+  if (a.few == 0) return launch_mx4_tiles(p, DT, col_blocks, mx4_grid(a), stream);
+  return launch_few<RT, DT, 1, 4>(p, col_blocks, mx4_grid(a), stream);
 }
 
 hipError_t launch_mx4_act(const LayoutView& L, const Mx4Act& p, int dtype, hipStream_t stream) {

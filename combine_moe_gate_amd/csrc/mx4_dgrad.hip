@@ -7,7 +7,6 @@
 //
 // A workgroup of four waves takes 64 rows by 64 input features, each wave 16 of the rows: 32 weight
 // rows at a time are widened into LDS.
-#include "expert_act.h"
 #include "mx4_product.h"
 
 namespace moe {

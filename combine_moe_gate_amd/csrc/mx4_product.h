@@ -1,8 +1,8 @@
-// What the products with 4-bit weights share: 16-bit matrix instructions and the exact forms in
-// which 4-bit weights meet f16 rows.
+// What the products with 4-bit weights share: matrix instructions, the exact forms in which 4-bit
+// weights meet f16 rows, and the ends of the epilogue.
 #pragma once
 
-#include "gemm_common.h"
+#include "expert_act.h"
 #include "mx4.h"
 
 namespace moe {
@@ -38,6 +38,50 @@ __device__ __forceinline__ void split_f16(const chunk_t& a, chunk_t& hi, chunk_t
     hi[i] = (h[0] >> 16) | h[1];
     lo[i] = (l[0] >> 16) | (l[1] & 0xffff0000u);
   }
+}
+
+typedef int i32x8_t __attribute__((ext_vector_type(8)));
+
+// A block of 4-bit codes per lane on each side, lane l's of row l % 16 and K block l / 16, with the
+// scales in byte SA of sa and byte SB of sb.
+template <int SA = 0, int SB = 0>
+__device__ __forceinline__ f32x4_t mfma_mx4(const chunk_t& a, uint32_t sa, const chunk_t& b, uint32_t sb, f32x4_t c) {
+  const i32x8_t va = {static_cast<int>(a.x), static_cast<int>(a.y), static_cast<int>(a.z), static_cast<int>(a.w), 0, 0, 0, 0};
+  const i32x8_t vb = {static_cast<int>(b.x), static_cast<int>(b.y), static_cast<int>(b.z), static_cast<int>(b.w), 0, 0, 0, 0};
+  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(va, vb, c, 4, 4, SA, static_cast<int>(sa), SB, static_cast<int>(sb));
+}
+
+// Eight output features, finished and stored: rounded to 16 bits, or to 4 with the block's other
+// 24 in the lane's group of four (lanes 4 i .. 4 i + 3 hold features c - c % 32 .. + 31 of a row).
+template <int DT>
+__device__ __forceinline__ void finish8_mx4(const Mx4Act& p, int x, int r, int t, float w, int c, float (&v)[8],
+                                            float (&u)[8]) {
+  epilogue8<DT>(p, x, r, t, w, c, v, u);
+  const size_t at = static_cast<size_t>(r) * p.n + c;
+  if (p.out_scales != nullptr) {
+    uint32_t E;
+    static_cast<uint32_t*>(p.out)[at / 8] = mx4_quantize8(v, &E);
+    if (c % 32 == 0) p.out_scales[at / 32] = static_cast<uint8_t>(E);
+  } else {
+    *reinterpret_cast<chunk_t*>(static_cast<uint16_t*>(p.out) + at) = pack<DT>(v);
+  }
+}
+
+__device__ __forceinline__ void zero_unfilled_mx4(const Mx4Act& p, int b, int nb) {
+  if (p.out_scales == nullptr) {
+    zero_unfilled(p, b, nb);
+    return;
+  }
+  each_unfilled(p, b, nb, [&](int r) {
+    const int blocks = p.n / kMx4Block;
+    chunk_t* o = static_cast<chunk_t*>(p.out) + static_cast<size_t>(r) * blocks;
+    uint8_t* s = p.out_scales + static_cast<size_t>(r) * blocks;
+    for (int c = lane_id(); c < blocks; c += kWave) {
+      o[c] = chunk_t{0u, 0u, 0u, 0u};
+      s[c] = 0;
+    }
+    clear_preact(p, r);
+  });
 }
 
 }  // namespace moe

@@ -122,6 +122,10 @@ struct Mx4Act : ExpertAct {
 };
 hipError_t launch_mx4_act(const LayoutView& L, const Mx4Act& p, int dtype, hipStream_t stream);
 bool mx4_act_fits(const LayoutView& L, const Mx4Act& p, int dtype);
+// Its form for long segments: tiles of at most so many rows, by 256 weight rows.
+constexpr int kMx4TileThreads = 512;
+int mx4_tile_rows();
+hipError_t launch_mx4_tiles(const Mx4Act& p, int dtype, int col_blocks, int64_t grid, hipStream_t stream);
 // Its input gradient: out[r] = a[r] @ W[x] with W [e, m, n] (m weight rows, n inputs): the struct's
 // a = the gradient rows [rows, m], out [rows, n], nz = n; no epilogue.
 hipError_t launch_mx4_dgrad(const LayoutView& L, const Mx4Act& p, int dtype, hipStream_t stream);
