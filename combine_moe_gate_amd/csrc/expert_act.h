@@ -298,6 +298,29 @@ __device__ __forceinline__ UnitTile unit_tile(int b, int e, const int32_t* __res
                   s.offset};
 }
 
+// Four weight fragments of a [K][N] stage: for tile j two transposing reads at at[j] and 4 K
+// rows (2048 bytes) on. They are written out with their wait because the compiler lets no
+// transposing read it knows start while direct-to-LDS loads are in flight, and those are in
+// flight nearly always.
+__device__ __forceinline__ void read_tr16(const uint32_t (&at)[4], chunk_t (&b)[4]) {
+  uint2 lo[4], hi[4];
+  asm volatile(
+      "ds_read_b64_tr_b16 %0, %8\n\t"
+      "ds_read_b64_tr_b16 %4, %8 offset:2048\n\t"
+      "ds_read_b64_tr_b16 %1, %9\n\t"
+      "ds_read_b64_tr_b16 %5, %9 offset:2048\n\t"
+      "ds_read_b64_tr_b16 %2, %10\n\t"
+      "ds_read_b64_tr_b16 %6, %10 offset:2048\n\t"
+      "ds_read_b64_tr_b16 %3, %11\n\t"
+      "ds_read_b64_tr_b16 %7, %11 offset:2048\n\t"
+      "s_waitcnt lgkmcnt(0)"
+      : "=&v"(lo[0]), "=&v"(lo[1]), "=&v"(lo[2]), "=&v"(lo[3]), "=&v"(hi[0]), "=&v"(hi[1]), "=&v"(hi[2]), "=&v"(hi[3])
+      : "v"(at[0]), "v"(at[1]), "v"(at[2]), "v"(at[3])
+      : "memory");
+#pragma unroll
+  for (int j = 0; j < 4; ++j) b[j] = chunk_t{lo[j].x, lo[j].y, hi[j].x, hi[j].y};
+}
+
 // f(0), f(1), ... with compile-time arguments.
 template <int... I, class F>
 __device__ __forceinline__ void static_for(std::integer_sequence<int, I...>, F f) {
