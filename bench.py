@@ -61,7 +61,7 @@ HOST_SOURCES = ("api.hip", "moe_gate.h")
 # kernels that no step of this benchmark launches: the balance loss and the expert
 # products with an epilogue
 OTHER_SOURCES = ("ops.h", "balance.hip", "expert_act.h", "expert_act.hip", "expert_act_bwd.hip", "mx4.h", "mx4_product.h",
-                 "mx4.hip", "mx4_act.hip", "mx4_tile.hip", "mx4_dgrad.hip")
+                 "mx4.hip", "mx4_act.hip", "mx4_tile.hip", "mx4_stream.hip", "mx4_dgrad.hip")
 
 
 _COMMENT = re.compile(rb"//[^\n]*|/\*.*?\*/", re.S)

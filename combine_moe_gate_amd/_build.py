@@ -20,7 +20,7 @@ ROOT = os.path.dirname(HERE)
 LIB_NAME = "libmoe_gate.so"
 LIB_PATH = os.path.join(HERE, LIB_NAME)
 SOURCES = [os.path.join(HERE, "csrc", f) for f in ("api.hip", "gate.hip", "layout.hip", "rows.hip", "gemm.hip", "gemm_bwd.hip",
-                                                     "balance.hip", "expert_act.hip", "expert_act_bwd.hip", "mx4.hip", "mx4_act.hip", "mx4_tile.hip",
+                                                     "balance.hip", "expert_act.hip", "expert_act_bwd.hip", "mx4.hip", "mx4_act.hip", "mx4_tile.hip", "mx4_stream.hip",
                                                      "mx4_dgrad.hip")]
 HEADERS = [os.path.join(HERE, "csrc", f) for f in ("internal.h", "moe_device.h", "gemm_common.h", "ops.h", "expert_act.h", "mx4.h",
                                                      "mx4_product.h")] + [

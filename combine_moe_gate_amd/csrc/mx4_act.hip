@@ -11,12 +11,11 @@
 // weights have in earnest); elsewhere each row value is split into two bf16 values, the upper 8
 // bits of its 11 and the rest, both products exact again.
 //
-// Two kernels, chosen by the rows an expert has on average: the tiles of mx4_tile.hip, and few rows:
-// a workgroup of four waves multiplies up to 16 F rows by 16 FB weight rows, each wave a
-// quarter of the K steps of four blocks: codes, scales and rows go from memory straight to the
-// registers, several steps ahead, and the four partial sums meet in LDS.
-#include <atomic>
-
+// Three kernels, chosen by the rows an expert has on average, the workgroups there would be and the
+// scales' alignment (mx4_shape() below): the tiles of mx4_tile.hip, the streams of mx4_stream.hip, and
+// here the form that takes rows and scales of any alignment: a workgroup of four waves multiplies up
+// to 16 F rows by 64 weight rows, each wave a quarter of the K steps of four blocks: codes, scales
+// and rows go from memory straight to the registers, and the four partial sums meet in LDS.
 #include "mx4_product.h"
 
 namespace moe {
@@ -26,13 +25,13 @@ namespace moe {
 
 constexpr int kMxFewThreads = 256, kMxFewWaves = 4, kMxFewBand = 8;
 
-// RT: the rows' type (kBF16, kF16 or kMx4); DT: the element type of bias, residual and results.
-template <int RT, int DT, int F, int FB>
-__global__ __launch_bounds__(kMxFewThreads, 2) void mx4_few_kernel(Mx4Act p, int col_blocks, int tile_grid) {
+// RT: the rows' type (kBF16, kF16 or kMx4); DT: the element type of bias, residual and results; kDepth:
+// the K steps in flight per wave.
+template <int RT, int DT, int F, int kDepth, int kOcc>
+__global__ __launch_bounds__(kMxFewThreads, kOcc) void mx4_few_kernel(Mx4Act p, int col_blocks, int tile_grid) {
   constexpr bool kQ = RT == kMx4;
   constexpr int kAChunks = kQ ? 1 : 4;                  // 16-byte pieces of a row's block
-  constexpr int kStepRegs = FB * 5 + F * (kQ ? 5 : 16);
-  constexpr int kDepth = kStepRegs <= 26 ? 4 : kStepRegs <= 40 ? 2 : 1;  // K steps in flight per wave
+  constexpr int FB = 4;
   constexpr int kCols = 16 * FB;                        // weight rows per workgroup
   constexpr int kPitch = kCols * 4 + 16;                // bytes per row of a wave's float32 sums
   extern __shared__ __attribute__((aligned(1024))) char lds[];  // [wave][16 F rows][kPitch]
@@ -52,18 +51,6 @@ __global__ __launch_bounds__(kMxFewThreads, 2) void mx4_few_kernel(Mx4Act p, int
   const int col0 = tc.cb * out_cols;
   const int kb = p.m / kMx4Block;
 
-  // lane l takes block 4 step + l / 16 of row l % 16 of each fragment; rows past the segment repeat
-  // its first one, whose results are not stored
-  const chunk_t* a_row[F];
-  const uint8_t* a_scale[F];
-#pragma unroll
-  for (int i = 0; i < F; ++i) {
-    const int r = i * 16 + (lane & 15);
-    const int rr = row0 + (r < nrows ? r : 0);
-    const size_t block = static_cast<size_t>(p.gather ? p.src[rr] : rr) * kb + g;
-    a_row[i] = static_cast<const chunk_t*>(p.a) + block * kAChunks;
-    a_scale[i] = p.a_scales + block;  // read for 4-bit rows only
-  }
   // The first half of the fragments are gate rows and the second the up rows that meet them, or all
   // are plain; each fragment by a uniform base and a lane's own offset in its 16 rows.
   const chunk_t* b_base[FB];
@@ -89,12 +76,32 @@ __global__ __launch_bounds__(kMxFewThreads, 2) void mx4_few_kernel(Mx4Act p, int
 
   chunk_t fb[kDepth][FB], fa[kDepth][F][kAChunks];
   uint32_t sb[kDepth][FB], sa[kDepth][F];
-  auto load = [&](int step, int d) {
+  auto load_b = [&](int step, int d) {
 #pragma unroll
     for (int j = 0; j < FB; ++j) {
       fb[d][j] = __builtin_nontemporal_load(b_base[j] + 4 * static_cast<size_t>(step) + b_off[j]);
       sb[d][j] = s_base[j][4 * static_cast<size_t>(step) + b_off[j]];
     }
+  };
+  const int full = kb / 4;  // whole K steps; wave wv takes steps wv, wv + 4, ...
+#pragma unroll
+  for (int d = 0; d < kDepth; ++d)
+    if (wv + d * kMxFewWaves < full) load_b(wv + d * kMxFewWaves, d);  // uniform
+  __builtin_amdgcn_sched_barrier(0);
+
+  // lane l takes block 4 step + l / 16 of row l % 16 of each fragment; rows past the segment repeat
+  // its first one, whose results are not stored
+  const chunk_t* a_row[F];
+  const uint8_t* a_scale[F];
+#pragma unroll
+  for (int i = 0; i < F; ++i) {
+    const int r = i * 16 + (lane & 15);
+    const int rr = row0 + (r < nrows ? r : 0);
+    const size_t block = static_cast<size_t>(p.gather ? p.src[rr] : rr) * kb + g;
+    a_row[i] = static_cast<const chunk_t*>(p.a) + block * kAChunks;
+    a_scale[i] = p.a_scales + block;  // read for 4-bit rows only
+  }
+  auto load_a = [&](int step, int d) {
 #pragma unroll
     for (int i = 0; i < F; ++i) {
 #pragma unroll
@@ -142,10 +149,13 @@ __global__ __launch_bounds__(kMxFewThreads, 2) void mx4_few_kernel(Mx4Act p, int
       }
     }
   };
-  const int full = kb / 4;  // whole K steps; wave wv takes steps wv, wv + 4, ...
+  auto load = [&](int step, int d) {
+    load_b(step, d);
+    load_a(step, d);
+  };
 #pragma unroll
   for (int d = 0; d < kDepth; ++d)
-    if (wv + d * kMxFewWaves < full) load(wv + d * kMxFewWaves, d);  // uniform
+    if (wv + d * kMxFewWaves < full) load_a(wv + d * kMxFewWaves, d);  // uniform
   int step = wv;
   for (; step + (2 * kDepth - 1) * kMxFewWaves < full; step += kDepth * kMxFewWaves) {  // every refill is a real step
 #pragma unroll
@@ -211,60 +221,91 @@ __global__ __launch_bounds__(kMxFewThreads, 2) void mx4_few_kernel(Mx4Act p, int
 // ---------------------------------------------------------------------------------
 // launches
 
-// How a launch is shaped: F of its row tiles (16 F rows; 0: the large tiles), the weight rows
+// How a launch is formed: the tiles, streams of 16 `few` rows, or this file's kernel, the weight rows
 // per workgroup, and its workgroups.
+enum class Mx4Form { tiles, stream, few };
 struct Mx4Shape {
-  int few, cols;
+  Mx4Form form;
+  int few;             // row tiles of 16 of a workgroup
   int64_t col_blocks, tiles;
 };
 
-static Mx4Shape mx4_shape(const LayoutView& L, const Mx4Act& p) {
-  auto shape = [&](int few) {
-    // 64 weight rows, so that a 4-bit block of 32 gated results lies in one workgroup
-    Mx4Shape a{few, few ? 64 : 256, 0, 0};
-    a.col_blocks = (static_cast<int64_t>(p.nz) + a.cols - 1) / a.cols;
-    a.tiles = L.s == 0 ? 0 : row_tiles(L, few ? 16 * few : mx4_tile_rows()) * a.col_blocks;
+// Streams read weights best (5.2 TB/s where the tiles reach 4.3); the tiles multiply best, once an
+// expert has rows to fill them and there are enough of them for the CUs. Microseconds, random rows,
+// bf16 and 4-bit (`mean` per expert; `tiles` as counted below):
+//                                          bf16: stream of           4-bit: stream of
+//   experts, weight rows x length   mean    16     32    tiles        16     32     64    tiles  (tiles)
+//   128, 4096 x 4096                1/16    17     21     61          14     14     15     20
+//   128, 2816 x 2816                8      112    127    313         103    104    106    126
+//   128, 2816 x 2816                16     138    131    315         129    113    115    128
+//   128, 2816 x 2816                32     206    166    326         176    135    121    136
+//   128, 2816 x 2816                64            244    357                190    148    151
+//   64, 2816 x 1408                 96            107    101                 72     58     52
+//   128, 2816 x 2816                128           422    447                320    226    175
+//   128, 2816 x 2816                256           770    608                594    376    253
+//   8, 1024 x 1024                  16     7.0    8.1     16         5.8    6.4    7.2    8.2
+//   16, 1024 x 1024                 256            24     38                 18     17     20    (120)
+//   8, 1024 x 2048                  1024           61     72                 39     33     30    (144)
+//   16, 1024 x 1024                 512            40     42                 29     24     22    (176)
+//   8, 512 x 512                    4000           50     31                 40     29     20    (238)
+// Rows that are no multiple of 128 elements, or unaligned scales, take this file's kernel in place of a
+// stream: 16 experts, 576 x 544, mean 125 in 9.1 and 7.2 (tiles 19 and 12). It takes 32 rows at a time,
+// of f16 16: beside more, the split form does not fit the registers (25 us where 32 rows take 39).
+constexpr int kMx4Mean16 = 112, kMx4Mean4 = 72;      // mean rows from which the tiles are worth while
+constexpr int64_t kMx4Tiles16 = 200, kMx4Tiles4 = 128;
+static Mx4Shape mx4_shape(const LayoutView& L, const Mx4Act& p, int dtype) {
+  const bool q = p.a_scales != nullptr;
+  auto shape = [&](Mx4Form form, int few, int height, int cols) {
+    Mx4Shape a{form, few, (static_cast<int64_t>(p.nz) + cols - 1) / cols, 0};
+    a.tiles = L.s == 0 ? 0 : row_tiles(L, height) * a.col_blocks;
     return a;
   };
+  const Mx4Shape large = shape(Mx4Form::tiles, 0, mx4_tile_rows(), 256);
   const int64_t routes = static_cast<int64_t>(L.s) * L.k;
   int64_t mean = (routes + L.e - 1) / L.e;
   if (L.capacity > 0 && mean > L.capacity) mean = L.capacity;
-  return shape(mean <= 16 ? 1 : 0);
+  const bool many = large.tiles >= (q ? kMx4Tiles4 : kMx4Tiles16);
+  if (many && mean >= (q ? kMx4Mean4 : kMx4Mean16)) return large;
+  const uintptr_t scales = reinterpret_cast<uintptr_t>(p.w_scales) | reinterpret_cast<uintptr_t>(p.a_scales);
+  if (p.m % 128 == 0 && scales % 4 == 0) {
+    const int few = mean <= (q ? 8 : 12) ? 1 : q && mean > 24 ? 4 : 2;
+    return shape(Mx4Form::stream, few, 16 * few, 128);
+  }
+  if (many && (q || mean > 32)) return large;
+  const int few = !q && dtype == kF16 ? 1 : 2;
+  // 64 weight rows, so that a 4-bit block of 32 gated results lies in one workgroup
+  return shape(Mx4Form::few, few, 16 * few, 64);
 }
 
 static int64_t mx4_grid(const Mx4Shape& a) { return (a.tiles + kXcds - 1) / kXcds * kXcds + kZeroBlocks; }
 
-bool mx4_act_fits(const LayoutView& L, const Mx4Act& p, int) {
-  const Mx4Shape a = mx4_shape(L, p);
-  return mx4_grid(a) <= most_workgroups(a.few ? kMxFewThreads : kMx4TileThreads);
+bool mx4_act_fits(const LayoutView& L, const Mx4Act& p, int dtype) {
+  const Mx4Shape a = mx4_shape(L, p, dtype);
+  static_assert(kMxFewThreads == kMx4StreamThreads);
+  return mx4_grid(a) <= most_workgroups(a.form == Mx4Form::tiles ? kMx4TileThreads : kMxFewThreads);
 }
 
-template <int RT, int DT, int F, int FB>
+template <int RT, int DT, int F, int kDepth, int kOcc>
 static hipError_t launch_few(const Mx4Act& p, int col_blocks, int64_t grid, hipStream_t stream) {
-  static std::atomic<uint64_t> done{0};
-  constexpr int kBytes = kMxFewWaves * 16 * F * (16 * FB * 4 + 16);
-  auto kern = mx4_few_kernel<RT, DT, F, FB>;
-  if (kBytes > 65536) {
-    const hipError_t err = allow_lds(reinterpret_cast<const void*>(kern), kBytes, done);
-    if (err != hipSuccess) return err;
-  }
-  kern<<<static_cast<unsigned>(grid), kMxFewThreads, kBytes, stream>>>(p, col_blocks, static_cast<int>(grid) - kZeroBlocks);
+  constexpr int kBytes = kMxFewWaves * 16 * F * (64 * 4 + 16);
+  static_assert(kBytes <= 65536);
+  mx4_few_kernel<RT, DT, F, kDepth, kOcc><<<static_cast<unsigned>(grid), kMxFewThreads, kBytes, stream>>>(
+      p, col_blocks, static_cast<int>(grid) - kZeroBlocks);
   return hipGetLastError();
-}
-
-template <int RT, int DT>
-static hipError_t launch_rt(const LayoutView& L, const Mx4Act& p, hipStream_t stream) {
-  const Mx4Shape a = mx4_shape(L, p);
-  const int col_blocks = static_cast<int>(a.col_blocks);
-  if (a.few == 0) return launch_mx4_tiles(p, DT, col_blocks, mx4_grid(a), stream);
-  return launch_few<RT, DT, 1, 4>(p, col_blocks, mx4_grid(a), stream);
 }
 
 hipError_t launch_mx4_act(const LayoutView& L, const Mx4Act& p, int dtype, hipStream_t stream) {
   if (p.rows == 0) return hipSuccess;
+  const Mx4Shape a = mx4_shape(L, p, dtype);
+  const int64_t grid = mx4_grid(a);
+  const int col_blocks = static_cast<int>(a.col_blocks);
+  if (a.form == Mx4Form::tiles) return launch_mx4_tiles(p, dtype, col_blocks, grid, stream);
+  if (a.form == Mx4Form::stream) return launch_mx4_stream(p, dtype, a.few, col_blocks, grid, stream);
   if (p.a_scales != nullptr)
-    return dtype == kBF16 ? launch_rt<kMx4, kBF16>(L, p, stream) : launch_rt<kMx4, kF16>(L, p, stream);
-  return dtype == kBF16 ? launch_rt<kBF16, kBF16>(L, p, stream) : launch_rt<kF16, kF16>(L, p, stream);
+    return dtype == kBF16 ? launch_few<kMx4, kBF16, 2, 2, 3>(p, col_blocks, grid, stream)
+                          : launch_few<kMx4, kF16, 2, 2, 3>(p, col_blocks, grid, stream);
+  return dtype == kBF16 ? launch_few<kBF16, kBF16, 2, 1, 3>(p, col_blocks, grid, stream)
+                        : launch_few<kF16, kF16, 1, 2, 2>(p, col_blocks, grid, stream);
 }
 
 }  // namespace moe

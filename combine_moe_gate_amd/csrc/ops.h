@@ -126,6 +126,10 @@ bool mx4_act_fits(const LayoutView& L, const Mx4Act& p, int dtype);
 constexpr int kMx4TileThreads = 512;
 int mx4_tile_rows();
 hipError_t launch_mx4_tiles(const Mx4Act& p, int dtype, int col_blocks, int64_t grid, hipStream_t stream);
+// Its form for few rows: 16 `few` (1, 2 or, of 4 bits, 4) rows by 128 weight rows; m a multiple of 128,
+// scales 4-byte aligned.
+constexpr int kMx4StreamThreads = 256;
+hipError_t launch_mx4_stream(const Mx4Act& p, int dtype, int few, int col_blocks, int64_t grid, hipStream_t stream);
 // Its input gradient: out[r] = a[r] @ W[x] with W [e, m, n] (m weight rows, n inputs): the struct's
 // a = the gradient rows [rows, m], out [rows, n], nz = n; no epilogue.
 hipError_t launch_mx4_dgrad(const LayoutView& L, const Mx4Act& p, int dtype, hipStream_t stream);

@@ -297,6 +297,29 @@ def test_every_tile_height(height, rows):
 
 
 @pytest.mark.parametrize("rows", ["16", "4"])
+@pytest.mark.parametrize("m,dtype", [(96, "bf16"), (544, "f16"), (768, "bf16"), (32, "f16")])
+def test_large_tiles_at_every_height(m, dtype, rows):
+    """Experts with as many rows as make every tile height, enough of them for the large tiles of either
+    row type, gated and not, with a last column tile that is partly there."""
+    announce("mx4 large tiles", m, dtype, rows)
+    idx = np.repeat(np.arange(len(HEIGHTS) + 1), [1, *HEIGHTS]).astype(np.int32)
+    idx = idx[np.random.default_rng(1).permutation(len(idx))][:, None]
+    run_case(idx, m, 864, len(HEIGHTS) + 1, 0, 1, False, dtype, rows, "silu", True, "own", True, "tokens", True, 7)
+    run_case(idx, m, 1672, len(HEIGHTS) + 1, 0, 1, False, dtype, rows, "gelu", False, "f32", False, None, False, 8)
+
+
+# rows an expert that ask for each height of the streams
+@pytest.mark.parametrize("rows", ["16", "4"])
+@pytest.mark.parametrize("m,dtype", [(128, "bf16"), (1408, "f16"), (2688, "bf16")])
+@pytest.mark.parametrize("s,n,gated", [(1, 64, True), (11, 136, False), (50, 200, False), (160, 96, True), (200, 160, False)])
+def test_streams(s, n, gated, m, dtype, rows):
+    announce("mx4 streams", s, n, gated, m, dtype, rows)
+    idx = W.random_idx(np.random.default_rng(m + s), s, 8, 3)
+    run_case(idx, m, n, 8, 0, 1, False, dtype, rows, "gelu_tanh", gated, "own", True, "rows", True, s)
+    run_case(idx, m, n, 8, 4 * s // 8 + 1, 1, True, dtype, rows, "relu", gated, "f32", False, "tokens", False, s)
+
+
+@pytest.mark.parametrize("rows", ["16", "4"])
 @pytest.mark.parametrize("n", [288, 1632])
 def test_uneven_segments(rows, n):
     """Segments of 1, 30, 33, 0, 700 and 64 rows beside each other."""
@@ -317,15 +340,14 @@ def test_every_k_tail(m, rows):
 
 
 @pytest.mark.parametrize("rows", ["16", "4"])
-@pytest.mark.parametrize("n", [96, 1536])
+@pytest.mark.parametrize("n,m", [(96, 160), (1536, 160), (96, 384), (4160, 160)])
 @pytest.mark.parametrize("s,e,k", [(1, 8, 4), (40, 8, 4), (300, 64, 4), (1500, 3, 2)])
 @pytest.mark.parametrize("dtype", ["bf16", "f16"])
-def test_whole_numbers_are_exact(s, e, k, n, dtype, rows):
+def test_whole_numbers_are_exact(s, e, k, n, m, dtype, rows):
     """Products of small whole numbers have exact sums in any order: all forms agree bit for bit. Results
     rounded to 4 bits are then those of the rounded results, whole numbers below 2^8 being bf16 values."""
-    announce("mx4 product integers", s, e, k, n, dtype, rows)
+    announce("mx4 product integers", s, e, k, n, m, dtype, rows)
     rng = np.random.default_rng(s)
-    m = 160
     idx = W.random_idx(rng, s, e, k)
     L, Lg = oracle.dispatch_layout(idx, e, 0), M.moe_dispatch_layout(to_dev(idx), e, 0)
     x = rng.integers(-2, 3, (s, m)).astype(np.float32)
@@ -361,10 +383,10 @@ def test_scales_of_every_size(dtype):
     of each row carries all of it, so that the results are exact."""
     announce("mx4 product scales", dtype)
     rng = np.random.default_rng(8)
-    e, m, k = 3, 512, 1
+    e, k = 3, 1
     lo, hi = (-24, 15) if dtype == "f16" else (-120, 120)
     draw = (lambda shape: 127 + rng.integers(-30, 25, shape)) if dtype == "f16" else lambda shape: 127 + rng.integers(-120, 121, shape)
-    for s, n in ((6, 32), (700, 1504)):
+    for s, n, m in ((6, 32, 512), (700, 1504, 512), (6, 32, 544), (200, 96, 544), (1400, 7456, 512)):  # streams, few rows, tiles
         idx = W.random_idx(rng, s, e, k)
         L, Lg = oracle.dispatch_layout(idx, e, 0), M.moe_dispatch_layout(to_dev(idx), e, 0)
         E_ = draw((e, 1, m // 32)).repeat(n, 1).astype(np.uint8)
@@ -395,8 +417,8 @@ def test_blocks_that_are_not_numbers_stay_where_they_are():
     through the K tail and the rows a tile repeats; infinities of 16-bit rows likewise."""
     announce("mx4 product nan")
     rng = np.random.default_rng(4)
-    for m in (96, 288):
-        for s, e, k, n in ((12, 8, 2, 160), (700, 3, 2, 160), (700, 3, 2, 1632)):
+    for m in (96, 288, 384):
+        for s, e, k, n in ((12, 8, 2, 160), (700, 3, 2, 160), (1500, 3, 2, 2080)):
             idx = W.random_idx(rng, s, e, k)
             idx[0], idx[1] = [0, 1], [1, 2]
             L, Lg = oracle.dispatch_layout(idx, e, 0), M.moe_dispatch_layout(to_dev(idx), e, 0)
@@ -451,8 +473,8 @@ def test_unaligned_scales():
     """Scale bytes at any address, of rows, weights and results."""
     announce("mx4 unaligned scales")
     rng = np.random.default_rng(9)
-    for s, n in ((9, 64), (600, 1536)):
-        e, m, k = 3, 544, 2
+    for s, n, m in ((9, 64, 544), (9, 64, 512), (600, 1536, 512), (1500, 4160, 544)):
+        e, k = 3, 2
         idx = W.random_idx(rng, s, e, k)
         Lg = M.moe_dispatch_layout(to_dev(idx), e, 0)
         xc, xs, _ = four_bits(rng, (s, m))
@@ -667,7 +689,7 @@ def test_captured_and_replayed_with_new_inputs():
     equal the eager results bit for bit."""
     announce("mx4 graph")
     rng = np.random.default_rng(31)
-    for s, m, n, e, k in ((3, 96, 64, 8, 2), (500, 128, 1056, 4, 2)):
+    for s, m, n, e, k in ((3, 96, 64, 8, 2), (500, 128, 1056, 4, 2), (3000, 256, 2048, 4, 2)):
         t = layer_inputs(rng, s, m, n, e, k, "bf16")
         idx, w = M.moe_gate_topk(t["logits"], k)
         t["w"] = w
