@@ -2,8 +2,9 @@
 //
 // For each placed row r of expert x: out[r] = a[r] @ W[x], a the 16-bit gradient rows [rows, nz], W
 // [nz, m] the values the codes stand for. The sum runs along the weights' rows, each with scales of
-// its own, so the weights are widened (to bf16, exact) on their way to LDS; f16 gradients are split
-// into two bf16 values each there, exact as well, for twice the products.
+// its own, so the weights are widened on their way to LDS: to bf16, which is exact, or for f16 gradients
+// to f16, exact for scales from 2^-23 to 2^13. A tile that met others is formed again from gradients in
+// two parts (split_f16) and bf16 weights, straight from memory: far slower, and in few registers.
 //
 // Tiles of up to 256 rows by 256 input features, eight waves, as in mx4_tile.hip: a step is 64 weight
 // rows. Each thread has one block of 32 weights of a step: loaded two steps ahead, widened and written
@@ -23,12 +24,14 @@ constexpr int kMdBand = 8;                         // row-blocks per band of the
 constexpr int kMdRowBytes = 128;                   // a staged gradient row: 64 elements
 constexpr int kMdAStage = 32 * kMdUnits * kMdRowBytes, kMdBStage = 64 * kMdBN * 2;
 constexpr int kMdB = 2 * kMdAStage;
-constexpr int kMdLds = kMdB + 2 * kMdBStage;
+constexpr int kMdVotes = kMdB + 2 * kMdBStage;
+constexpr int kMdLds = kMdVotes + 32;
 constexpr int kMdSlabPitch = 64 * 4 + 16;          // bytes per row of a wave's 16 x 64 float32 slab
-static_assert(8 * 2 * 16 * kMdSlabPitch <= kMdLds, "the slabs reuse the stages");
+static_assert(8 * 2 * 16 * kMdSlabPitch <= kMdVotes, "the slabs reuse the stages");
 
+// A tile of 32 FM rows; false if it is left to mx4_dgrad_split (f16 alone).
 template <int DT, int FM>
-__device__ __forceinline__ void mx4_dgrad_body(const Mx4Act& p, const UnitTile& tc, char* lds) {
+__device__ __forceinline__ bool mx4_dgrad_body(const Mx4Act& p, const UnitTile& tc, char* lds) {
   constexpr int FN = 4;
   // A step's products in order: (k32 half, row tile), 2 FM slots of FN MFMAs, cut into groups of up to
   // four slots whose fragments are read together; the last group lies in the second half.
@@ -50,6 +53,7 @@ __device__ __forceinline__ void mx4_dgrad_body(const Mx4Act& p, const UnitTile& 
   const size_t w0 = static_cast<size_t>(tc.expert) * K * kb + my_block;
   chunk_t breg;
   uint32_t sreg;
+  uint32_t reach = 0;  // f16: the largest distance from the least scale that fits
   auto load_b = [&](int kt) __attribute__((always_inline)) {
     const int r = kt * 64 + b_row;
     const size_t at = w0 + static_cast<size_t>(r < K ? r : K - 1) * kb;
@@ -61,13 +65,15 @@ __device__ __forceinline__ void mx4_dgrad_body(const Mx4Act& p, const UnitTile& 
   const int turn = (b_col >> 2) | ((b_row & 1) << 1);  // part q goes out as q ^ turn
   const int b_to = b_row * 512 + (((4 * b_col) ^ kn_swizzle(b_row) ^ turn) << 4);
   auto write_b = [&](int kt) __attribute__((always_inline)) {
-    const float s = mx4_scale(kt * 64 + b_row < K ? sreg : 127u);
+    const uint32_t E = kt * 64 + b_row < K ? sreg : 127u;
+    const float s = mx4_scale(E);
+    reach = mx4_f16_reach(E) > reach ? mx4_f16_reach(E) : reach;
     chunk_t c = breg;
     c = turn & 1 ? chunk_t{c.y, c.x, c.w, c.z} : c;
     c = turn & 2 ? chunk_t{c.z, c.w, c.x, c.y} : c;
     char* st = lds + kMdB + (kt % 2) * kMdBStage;
 #pragma unroll
-    for (int q = 0; q < 4; ++q) *reinterpret_cast<chunk_t*>(st + (b_to ^ (q << 4))) = mx4_values8<kBF16>(c[q], s);
+    for (int q = 0; q < 4; ++q) *reinterpret_cast<chunk_t*>(st + (b_to ^ (q << 4))) = mx4_values8<DT>(c[q], s);
   };
   load_b(0);
 
@@ -178,19 +184,9 @@ __device__ __forceinline__ void mx4_dgrad_body(const Mx4Act& p, const UnitTile& 
       for (int q = 0; q < 4; ++q) {
         const int slot = first_slot(g) + q;
         if (slot < first_slot(g + 1)) {
-          if constexpr (DT == kF16) {
-            chunk_t hi, lo;
-            split_f16(fa[g % 2][q], hi, lo);
 #pragma unroll
-            for (int j = 0; j < FN; ++j) {
-              acc[slot % FM][j] = mfma_16x16x32<kBF16>(fb[slot / FM][j], lo, acc[slot % FM][j]);
-              acc[slot % FM][j] = mfma_16x16x32<kBF16>(fb[slot / FM][j], hi, acc[slot % FM][j]);
-            }
-          } else {
-#pragma unroll
-            for (int j = 0; j < FN; ++j)
-              acc[slot % FM][j] = mfma_16x16x32<kBF16>(fb[slot / FM][j], fa[g % 2][q], acc[slot % FM][j]);
-          }
+          for (int j = 0; j < FN; ++j)
+            acc[slot % FM][j] = mfma_16x16x32<DT>(fb[slot / FM][j], fa[g % 2][q], acc[slot % FM][j]);
         }
       }
       __builtin_amdgcn_sched_barrier(0);
@@ -206,9 +202,21 @@ __device__ __forceinline__ void mx4_dgrad_body(const Mx4Act& p, const UnitTile& 
     }
   }
 
+  int* votes = reinterpret_cast<int*>(lds + kMdVotes);
+  if (DT == kF16) {
+    const bool misfit = __any(reach > kMx4F16Reach);
+    if (lane == 0) votes[wv] = misfit;
+  }
+  __syncthreads();
+  if constexpr (DT == kF16) {
+    int any = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) any |= votes[i];
+    if (__builtin_amdgcn_readfirstlane(any)) return false;
+  }
+
   // each 16-row tile's sums through one of the wave's two slabs: lane l holds row l % 16, features
   // 16 j + 4 (l / 16) .. + 3 of its 64; it takes back row l / 4, features 8 (l % 4) .. + 7 of each 32
-  __syncthreads();
   char* slabs = lds + wv * 2 * 16 * kMdSlabPitch;
   const int below = nrows - wm * 16 * FM;
 #pragma unroll
@@ -231,6 +239,45 @@ __device__ __forceinline__ void mx4_dgrad_body(const Mx4Act& p, const UnitTile& 
       }
     }
   }
+  return true;
+}
+
+// A tile whose weights f16 does not hold, 16 rows by 16 features of a wave at a time.
+__device__ __forceinline__ void mx4_dgrad_split(const Mx4Act& p, const UnitTile& tc) {
+  const int lane = lane_id(), wv = wave_in_block(), grp = lane >> 4, lrow = lane & 15;
+  const int row0 = tc.offset + tc.unit0 * 32;
+  const int rem = tc.rows - tc.unit0 * 32;
+  const int nrows = rem < 32 * tc.units ? rem : 32 * tc.units;
+  const int K = p.m, kb = p.n / kMx4Block;
+  const uint8_t* codes = static_cast<const uint8_t*>(p.w);
+  for (int item = wv; item < 2 * tc.units * (kMdBN / 16); item += kMdThreads / kWave) {
+    const int first = item / (kMdBN / 16) * 16, col = tc.cb * kMdBN + item % (kMdBN / 16) * 16;
+    if (first >= nrows || col >= p.n) continue;  // uniform; p.n is a multiple of 32
+    const int row = first + lrow;
+    const chunk_t* a_row = static_cast<const chunk_t*>(p.a) + static_cast<size_t>(row0 + (row < nrows ? row : 0)) * (K / 8);
+    const int c = col + lrow;
+    f32x4_t acc = {0.0f, 0.0f, 0.0f, 0.0f};
+    for (int k = 0; k < K; k += 32) {
+      const int k8 = k + 8 * grp;  // this lane's eight weight rows; K is a multiple of 8
+      chunk_t a = {0u, 0u, 0u, 0u}, w = a, hi, lo;
+      if (k8 < K) {
+        a = a_row[k8 / 8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const size_t block = (static_cast<size_t>(tc.expert) * K + k8 + i) * kb + c / kMx4Block;
+          const uint32_t code = (codes[block * 16 + c % kMx4Block / 2] >> (4 * (c % 2))) & 15u;
+          const f32x2_t v = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(code, mx4_scale(p.w_scales[block]), 0);
+          w[i / 2] |= (__float_as_uint(v[0]) >> 16) << (16 * (i % 2));  // a bf16 value
+        }
+      }
+      split_f16(a, hi, lo);
+      acc = mfma_16x16x32<kBF16>(w, lo, acc);
+      acc = mfma_16x16x32<kBF16>(w, hi, acc);
+    }
+    if (row < nrows)
+      *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + static_cast<size_t>(row0 + row) * p.n + col + 4 * grp) =
+          uint2{narrow2<kF16>(acc[0], acc[1]), narrow2<kF16>(acc[2], acc[3])};
+  }
 }
 
 template <int DT>
@@ -243,16 +290,19 @@ __global__ __launch_bounds__(kMdThreads) __attribute__((amdgpu_waves_per_eu(2, 2
   }
   const UnitTile tc = unit_tile<kMdUnits>(blockIdx.x, p.e, p.kept, p.offsets, col_blocks, kMdBand);
   if (tc.expert < 0) return;
+  bool done = true;
   switch (tc.units) {
-    case 1: mx4_dgrad_body<DT, 1>(p, tc, lds); break;
-    case 2: mx4_dgrad_body<DT, 2>(p, tc, lds); break;
-    case 3: mx4_dgrad_body<DT, 3>(p, tc, lds); break;
-    case 4: mx4_dgrad_body<DT, 4>(p, tc, lds); break;
-    case 5: mx4_dgrad_body<DT, 5>(p, tc, lds); break;
-    case 6: mx4_dgrad_body<DT, 6>(p, tc, lds); break;
-    case 7: mx4_dgrad_body<DT, 7>(p, tc, lds); break;
-    default: mx4_dgrad_body<DT, 8>(p, tc, lds); break;
+    case 1: done = mx4_dgrad_body<DT, 1>(p, tc, lds); break;
+    case 2: done = mx4_dgrad_body<DT, 2>(p, tc, lds); break;
+    case 3: done = mx4_dgrad_body<DT, 3>(p, tc, lds); break;
+    case 4: done = mx4_dgrad_body<DT, 4>(p, tc, lds); break;
+    case 5: done = mx4_dgrad_body<DT, 5>(p, tc, lds); break;
+    case 6: done = mx4_dgrad_body<DT, 6>(p, tc, lds); break;
+    case 7: done = mx4_dgrad_body<DT, 7>(p, tc, lds); break;
+    default: done = mx4_dgrad_body<DT, 8>(p, tc, lds); break;
   }
+  if constexpr (DT == kF16)
+    if (!done) mx4_dgrad_split(p, tc);
 }
 
 static int64_t mx4_dgrad_grid(const LayoutView& L, int m, int64_t* col_blocks) {

@@ -21,7 +21,9 @@ __device__ __forceinline__ f32x4_t mfma_16x16x32(const chunk_t& a, const chunk_t
 
 // Whether every value of a block with scale byte E is an f16 value: 0.5 2^(E - 127) is a multiple
 // of f16's smallest, 2^-24, and 6 2^(E - 127) is within its range.
-__device__ __forceinline__ bool mx4_fits_f16(uint32_t E) { return E - 104u <= 36u; }
+constexpr uint32_t kMx4F16Reach = 36u;
+__device__ __forceinline__ uint32_t mx4_f16_reach(uint32_t E) { return E - 104u; }
+__device__ __forceinline__ bool mx4_fits_f16(uint32_t E) { return mx4_f16_reach(E) <= kMx4F16Reach; }
 
 // Eight f16 values as the sums of two bf16 values each: the upper 8 of the 11 significant bits, and
 // the other 3. An infinity or NaN is all in the first.

@@ -16,7 +16,7 @@
 
 namespace moe {
 
-constexpr int kMsThreads = kMx4StreamThreads, kMsWaves = kMsThreads / kWave;
+constexpr int kMsThreads = kMx4StreamThreads;
 constexpr int kMsBN = 128;                         // weight rows per workgroup
 constexpr int kMsBand = 8;                         // row-blocks per band of the tile order
 constexpr int kMsPitch = kMsBN * 4 + 16;           // bytes per row of the float32 sums

@@ -33,8 +33,6 @@ constexpr int kMtSlabPitch = 64 * 4 + 16;          // bytes per row of a wave's 
 
 // The most units of 32 rows of a tile, its LDS in order: rows, weights, scales (two stages each), and
 // per row its token and route weight.
-constexpr int kMtSplit = 4;                        // beside the row types: f16 rows as pairs of bf16 values
-
 template <int RT>
 struct MtLds {
   static constexpr int kUnits = 9;
@@ -50,8 +48,8 @@ struct MtLds {
   static_assert(kBytes <= 160 * 1024);
 };
 
-// The tile's float32 sums, for a height of 32 FM rows. f16 rows (RT = kF16): true if some scale that
-// this wave met does not let f16 hold the weights; the sums are then to be formed again, split.
+// The tile's float32 sums, for a height of 32 FM rows. f16 rows: true if some scale that this wave met
+// does not let f16 hold the weights.
 template <int RT, int FM>
 __device__ __forceinline__ bool mx4_tile_products(const Mx4Act& p, const UnitTile& tc, char* lds, f32x4_t (&acc)[FM][4]) {
   using Lds = MtLds<RT>;
@@ -59,7 +57,7 @@ __device__ __forceinline__ bool mx4_tile_products(const Mx4Act& p, const UnitTil
   constexpr int FN = 4;
   // A step's products in order: (half, row tile), 2 FM slots of FN MFMAs, cut into groups of up to
   // four slots whose fragments are read together; the last group lies in the second half.
-  constexpr int kSlots = 2 * FM, kGroups = FM <= 4 ? 2 : (kSlots + 3) / 4;
+  constexpr int kSlots = 2 * FM, kGroups = FM <= 4 ? 2 : FM > 8 ? 6 : (kSlots + 3) / 4;
   auto first_slot = [](int g) constexpr { return g * kSlots / kGroups; };
   constexpr int kALoads = (4 * FM + 7) / 8;            // direct-to-LDS loads of 8 rows, per wave
   constexpr bool kMoreScales = kQ && FM > 8;           // rows whose scales have no thread of their own
@@ -103,7 +101,6 @@ __device__ __forceinline__ bool mx4_tile_products(const Mx4Act& p, const UnitTil
     __builtin_amdgcn_global_load_lds(static_cast<const void*>(from),
                                      (lds_void_t*)(lds + Lds::kB + (u % 2) * kMtBStage + (q * 8 + wv) * 1024), 16, 0, 0);
   };
-  // the weights' first loads start before the rows' addresses are read from the layout
 #pragma unroll
   for (int q = 0; q < 4; ++q) issue_b(0, q);
   if (kQ && nk > 1) {
@@ -111,6 +108,7 @@ __device__ __forceinline__ bool mx4_tile_products(const Mx4Act& p, const UnitTil
     for (int q = 0; q < 4; ++q) issue_b(1, q);
   }
   __builtin_amdgcn_sched_barrier(0);
+  // the rows are looked up before any load to LDS starts: the wait for them would be one for those as well
   uint32_t a_row[kALoads];
 #pragma unroll
   for (int q = 0; q < kALoads; ++q) a_row[q] = input_row((q * 8 + wv) * 8 + lane / 8);
@@ -183,18 +181,21 @@ __device__ __forceinline__ bool mx4_tile_products(const Mx4Act& p, const UnitTil
     sreg = v << (8 * (8 - kb));
     smore = more << (8 * (8 - kb));
   }
-  write_scales(0);
-  load_scales(1);
+  {  // the second stage's loads start before the first's are waited for
+    const uint64_t s0 = sreg, more0 = smore;
+    load_scales(1);
+    if (has_scale) put(0, s0, tid);
+    if (kMoreScales && tid < 32) put(0, more0, 512 + tid);
+  }
 
-  if constexpr (RT != kMtSplit) {  // per tile row: its token and route weight, for the epilogue
-    int* row_token = reinterpret_cast<int*>(lds + Lds::kRows);
-    float* row_weight = reinterpret_cast<float*>(lds + Lds::kRows + Lds::kBM * 4);
-    if (tid < nrows) {
-      const int r = row0 + tid;
-      const int t = p.src[r];
-      row_token[tid] = t;
-      row_weight[tid] = p.route_w != nullptr ? route_weight(p, r, t) : 1.0f;
-    }
+  // per tile row: its token and route weight, for the epilogue
+  int* row_token = reinterpret_cast<int*>(lds + Lds::kRows);
+  float* row_weight = reinterpret_cast<float*>(lds + Lds::kRows + Lds::kBM * 4);
+  if (tid < nrows) {
+    const int r = row0 + tid;
+    const int t = p.src[r];
+    row_token[tid] = t;
+    row_weight[tid] = p.route_w != nullptr ? route_weight(p, r, t) : 1.0f;
   }
 
 #pragma unroll
@@ -272,12 +273,12 @@ __device__ __forceinline__ bool mx4_tile_products(const Mx4Act& p, const UnitTil
         write_scales(u + 1);
         load_scales(u + 2);
       }
-      if (u + 1 < nu) {
+      if (u + 1 < nu) {  // all landed a step before their own: their first codes are read under the step before
         switch (t % 4) {  // uniform
-          case 0: issue_b(u + 1, 0); break;
-          case 1: issue_b(u + 1, 1); break;
-          case 2: issue_b(u + 1, 2); break;
-          default: issue_b(u + 1, 3); break;
+          case 0: issue_b(u + 1, 0); issue_b(u + 1, 1); break;
+          case 1: issue_b(u + 1, 2); break;
+          case 2: issue_b(u + 1, 3); break;
+          default: break;
         }
       }
     }
@@ -297,31 +298,28 @@ __device__ __forceinline__ bool mx4_tile_products(const Mx4Act& p, const UnitTil
   } else {
     read_codes(0, codes, sc);
   }
+  uint32_t reach = 0;  // f16 rows: the largest distance from the least scale that fits f16
   constexpr int kWide = RT == kF16 ? kF16 : kBF16;  // 16-bit rows: what the weights are widened to
   auto widen = [&](int half) __attribute__((always_inline)) {
 #pragma unroll
     for (int j = 0; j < FN; ++j) fb[half][j] = mx4_values8<kWide>(half == 0 ? codes[j].x : codes[j].y, mx4_scale(sc[j]));
   };
-  bool misfit = false;
+  if constexpr (!kQ) {
+    __builtin_amdgcn_s_waitcnt(kWaitLdsOnly);
+    widen(0);
+  }
 
   // Under each group's MFMAs the next group's fragments are read, and with the group before the
   // first one of the second half the weights' of that half. Before the last group's MFMAs the next
   // step is published (by then every fragment of this step is in registers), the loads of the one
   // after it start, and the next step's first fragments are read; after the last step these find old
-  // contents, which nothing uses.
+  // contents, which nothing uses. 16-bit rows: the second half's weights are widened among the first
+  // group's MFMAs, the next step's first among the last group's, from codes read after the first.
   for (int kt = 0; kt < nk; ++kt) {
 #pragma unroll
     for (int g = 0; g < kGroups; ++g) {
       __builtin_amdgcn_s_waitcnt(kWaitLdsOnly);  // this group's fragments have landed
       __builtin_amdgcn_sched_barrier(0);
-      if constexpr (!kQ) {
-        if (RT == kF16 && g == 0) {
-#pragma unroll
-          for (int j = 0; j < FN; ++j) misfit = misfit || !mx4_fits_f16(sc[j]);
-        }
-        if (g == 0) widen(0);
-        if (first_slot(g + 1) > FM && first_slot(g) <= FM) widen(1);  // the group that begins the second half
-      }
       if (g + 1 < kGroups) {
         read_a(kt, g + 1, fa[(g + 1) % 2]);
         if (kQ && first_slot(g + 1) <= FM && first_slot(g + 2) > FM) read_b(kt, 1, fb[1]);
@@ -335,8 +333,6 @@ __device__ __forceinline__ bool mx4_tile_products(const Mx4Act& p, const UnitTil
         if constexpr (kQ) {
           read_b(kt + 1, 0, fb[0]);  // the last group is all of the second half
           read_scales(kt + 1, sa[1], sb[1]);
-        } else {
-          read_codes(kt + 1, codes, sc);
         }
       }
       __builtin_amdgcn_sched_barrier(0);
@@ -367,21 +363,16 @@ __device__ __forceinline__ bool mx4_tile_products(const Mx4Act& p, const UnitTil
             }
           }
         });
-      } else if constexpr (RT == kMtSplit) {
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const int slot = first_slot(g) + q;
-          if (slot < first_slot(g + 1)) {
-            chunk_t hi, lo;
-            split_f16(fa[g % 2][q], hi, lo);
-#pragma unroll
-            for (int j = 0; j < FN; ++j) {
-              acc[slot % FM][j] = mfma_16x16x32<kBF16>(fb[slot / FM][j], lo, acc[slot % FM][j]);
-              acc[slot % FM][j] = mfma_16x16x32<kBF16>(fb[slot / FM][j], hi, acc[slot % FM][j]);
-            }
-          }
-        }
       } else {
+        if (g == 0) {
+          widen(1);
+          if (RT == kF16) {
+#pragma unroll
+            for (int j = 0; j < FN; ++j) reach = mx4_f16_reach(sc[j]) > reach ? mx4_f16_reach(sc[j]) : reach;
+          }
+        } else if (g + 1 == kGroups) {
+          widen(0);  // the next step's
+        }
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
           const int slot = first_slot(g) + q;
@@ -391,8 +382,19 @@ __device__ __forceinline__ bool mx4_tile_products(const Mx4Act& p, const UnitTil
               acc[slot % FM][j] = mfma_16x16x32<kWide>(fb[slot / FM][j], fa[g % 2][q], acc[slot % FM][j]);
           }
         }
+        if (g == 0 || g + 1 == kGroups) {  // the widening goes between the products
+#pragma unroll
+          for (int q = 0; q < 16; ++q) {
+            __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);  // a matrix instruction
+            __builtin_amdgcn_sched_group_barrier(0x002, 2, 0);  // two others
+          }
+        }
       }
       __builtin_amdgcn_sched_barrier(0);
+      if (!kQ && g == 0) {
+        read_codes(kt + 1, codes, sc);
+        __builtin_amdgcn_sched_barrier(0);
+      }
     }
     if (kGroups % 2 != 0) {
 #pragma unroll
@@ -405,12 +407,12 @@ __device__ __forceinline__ bool mx4_tile_products(const Mx4Act& p, const UnitTil
       for (int i = 0; i < 2; ++i) sb[0][i] = sb[1][i];
     }
   }
-  return __any(misfit);
+  return __any(reach > kMx4F16Reach);
 }
 
-// A tile of 32 FM rows.
+// A tile of 32 FM rows; false if it is left to mx4_tile_split (f16 rows alone).
 template <int RT, int DT, int FM>
-__device__ __forceinline__ void mx4_tile_body(const Mx4Act& p, const UnitTile& tc, char* lds) {
+__device__ __forceinline__ bool mx4_tile_body(const Mx4Act& p, const UnitTile& tc, char* lds) {
   using Lds = MtLds<RT>;
   constexpr int FN = 4;
   const int lane = lane_id(), wv = wave_in_block(), grp = lane >> 4;
@@ -432,7 +434,7 @@ __device__ __forceinline__ void mx4_tile_body(const Mx4Act& p, const UnitTile& t
     int any = 0;
 #pragma unroll
     for (int i = 0; i < 8; ++i) any |= votes[i];
-    if (__builtin_amdgcn_readfirstlane(any)) mx4_tile_products<kMtSplit, FM>(p, tc, lds, acc);
+    if (__builtin_amdgcn_readfirstlane(any)) return false;
   }
 
   // epilogue: each 16-row tile's sums through one of the wave's two slabs. Lane l holds token
@@ -480,6 +482,82 @@ __device__ __forceinline__ void mx4_tile_body(const Mx4Act& p, const UnitTile& t
     if (i + 2 < tiles) pass(i + 2, v[0], u[0]);
     if (i + 1 < tiles) finish(i + 1, v[1], u[1]);
   }
+  return true;
+}
+
+// A tile of f16 rows whose weights f16 does not hold: each row value in two parts (split_f16) times the
+// weights in bf16, 16 rows by 64 weight rows of a wave at a time, straight from memory. Several times
+// slower than the tile's own loop, in few registers: a second loop of that kind, next to the first,
+// would take registers from it (8192 rows of 4096: 2.5 ms where 2.0 are). Only weights with scales below
+// 2^-23 or above 2^13 come here.
+template <int DT>
+__device__ __forceinline__ void mx4_tile_split(const Mx4Act& p, const UnitTile& tc, char* lds) {
+  using Lds = MtLds<kF16>;
+  const int lane = lane_id(), wv = wave_in_block(), grp = lane >> 4, lrow = lane & 15;
+  const int wm = wv / 4, wn = wv % 4;
+  const int row0 = tc.offset + tc.unit0 * 32;
+  const int rem = tc.rows - tc.unit0 * 32;
+  const int nrows = rem < 32 * tc.units ? rem : 32 * tc.units;
+  const int out_cols = p.gated ? kMtBN / 2 : kMtBN;
+  const int col0 = tc.cb * out_cols, kb = p.m / kMx4Block;
+  const int* row_token = reinterpret_cast<const int*>(lds + Lds::kRows);
+  const float* row_weight = reinterpret_cast<const float*>(lds + Lds::kRows + Lds::kBM * 4);
+  char* slab = lds + wv * 16 * kMtSlabPitch;
+  size_t block[4];  // of this lane's weight rows, as the tile stages them: gated, 32 gate rows and their up rows
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    int f = p.gated ? col0 + wn * 32 + (j % 2) * 16 + lrow : col0 + wn * 64 + j * 16 + lrow;
+    f = (f < p.n ? f : p.n - 1) + (p.gated && j >= 2 ? p.n : 0);
+    block[j] = (static_cast<size_t>(tc.expert) * p.nz + f) * kb + grp;
+  }
+  for (int i = 0; i < tc.units; ++i) {
+    const int first = (wm * tc.units + i) * 16;
+    if (first >= nrows) return;  // uniform
+    const int rr = row0 + (first + lrow < nrows ? first + lrow : 0);
+    const chunk_t* a_row = static_cast<const chunk_t*>(p.a) + (static_cast<size_t>(p.gather ? p.src[rr] : rr) * kb + grp) * 4;
+    f32x4_t acc[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) acc[j] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+    for (int b = 0; b < kb; b += 4) {
+      const bool in = b + grp < kb;  // past the row's end: zeros
+      chunk_t codes[4], a[4];
+      uint32_t E[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        codes[j] = in ? static_cast<const chunk_t*>(p.w)[block[j] + b] : chunk_t{0u, 0u, 0u, 0u};
+        E[j] = in ? p.w_scales[block[j] + b] : 127u;
+        a[j] = in ? a_row[4 * b + j] : chunk_t{0u, 0u, 0u, 0u};
+      }
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        chunk_t hi, lo;
+        split_f16(a[q], hi, lo);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const chunk_t w = mx4_values8<kBF16>(codes[j][q], mx4_scale(E[j]));
+          acc[j] = mfma_16x16x32<kBF16>(w, lo, acc[j]);
+          acc[j] = mfma_16x16x32<kBF16>(w, hi, acc[j]);
+        }
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) *reinterpret_cast<f32x4_t*>(slab + lrow * kMtSlabPitch + j * 64 + grp * 16) = acc[j];
+    const float* back = reinterpret_cast<const float*>(slab + (lane >> 2) * kMtSlabPitch) + 8 * (lane & 3);
+    float v[8], u[8];
+#pragma unroll
+    for (int q = 0; q < 8; ++q) {
+      v[q] = back[q];
+      u[q] = back[32 + q];
+    }
+    const int row = first + (lane >> 2);
+    if (row < nrows) {
+      const int c = col0 + wn * (out_cols / 4) + 8 * (lane & 3);
+      const int t = row_token[row];
+      const float w = row_weight[row];
+      if (c < p.n) finish8_mx4<DT>(p, tc.expert, row0 + row, t, w, c, v, u);
+      if (!p.gated && c + 32 < p.n) finish8_mx4<DT>(p, tc.expert, row0 + row, t, w, c + 32, u, v);
+    }
+  }
 }
 
 template <int RT, int DT>
@@ -493,17 +571,20 @@ __global__ __launch_bounds__(kMtThreads) __attribute__((amdgpu_waves_per_eu(2, 2
   constexpr int kUnits = MtLds<RT>::kUnits;
   const UnitTile tc = unit_tile<kUnits>(blockIdx.x, p.e, p.kept, p.offsets, col_blocks, kMtBand);
   if (tc.expert < 0) return;
+  bool done = true;
   switch (tc.units) {
-    case 1: mx4_tile_body<RT, DT, 1>(p, tc, lds); break;
-    case 2: mx4_tile_body<RT, DT, 2>(p, tc, lds); break;
-    case 3: mx4_tile_body<RT, DT, 3>(p, tc, lds); break;
-    case 4: mx4_tile_body<RT, DT, 4>(p, tc, lds); break;
-    case 5: mx4_tile_body<RT, DT, 5>(p, tc, lds); break;
-    case 6: mx4_tile_body<RT, DT, 6>(p, tc, lds); break;
-    case 7: mx4_tile_body<RT, DT, 7>(p, tc, lds); break;
-    case 8: mx4_tile_body<RT, DT, 8>(p, tc, lds); break;
-    default: mx4_tile_body<RT, DT, 9>(p, tc, lds); break;
+    case 1: done = mx4_tile_body<RT, DT, 1>(p, tc, lds); break;
+    case 2: done = mx4_tile_body<RT, DT, 2>(p, tc, lds); break;
+    case 3: done = mx4_tile_body<RT, DT, 3>(p, tc, lds); break;
+    case 4: done = mx4_tile_body<RT, DT, 4>(p, tc, lds); break;
+    case 5: done = mx4_tile_body<RT, DT, 5>(p, tc, lds); break;
+    case 6: done = mx4_tile_body<RT, DT, 6>(p, tc, lds); break;
+    case 7: done = mx4_tile_body<RT, DT, 7>(p, tc, lds); break;
+    case 8: done = mx4_tile_body<RT, DT, 8>(p, tc, lds); break;
+    default: done = mx4_tile_body<RT, DT, 9>(p, tc, lds); break;
   }
+  if constexpr (RT == kF16)
+    if (!done) mx4_tile_split<DT>(p, tc, lds);
 }
 
 int mx4_tile_rows() { return MtLds<kMx4>::kBM; }

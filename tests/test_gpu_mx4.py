@@ -386,7 +386,7 @@ def test_scales_of_every_size(dtype):
     e, k = 3, 1
     lo, hi = (-24, 15) if dtype == "f16" else (-120, 120)
     draw = (lambda shape: 127 + rng.integers(-30, 25, shape)) if dtype == "f16" else lambda shape: 127 + rng.integers(-120, 121, shape)
-    for s, n, m in ((6, 32, 512), (700, 1504, 512), (6, 32, 544), (200, 96, 544), (1400, 7456, 512)):  # streams, few rows, tiles
+    for s, n, m in ((6, 32, 512), (700, 1504, 512), (6, 32, 544), (200, 96, 544), (1400, 7456, 512), (1400, 7456, 160)):  # streams, few rows, tiles
         idx = W.random_idx(rng, s, e, k)
         L, Lg = oracle.dispatch_layout(idx, e, 0), M.moe_dispatch_layout(to_dev(idx), e, 0)
         E_ = draw((e, 1, m // 32)).repeat(n, 1).astype(np.uint8)
