@@ -625,19 +625,23 @@ def moe_expert_act_dgrad(layout: Layout, grad_preact: torch.Tensor, weights: tor
 _MX4_BLOCK = 32
 
 
-def _expect_mx4(pair, name: str, shape) -> None:
-    """Check a (codes, scales) pair that stands for values of `shape` (None matches any size)."""
-    if not isinstance(pair, (tuple, list)) or len(pair) != 2:
+def _expect_mx4(pair, name: str, shape) -> int:
+    """Check a (codes, scales) pair that stands for values of `shape` (None matches any size); the length
+    of its rows."""
+    if type(pair) is not tuple and type(pair) is not list or len(pair) != 2:
         raise TypeError(f"{name} must be a (codes, scales) pair, as moe_mx4_quantize returns")
     codes, scales = pair
     for t, part in ((codes, "codes"), (scales, "scales")):
-        if t is None:
-            raise TypeError(f"{name}: {part} must be a torch.Tensor, got None")
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{name}: {part} must be a torch.Tensor, got {type(t).__name__}")
     m = shape[-1]
     _expect(codes, f"{name}: codes", (*shape[:-1], None if m is None else m // 2), torch.uint8)
-    if codes.shape[-1] % (_MX4_BLOCK // 2):
-        raise ValueError(f"{name}: codes must have whole blocks of {_MX4_BLOCK // 2} bytes a row, got {codes.shape[-1]}")
-    _expect(scales, f"{name}: scales", (*codes.shape[:-1], codes.shape[-1] // (_MX4_BLOCK // 2)), torch.uint8)
+    *lead, half = codes.shape
+    if half == 0 or half % (_MX4_BLOCK // 2):
+        raise ValueError(f"{name}: codes must have whole blocks of {_MX4_BLOCK // 2} bytes a row, got {half}")
+    if scales.dtype is not torch.uint8 or scales.shape != (*lead, half // (_MX4_BLOCK // 2)):
+        _expect(scales, f"{name}: scales", (*lead, half // (_MX4_BLOCK // 2)), torch.uint8)
+    return 2 * half
 
 
 def moe_mx4_quantize(x: torch.Tensor, codes=None, scales=None):
@@ -650,17 +654,20 @@ def moe_mx4_quantize(x: torch.Tensor, codes=None, scales=None):
     infinity or NaN gets scale 255 and reads back as NaN. codes, scales: tensors to write to."""
     if not isinstance(x, torch.Tensor):
         raise TypeError(f"x must be a torch.Tensor, got {type(x).__name__}")
-    if x.dim() < 1 or x.shape[-1] % _MX4_BLOCK or x.shape[-1] == 0:
+    *lead, m = x.shape or (0,)
+    if m == 0 or m % _MX4_BLOCK:
         raise ValueError(f"x must have rows of whole blocks of {_MX4_BLOCK} values, got shape {list(x.shape)}")
-    lead, m = x.shape[:-1], x.shape[-1]
-    _expect(x, "x", x.shape, _ROW_DTYPES)
-    _expect(codes, "codes", (*lead, m // 2), torch.uint8)
-    _expect(scales, "scales", (*lead, m // _MX4_BLOCK), torch.uint8)
+    if x.dtype not in _DTYPE_CODE:
+        _expect(x, "x", x.shape, _ROW_DTYPES)
+    if codes is not None:
+        _expect(codes, "codes", (*lead, m // 2), torch.uint8)
+    if scales is not None:
+        _expect(scales, "scales", (*lead, m // _MX4_BLOCK), torch.uint8)
     _one_device(x, codes, scales)
     if codes is None:
-        codes = torch.empty((*lead, m // 2), dtype=torch.uint8, device=x.device)
+        codes = x.new_empty((*lead, m // 2), dtype=torch.uint8)
     if scales is None:
-        scales = torch.empty((*lead, m // _MX4_BLOCK), dtype=torch.uint8, device=x.device)
+        scales = x.new_empty((*lead, m // _MX4_BLOCK), dtype=torch.uint8)
     _launch(x, lib().moe_mx4_quantize, x.data_ptr(), x.numel() // m, m, _DTYPE_CODE[x.dtype], codes.data_ptr(), scales.data_ptr())
     return codes, scales
 
@@ -670,18 +677,17 @@ def moe_mx4_dequantize(codes: torch.Tensor, scales: torch.Tensor, dtype: torch.d
     moe_mx4_quantize), in dtype (or out's): exact in float32 and bfloat16, rounded once in float16."""
     if not isinstance(codes, torch.Tensor):
         raise TypeError(f"codes must be a torch.Tensor, got {type(codes).__name__}")
-    if codes.dim() < 1 or codes.shape[-1] == 0:
-        raise ValueError(f"codes must have rows of whole blocks, got shape {list(codes.shape)}")
-    _expect_mx4((codes, scales), "codes", codes.shape[:-1] + (2 * codes.shape[-1],))
-    m = 2 * codes.shape[-1]
+    *lead, half = codes.shape or (0,)
+    m = _expect_mx4((codes, scales), "codes", (*lead, 2 * half))
     if out is not None:
         dtype = out.dtype if isinstance(out, torch.Tensor) else dtype
     if dtype not in _DTYPE_CODE:
         raise ValueError(f"unsupported element type {dtype}")
-    _expect(out, "out", (*codes.shape[:-1], m), dtype)
+    if out is not None:
+        _expect(out, "out", (*lead, m), dtype)
     _one_device(codes, scales, out)
     if out is None:
-        out = torch.empty((*codes.shape[:-1], m), dtype=dtype, device=codes.device)
+        out = codes.new_empty((*lead, m), dtype=dtype)
     _launch(codes, lib().moe_mx4_dequantize, codes.data_ptr(), scales.data_ptr(), out.numel() // m, m, _DTYPE_CODE[dtype],
             out.data_ptr())
     return out
@@ -698,12 +704,11 @@ def moe_mx4_expert_gemm(layout: Layout, a, weights, gather: bool = True, bias=No
     given; with 16-bit rows it is theirs). quantize_out: the result is a (codes, scales) pair, the float32
     results rounded once to 4 bits (n a multiple of 32), for a next product; out is then such a pair.
     Everything else as in moe_expert_gemm_act; with save_preact (or preact given) returns (out, preact)."""
-    rows = layout.s if gather else layout.rows
-    pair = isinstance(a, (tuple, list))
-    if pair:
-        _expect_mx4(a, "a", (rows, None))
+    s, total = layout.s, layout.rows
+    rows = s if gather else total
+    if type(a) is tuple or type(a) is list:
+        m = _expect_mx4(a, "a", (rows, None))
         codes, a_scales = a
-        m = 2 * codes.shape[1]
         dtype = torch.bfloat16 if dtype is None else dtype
         if dtype not in _GEMM_DTYPES:
             raise ValueError(f"dtype must be bfloat16 or float16, got {dtype}")
@@ -712,49 +717,64 @@ def moe_mx4_expert_gemm(layout: Layout, a, weights, gather: bool = True, bias=No
     else:
         _expect(a, "a", (rows, None), _GEMM_DTYPES)
         codes, a_scales, m = a, None, a.shape[1]
-        if dtype not in (None, a.dtype):
+        if dtype is not None and dtype is not a.dtype:
             raise ValueError(f"dtype must be that of the rows, {a.dtype}, got {dtype}")
         dtype = a.dtype
-    if m == 0 or m % _MX4_BLOCK:
-        raise ValueError(f"rows must be whole blocks of {_MX4_BLOCK} values, got {m}")
-    _expect_mx4(weights, "weights", (layout.e, None, m))
-    nz = weights[0].shape[1]
+        if m == 0 or m % _MX4_BLOCK:
+            raise ValueError(f"rows must be whole blocks of {_MX4_BLOCK} values, got {m}")
+    e = layout.e
+    _expect_mx4(weights, "weights", (e, None, m))
+    w_codes, w_scales = weights
+    nz = w_codes.shape[1]
     if gated and nz % 2:
         raise ValueError(f"gated weights must have an even number of rows, got {nz}")
     n = nz // 2 if gated else nz
-    _expect(bias, "bias", (layout.e, nz), (torch.float32, dtype))
     code = _activation(act)
-    _expect(w, "w", (layout.s, layout.k), torch.float32)
-    _expect(residual, "residual", (layout.s if residual_gather else layout.rows, n), dtype)
-    if quantize_out and n % _MX4_BLOCK:
-        raise ValueError(f"quantize_out: the {n} results of a row must be whole blocks of {_MX4_BLOCK}")
+    others = [codes, w_codes, w_scales]  # every tensor of the call
+    if a_scales is not None:
+        others.append(a_scales)
+    if bias is not None:
+        _expect(bias, "bias", (e, nz), (torch.float32, dtype))
+        others.append(bias)
+    if w is not None:
+        _expect(w, "w", (s, layout.k), torch.float32)
+        others.append(w)
+    if residual is not None:
+        _expect(residual, "residual", (s if residual_gather else total, n), dtype)
+        others.append(residual)
+    out_scales = None
     if quantize_out:
+        if n % _MX4_BLOCK:
+            raise ValueError(f"quantize_out: the {n} results of a row must be whole blocks of {_MX4_BLOCK}")
         if out is not None:
-            _expect_mx4(out, "out", (layout.rows, n))
-        out_codes, out_scales = (None, None) if out is None else out
-    else:
-        _expect(out, "out", (layout.rows, n), dtype)
-        out_codes, out_scales = out, None
+            _expect_mx4(out, "out", (total, n))
+            out, out_scales = out
+            others += out, out_scales
+    elif out is not None:
+        _expect(out, "out", (total, n), dtype)
+        others.append(out)
     if preact_dtype is None:
         preact_dtype = dtype if preact is None else (dtype, torch.float32)
-    elif preact_dtype not in (dtype, torch.float32):
+    elif preact_dtype is not dtype and preact_dtype is not torch.float32:
         raise ValueError(f"preact_dtype must be float32 or {dtype}, got {preact_dtype}")
-    _expect(preact, "preact", (layout.rows, nz), preact_dtype)
-    _same_device(layout, codes, a_scales, weights[0], weights[1], bias, w, residual, out_codes, out_scales, preact)
-    if out_codes is None:
+    if preact is not None:
+        _expect(preact, "preact", (total, nz), preact_dtype)
+        others.append(preact)
+    _same_device(layout, *others)
+    if out is None:
         if quantize_out:
-            out_codes = torch.empty((layout.rows, n // 2), dtype=torch.uint8, device=codes.device)
-            out_scales = torch.empty((layout.rows, n // _MX4_BLOCK), dtype=torch.uint8, device=codes.device)
+            out = codes.new_empty((total, n // 2), dtype=torch.uint8)
+            out_scales = codes.new_empty((total, n // _MX4_BLOCK), dtype=torch.uint8)
         else:
-            out_codes = torch.empty((layout.rows, n), dtype=dtype, device=codes.device)
+            out = codes.new_empty((total, n), dtype=dtype)
     if save_preact and preact is None:
-        preact = torch.empty((layout.rows, nz), dtype=preact_dtype, device=codes.device)
-    ep = Epilogue(code, int(bool(gated)), _ptr(bias), _DTYPE_CODE[bias.dtype] if bias is not None else MOE_F32,
-                  int(bool(residual_gather)), _ptr(w), _ptr(residual), _ptr(preact))
-    _launch(codes, lib().moe_mx4_expert_gemm, layout.byref(), _ptr(codes), _ptr(a_scales), int(bool(gather)), _ptr(weights[0]),
-            _ptr(weights[1]), m, n, _DTYPE_CODE[dtype], ctypes.byref(ep), _DTYPE_CODE[dtype if preact is None else preact.dtype],
-            _ptr(out_codes), _ptr(out_scales))
-    result = (out_codes, out_scales) if quantize_out else out_codes
+        preact = codes.new_empty((total, nz), dtype=preact_dtype)
+    ep = Epilogue(code, 1 if gated else 0, _ptr(bias), MOE_F32 if bias is None else _DTYPE_CODE[bias.dtype],
+                  1 if residual_gather else 0, _ptr(w), _ptr(residual), _ptr(preact))
+    _launch(codes, lib().moe_mx4_expert_gemm, layout.byref(), codes.data_ptr(), _ptr(a_scales), 1 if gather else 0,
+            w_codes.data_ptr(), w_scales.data_ptr(), m, n, _DTYPE_CODE[dtype], ctypes.byref(ep),
+            _DTYPE_CODE[dtype if preact is None else preact.dtype], out.data_ptr(), _ptr(out_scales))
+    result = (out, out_scales) if quantize_out else out
     return result if preact is None else (result, preact)
 
 
@@ -765,8 +785,7 @@ def moe_mx4_expert_dgrad(layout: Layout, grad_preact: torch.Tensor, weights, out
     gathered forward is moe_dispatch_backward(layout, grad_a)."""
     _expect(grad_preact, "grad_preact", (layout.rows, None), _GEMM_DTYPES)
     nz = grad_preact.shape[1]
-    _expect_mx4(weights, "weights", (layout.e, nz, None))
-    m = 2 * weights[0].shape[2]
+    m = _expect_mx4(weights, "weights", (layout.e, nz, None))
     _expect(out, "out", (layout.rows, m), grad_preact.dtype)
     _same_device(layout, grad_preact, weights[0], weights[1], out)
     out = out if out is not None else torch.empty((layout.rows, m), dtype=grad_preact.dtype, device=grad_preact.device)
