@@ -61,9 +61,12 @@ __global__ __launch_bounds__(kMsThreads) void mx4_stream_kernel(Mx4Act p, int co
   const int achunks = kQ ? kb : 4 * kb;                // 16-byte pieces of a row
   const int nu = (kb + 7) / 8;
 
-  // rows: 16-bit ones fill two of 512 bytes a load, piece slot ^ (row % 16) of 32 at each slot; 4-bit
-  // ones eight of 128 bytes, swizzled as the codes. Rows past the segment repeat its first. They are
+  // rows: 16-bit ones fill two of 512 bytes a load, piece slot ^ a_swizzle(row % 16) of 32 at each slot
+  // (lanes of rows 0-3 and 12-15 of one group and 4-11 of the next read together, four pieces apart:
+  // the order of the rows' fours keeps them on different banks); 4-bit ones eight of 128 bytes,
+  // swizzled as the codes. Rows past the segment repeat its first. They are
   // looked up before any load to LDS starts: the wait for them would be one for those as well.
+  auto a_swizzle = [](int r) { return 4 * ((0x78 >> (r / 4 * 2)) & 3) + r % 4; };
   auto input_row = [&](int r) {
     const int rr = row0 + (r < nrows ? r : 0);
     return static_cast<size_t>(p.gather ? p.src[rr] : rr);
@@ -74,7 +77,7 @@ __global__ __launch_bounds__(kMsThreads) void mx4_stream_kernel(Mx4Act p, int co
   for (int q = 0; q < Lds::kALoads; ++q) {
     a_load[q] = kQ ? (q * 4 + wv) % (2 * FR) : q * 4 + wv;  // fewer loads than waves: some are issued twice
     const int r = kQ ? a_load[q] * 8 + lane / 8 : a_load[q] * 2 + lane / 32;
-    a_piece[q] = kQ ? (lane % 8) ^ (r / 2 % 8) : (lane % 32) ^ (r % 16);
+    a_piece[q] = kQ ? (lane % 8) ^ (r / 2 % 8) : (lane % 32) ^ a_swizzle(r % 16);
     a_row[q] = static_cast<const chunk_t*>(p.a) + input_row(r) * achunks;
   }
   const int as_load = kQ ? wv % (FR == 4 ? 2 : 1) : 0;
@@ -139,7 +142,7 @@ __global__ __launch_bounds__(kMsThreads) void mx4_stream_kernel(Mx4Act p, int co
 #pragma unroll
     for (int j = 0; j < 2; ++j) acc[i][j] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
 
-  const int lrow = lane & 15;
+  const int lrow = lane & 15, a_swz = a_swizzle(lrow);
   const int word_at = wv * 32 + lrow;  // staged weight row of this lane's first fragment
   for (int u = 0; u < nu; ++u) {
     // stage u has landed; up to S - 2 later ones may be in flight
@@ -184,7 +187,7 @@ __global__ __launch_bounds__(kMsThreads) void mx4_stream_kernel(Mx4Act p, int co
         for (int i = 0; i < FR; ++i)
 #pragma unroll
           for (int q = 0; q < 4; ++q)
-            a[i][q] = *reinterpret_cast<const chunk_t*>(st + (16 * i + lrow) * 512 + (((4 * (4 * h + grp) + q) ^ lrow) << 4));
+            a[i][q] = *reinterpret_cast<const chunk_t*>(st + (16 * i + lrow) * 512 + (((4 * (4 * h + grp) + q) ^ a_swz) << 4));
         bool split = false;
         if constexpr (RT == kF16) split = !__all(mx4_fits_f16(sb[0] & 255u) && mx4_fits_f16(sb[1] & 255u));
         constexpr int kWide = RT == kF16 ? kF16 : kBF16;

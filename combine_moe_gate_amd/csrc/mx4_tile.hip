@@ -9,10 +9,11 @@
 // loads of the stage after it start there.
 //
 // 4-bit rows: a step is 256 elements of both sides. In the products of half h lane group g = lane / 16
-// multiplies block 2 g + h of the step, so that the two scales it needs of a row lie side by side.
+// multiplies block 4 h + g of the step.
 // 16-bit rows: a step is 64 elements of the rows and a quarter of a 256-element stage of the weights;
-// of step p group g takes elements 64 p + 16 g + 8 h .. + 7 in half h, which lie in one block, and
-// widens its weights after they are read from LDS.
+// in half h of step p group g takes elements 8 g .. + 7 of the stage's block 2 p + h, and widens its
+// weights after they are read from LDS.
+// (With block 2 g + h, and elements 16 g + 8 h, an LDS read of rows would meet every bank twice.)
 //
 // Scales go through registers (a row's may start at any byte) to LDS, 8 bytes a staged row and 256
 // elements, a step later than loaded and a step before they are read. For 4-bit rows they lie there as
@@ -144,7 +145,7 @@ __device__ __forceinline__ bool mx4_tile_products(const Mx4Act& p, const UnitTil
     if (has_scale) sreg = *reinterpret_cast<const bytes8_t*>(s_from + first(u));
     if (kMoreScales && tid < 32) smore = *reinterpret_cast<const bytes8_t*>(s_more + first(u));
   };
-  // of staged row R's bytes, those of block pair i (blocks 2 i, 2 i + 1) go to scale_at(R) + 4 i; 16-bit
+  // of staged row R's bytes, those of lane group i (blocks i and 4 + i) go to scale_at(R) + 4 i; 16-bit
   // rows: the weights' as they are, row by row
   auto pair_row = [](int region, int tile, int row) { return ((region + tile / 2) * 16 + row) * 16 + (tile % 2) * 2; };
   auto scale_at = [&](int R) {
@@ -159,7 +160,8 @@ __device__ __forceinline__ bool mx4_tile_products(const Mx4Act& p, const UnitTil
     char* to = lds + Lds::kScales + (u % 2) * Lds::kScaleStage + scale_at(R);
     if constexpr (kQ) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) reinterpret_cast<uint16_t*>(to)[2 * i] = static_cast<uint16_t>(v >> (16 * i));
+      for (int i = 0; i < 4; ++i)
+        reinterpret_cast<uint16_t*>(to)[2 * i] = static_cast<uint16_t>((v >> (8 * i) & 255u) | (v >> (24 + 8 * i) & 0xff00u));
     } else {
       *reinterpret_cast<uint64_t*>(to) = v;
     }
@@ -203,7 +205,7 @@ __device__ __forceinline__ bool mx4_tile_products(const Mx4Act& p, const UnitTil
 #pragma unroll
     for (int j = 0; j < FN; ++j) acc[i][j] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
 
-  // fragments: row lane % 16 of a 16-row MFMA tile, piece 2 grp + half at slot piece ^ (row / 2 % 8)
+  // fragments: row lane % 16 of a 16-row MFMA tile, piece 4 half + grp at slot piece ^ (row / 2 % 8)
   const int frag_row = (lane & 15) * kMtRowBytes, frag_swz = (lane & 15) >> 1;
   const int a_base = wm * 16 * FM * kMtRowBytes + frag_row;
   const int b_base = Lds::kB + wn * 64 * kMtRowBytes + frag_row;
@@ -215,7 +217,7 @@ __device__ __forceinline__ bool mx4_tile_products(const Mx4Act& p, const UnitTil
       const int slot = first_slot(g) + q;
       if (slot < first_slot(g + 1))
         f[q] = *reinterpret_cast<const chunk_t*>(lds + (kt % 2) * Lds::kAStage + a_base + (slot % FM) * 16 * kMtRowBytes +
-                                                 (((2 * grp + slot / FM) ^ frag_swz) << 4));
+                                                 (((4 * (slot / FM) + grp) ^ frag_swz) << 4));
     }
   };
   // 4-bit rows: the weights' fragments of a half
@@ -223,7 +225,7 @@ __device__ __forceinline__ bool mx4_tile_products(const Mx4Act& p, const UnitTil
 #pragma unroll
     for (int j = 0; j < FN; ++j)
       b[j] = *reinterpret_cast<const chunk_t*>(lds + (kt % 2) * kMtBStage + b_base + j * 16 * kMtRowBytes +
-                                               (((2 * grp + half) ^ frag_swz) << 4));
+                                               (((4 * half + grp) ^ frag_swz) << 4));
   };
   // and a step's scales, of both sides
   constexpr int kPairs = (FM + 1) / 2;
@@ -234,14 +236,15 @@ __device__ __forceinline__ bool mx4_tile_products(const Mx4Act& p, const UnitTil
 #pragma unroll
     for (int i = 0; i < 2; ++i) b[i] = *reinterpret_cast<const uint32_t*>(st + bs_base + i * 256);
   };
-  // 16-bit rows: the 16 codes of a step's two halves, and their scale
+  // 16-bit rows: the eight codes of each half of a step, and both halves' scales
   auto read_codes = [&](int kt, uint2 (&c)[FN], uint32_t (&sc)[FN]) __attribute__((always_inline)) {
-    const int u = kt / 4, block = 2 * (kt % 4) + (grp >> 1);
+    const int u = kt / 4, block = 2 * (kt % 4);
 #pragma unroll
     for (int j = 0; j < FN; ++j) {
-      c[j] = *reinterpret_cast<const uint2*>(lds + (u % 2) * kMtBStage + b_base + j * 16 * kMtRowBytes +
-                                             ((block ^ frag_swz) << 4) + 8 * (grp & 1));
-      sc[j] = *reinterpret_cast<const uint8_t*>(lds + (u % 2) * Lds::kScaleStage + bs_base + j * 128 + block);
+      const char* row = lds + (u % 2) * kMtBStage + b_base + j * 16 * kMtRowBytes + 4 * grp;
+      c[j].x = *reinterpret_cast<const uint32_t*>(row + ((block ^ frag_swz) << 4));
+      c[j].y = *reinterpret_cast<const uint32_t*>(row + (((block + 1) ^ frag_swz) << 4));
+      sc[j] = *reinterpret_cast<const uint16_t*>(lds + (u % 2) * Lds::kScaleStage + bs_base + j * 128 + block);
     }
   };
   // step kt is whole in LDS and every wave has read out the step before it
@@ -302,7 +305,7 @@ __device__ __forceinline__ bool mx4_tile_products(const Mx4Act& p, const UnitTil
   constexpr int kWide = RT == kF16 ? kF16 : kBF16;  // 16-bit rows: what the weights are widened to
   auto widen = [&](int half) __attribute__((always_inline)) {
 #pragma unroll
-    for (int j = 0; j < FN; ++j) fb[half][j] = mx4_values8<kWide>(half == 0 ? codes[j].x : codes[j].y, mx4_scale(sc[j]));
+    for (int j = 0; j < FN; ++j) fb[half][j] = mx4_values8<kWide>(half == 0 ? codes[j].x : codes[j].y, mx4_scale(sc[j] >> (8 * half) & 255u));
   };
   if constexpr (!kQ) {
     __builtin_amdgcn_s_waitcnt(kWaitLdsOnly);
@@ -368,7 +371,11 @@ __device__ __forceinline__ bool mx4_tile_products(const Mx4Act& p, const UnitTil
           widen(1);
           if (RT == kF16) {
 #pragma unroll
-            for (int j = 0; j < FN; ++j) reach = mx4_f16_reach(sc[j]) > reach ? mx4_f16_reach(sc[j]) : reach;
+            for (int j = 0; j < FN; ++j) {
+              const uint32_t r0 = mx4_f16_reach(sc[j] & 255u), r1 = mx4_f16_reach(sc[j] >> 8 & 255u);
+              const uint32_t r = r0 > r1 ? r0 : r1;
+              reach = r > reach ? r : reach;
+            }
           }
         } else if (g + 1 == kGroups) {
           widen(0);  // the next step's
