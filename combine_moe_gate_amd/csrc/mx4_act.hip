@@ -212,7 +212,7 @@ __global__ __launch_bounds__(kMxFewThreads, kOcc) void mx4_few_kernel(Mx4Act p, 
     }
   }
   const int r = row0 + row, t = p.src[r];
-  const float w = p.route_w != nullptr ? route_weight(p, r, t) : 1.0f;
+  const float w = route_weight_wide(p, r, t);
   const int c = col0 + q8;
   if (c < p.n) finish8_mx4<DT>(p, x, r, t, w, c, v, u);
   if (!p.gated && c + 8 * FB < p.n) finish8_mx4<DT>(p, x, r, t, w, c + 8 * FB, u, v);

@@ -30,7 +30,8 @@ struct MsLds {
   static constexpr int kAScales = kQ ? (FR == 4 ? 512 : 256) : 0;    // whole wave loads of words
   static constexpr int kB = kA + kAScales, kBScales = kB + kMsBN * 128;
   static constexpr int kStage = kBScales + kMsBN * 8;
-  static constexpr int kBytes = kStages * kStage > 16 * FR * kMsPitch ? kStages * kStage : 16 * FR * kMsPitch;
+  static constexpr int kRows = kStages * kStage > 16 * FR * kMsPitch ? kStages * kStage : 16 * FR * kMsPitch;
+  static constexpr int kBytes = kRows + 16 * FR * 8;                 // per row its token and route weight
   // loads of a stage that each wave issues
   static constexpr int kALoads = kQ ? (FR == 4 ? 2 : 1) : 2 * FR;
   static constexpr int kLoads = kALoads + (kQ ? 1 : 0) + 4 + 1;
@@ -81,8 +82,11 @@ __global__ __launch_bounds__(kMsThreads) void mx4_stream_kernel(Mx4Act p, int co
     a_row[q] = static_cast<const chunk_t*>(p.a) + input_row(r) * achunks;
   }
   const int as_load = kQ ? wv % (FR == 4 ? 2 : 1) : 0;
+  int my_token = static_cast<int>(threadIdx.x) < nrows ? p.src[row0 + threadIdx.x] : 0;
   const uint32_t* as_row = nullptr;
   if constexpr (kQ) as_row = reinterpret_cast<const uint32_t*>(p.a_scales + input_row((as_load * 32 + lane / 2) % (16 * FR)) * kb);
+  asm volatile("" : "+v"(my_token));
+
   // weight row of staged row r: gated, 64 gate rows and the 64 up rows that meet them; rows past the
   // last repeat it: they reach only results never stored
   auto weight_row = [&](int r) {
@@ -134,6 +138,13 @@ __global__ __launch_bounds__(kMsThreads) void mx4_stream_kernel(Mx4Act p, int co
       issue_b(u);
       issue_a(u);
     }
+  }
+
+  int* row_token = reinterpret_cast<int*>(lds + Lds::kRows);
+  float* row_weight = reinterpret_cast<float*>(lds + Lds::kRows + 16 * FR * 4);
+  if (static_cast<int>(threadIdx.x) < nrows) {
+    row_token[threadIdx.x] = my_token;
+    row_weight[threadIdx.x] = route_weight_wide(p, row0 + threadIdx.x, my_token);
   }
 
   f32x4_t acc[FR][2];
@@ -237,8 +248,9 @@ __global__ __launch_bounds__(kMsThreads) void mx4_stream_kernel(Mx4Act p, int co
       v[q] = at[q];
       u[q] = p.gated ? at[64 + q] : 0.0f;
     }
-    const int r = row0 + row, t = p.src[r];
-    finish8_mx4<DT>(p, x, r, t, p.route_w != nullptr ? route_weight(p, r, t) : 1.0f, c, v, u);
+    const int t = row_token[row];
+    const float w = row_weight[row];
+    finish8_mx4<DT>(p, x, row0 + row, t, w, c, v, u);
   }
 }
 

@@ -197,7 +197,7 @@ __device__ __forceinline__ bool mx4_tile_products(const Mx4Act& p, const UnitTil
     const int r = row0 + tid;
     const int t = p.src[r];
     row_token[tid] = t;
-    row_weight[tid] = p.route_w != nullptr ? route_weight(p, r, t) : 1.0f;
+    row_weight[tid] = route_weight_wide(p, r, t);
   }
 
 #pragma unroll

@@ -511,9 +511,10 @@ moe_status_t moe_mx4_dequantize(const void* codes, const uint8_t* scales, int64_
  *               multiple of 32); rows no route fills get zero codes and scales
  *   epilogue, preact_dtype, gather, dtype (bf16 or f16: rows, bias, residual and results): as in
  *               moe_expert_gemm_act_ex. m a multiple of 32, n of 8.
- * Products are exact and summed in float32 (order unspecified, one order per sizes). A block with
- * scale 255 makes the sums it enters NaN. out, out_scales and preact may not overlap each other
- * or anything read. codes, rows, bias, residual, preact and out 16-byte aligned.
+ * Products are exact and summed in float32 (order unspecified; one order per sizes, types, kind of
+ * rows and remainder of the scales' addresses by 4: the results are reproducible). A block with scale 255
+ * makes the sums it enters NaN. out, out_scales and preact may not overlap each other or anything read.
+ * codes, rows, bias, residual, preact and out 16-byte aligned.
  */
 moe_status_t moe_mx4_expert_gemm(const moe_layout_t* layout, const void* a, const uint8_t* a_scales,
                                  int32_t gather, const void* w_codes, const uint8_t* w_scales,
