@@ -11,6 +11,10 @@
 // to LDS under the step before its own (64-byte pieces, their 16-byte parts in an order that keeps the
 // sixteen lanes of a write on different banks), and read through LDS's transposing reads. Gradient rows
 // go to LDS directly.
+//
+// Measured, 49152 routes, 64 experts: 2816 -> 2048 561 us and 2048 -> 1408 326 us (1.01 and 0.87 PFLOP/s;
+// the product with bf16 weights takes 600 and 370). Bound by the main loop: matrix units busy 42% at
+// the clock they leave the card, the rest is widening and the LDS.
 #include <atomic>
 
 #include "mx4_product.h"
