@@ -114,12 +114,12 @@ __global__ __launch_bounds__(kMsThreads) void mx4_stream_kernel(Mx4Act p, int co
   const uint32_t* bs_row = reinterpret_cast<const uint32_t*>(p.w_scales + weight_row(wv * 32 + lane / 2) * kb);
   auto issue_b = [&](int u) __attribute__((always_inline)) {
     char* st = lds + (u % S) * Lds::kStage;
-    const int at = u * 8 + b_piece < kb ? u * 8 + b_piece : 0;  // past the row's end: any codes, the rows' zeros meet them
+    const int at = u * 8 + b_piece < kb ? u * 8 + b_piece : 0;  // past the row's end: any codes, zeros meet them
 #pragma unroll
     for (int q = 0; q < 4; ++q)
       __builtin_amdgcn_global_load_lds(static_cast<const void*>(b_row[q] + at),
                                        (lds_void_t*)(st + Lds::kB + (q * 4 + wv) * 1024), 16, 0, 0);
-    // past the row's end: its first word, which is not a number only where the whole sum is none
+    // past the row's end: its first word, set to scales of 1 once landed
     const int word = 2 * u + lane % 2 < kb / 4 ? 2 * u + lane % 2 : 0;
     __builtin_amdgcn_global_load_lds(static_cast<const void*>(bs_row + word), (lds_void_t*)(st + Lds::kBScales + wv * 256), 4, 0, 0);
   };
@@ -169,6 +169,8 @@ __global__ __launch_bounds__(kMsThreads) void mx4_stream_kernel(Mx4Act p, int co
       for (int q = 0; q < Lds::kALoads; ++q)
         if (u * kPieces + a_piece[q] >= achunks)
           *reinterpret_cast<chunk_t*>(st + a_load[q] * 1024 + lane * 16) = chunk_t{0u, 0u, 0u, 0u};
+      // any codes times other blocks' scales could pass bf16's range, and zeros then make no zero of them
+      if (2 * u + lane % 2 >= kb / 4) *reinterpret_cast<uint32_t*>(st + Lds::kBScales + wv * 256 + lane * 4) = 0x7f7f7f7fu;
       __builtin_amdgcn_s_waitcnt(kWaitLdsOnly);
     }
     stage_barrier();  // and every wave has read out the stage before it

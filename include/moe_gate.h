@@ -513,7 +513,8 @@ moe_status_t moe_mx4_dequantize(const void* codes, const uint8_t* scales, int64_
  *               moe_expert_gemm_act_ex. m a multiple of 32, n of 8.
  * Products are exact and summed in float32 (order unspecified; one order per sizes, types, kind of
  * rows and remainder of the scales' addresses by 4: the results are reproducible). A block with scale 255
- * makes the sums it enters NaN. out, out_scales and preact may not overlap each other or anything read.
+ * makes the sums it enters NaN; with scales 253 and 254, which quantising never gives, a value past
+ * float32's range may enter as itself or as infinity. out, out_scales and preact may not overlap each other or anything read.
  * codes, rows, bias, residual, preact and out 16-byte aligned.
  */
 moe_status_t moe_mx4_expert_gemm(const moe_layout_t* layout, const void* a, const uint8_t* a_scales,

@@ -412,6 +412,32 @@ def test_scales_of_every_size(dtype):
         assert_bits_equal(to_host(got), oracle.from_f32(want.astype(np.float32), dtype), f"input gradient, s {s}")
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+def test_large_scales_before_a_tail(dtype):
+    """Rows whose last K stage is not whole, the largest scales in their first blocks but small codes under
+    them, and large codes under small scales: nothing of that may meet past the rows' end. One block alone
+    carries each sum, whole numbers times a power of two."""
+    announce("mx4 product large scales before a tail", dtype)
+    rng = np.random.default_rng(12)
+    e, k = 2, 1
+    for s, n, m in ((5, 64, 128), (40, 64, 384), (40, 64, 160), (1100, 4160, 384), (1100, 4160, 160)):
+        idx = W.random_idx(rng, s, e, k)
+        L, Lg = oracle.dispatch_layout(idx, e, 0), M.moe_dispatch_layout(to_dev(idx), e, 0)
+        codes = np.full((e, n, m // 2), 0x77, np.uint8)  # sixes
+        scales = np.full((e, n, m // 32), 127, np.uint8)
+        codes[:, :, 16:64] = 0x11  # blocks 1 to 3: halves
+        scales[:, :, 1:4] = 254
+        x = np.zeros((s, m), np.float32)
+        x[:, m - 32:] = rng.integers(-3, 4, (s, 32)) if m > 128 else 0
+        x[:, :32] = rng.integers(-3, 4, (s, 32))
+        want, _ = oracle.expert_gemm_act(L, x, mx4.values(codes, scales).astype(np.float32), "f32", True)
+        want = oracle.from_f32(want.astype(np.float32), dtype)
+        got = M.moe_mx4_expert_gemm(Lg, to_dev(W.cast_input(x, dtype), dtype), pair(codes, scales))
+        assert_bits_equal(to_host(got), want, f"s {s}, m {m}")
+        got = M.moe_mx4_expert_gemm(Lg, pair(*mx4.quantize(x)), pair(codes, scales), dtype=TORCH_DTYPE[dtype])
+        assert_bits_equal(to_host(got), want, f"4-bit rows, s {s}, m {m}")
+
+
 def test_blocks_that_are_not_numbers_stay_where_they_are():
     """A token's or a weight row's NaN block (scale 255) reaches its own rows and features alone, also
     through the K tail and the rows a tile repeats; infinities of 16-bit rows likewise."""
