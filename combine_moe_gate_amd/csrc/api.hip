@@ -773,17 +773,19 @@ moe_status_t moe_mx4_expert_gemm(const moe_layout_t* layout, const void* a, cons
   const Span writes[3] = {{out, out_scales != nullptr ? rows * n / 2 : rows * n * eb},
                           {out_scales, rows * n / 32},
                           {ep.preact, rows * nz * elem_bytes(preact_dtype)}};
-  const Span reads[5] = {{a, a_rows * (a_scales != nullptr ? blocks * 16 : m * eb)},
+  const Span reads[7] = {{a, a_rows * (a_scales != nullptr ? blocks * 16 : m * eb)},
                          {a_scales, a_rows * blocks},
                          {w_codes, static_cast<size_t>(v.e) * nz * blocks * 16},
                          {w_scales, static_cast<size_t>(v.e) * nz * blocks},
-                         {ep.residual, res_rows * n * eb}};
+                         {ep.residual, res_rows * n * eb},
+                         {ep.bias, static_cast<size_t>(v.e) * nz * (ep.bias_dtype == MOE_F32 ? 4u : 2u)},
+                         {ep.topk_w, static_cast<size_t>(v.s) * v.k * sizeof(float)}};
   for (int i = 0; i < 3; ++i) {
     bool clash = false;
     for (const Span& r : reads) clash = clash || overlap(writes[i].p, writes[i].bytes, r.p, r.bytes);
     for (int j = 0; j < i; ++j) clash = clash || overlap(writes[i].p, writes[i].bytes, writes[j].p, writes[j].bytes);
     if (clash)
-      return fail(MOE_ERR_INVALID_ARG, "out, out_scales and preact may not overlap each other, a, the weights or residual");
+      return fail(MOE_ERR_INVALID_ARG, "out, out_scales and preact may not overlap each other, a, the weights, residual, bias or topk_w");
   }
   return hip_status(moe::launch_mx4_act(v, p, static_cast<int>(dtype), static_cast<hipStream_t>(stream)),
                     "moe_mx4_expert_gemm");

@@ -70,6 +70,9 @@ def test_product_argument_checks(lib):
                dict(preact=at(3, 10224).value), dict(residual=at(3, 64).value), dict(out_s=at(0, 5119)),
                dict(a_s=at(3, 10239)), dict(a_s=at(3, 2559), out_s=at(4)), dict(a_s=at(4, 150), out_s=at(4)),
                dict(preact=at(2, 1008).value), dict(preact=at(4).value, out_s=at(4, 100))]
+    # the bias' 8 times 64 float32 values: 2048 bytes, 1024 in bf16; the 80 weights: 320
+    clashes += [dict(bias=at(4).value, out=at(4, 2032)), dict(bias=at(4).value, bias_dtype=1, out_s=at(4, 1023)),
+                dict(topk_w=at(4).value, out=at(4, 304)), dict(topk_w=at(4).value, preact=at(4, 304).value)]
     for clash in clashes:
         assert call(**clash) == 1, clash
         assert "overlap" in lib.moe_last_error().decode()
