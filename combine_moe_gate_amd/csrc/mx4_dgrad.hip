@@ -13,8 +13,8 @@
 // go to LDS directly.
 //
 // Measured, 49152 routes, 64 experts: 2816 -> 2048 561 us and 2048 -> 1408 326 us (1.01 and 0.87 PFLOP/s;
-// the product with bf16 weights takes 600 and 370). Bound by the main loop: matrix units busy 42% at
-// the clock they leave the card, the rest is widening and the LDS.
+// the product with bf16 weights takes 600 and 370). Bound by the main loop: a loop of its matrix
+// instruction alone reaches 1.3.
 #include <atomic>
 
 #include "mx4_product.h"
