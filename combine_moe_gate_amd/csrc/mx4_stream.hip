@@ -3,7 +3,7 @@
 //
 // A workgroup of four waves multiplies up to 16 FR rows (16 or 32, of 4 bits 64) by 128 weight rows of one
 // expert, 32 of them each wave. Both sides stream through LDS in stages of 256 elements (codes and 16-bit rows in
-// XOR-swizzled 16-byte pieces, scales in 4-byte words), all loaded directly, S - 1 stages ahead: every
+// XOR-swizzled 16-byte pieces, scales in 4-byte words), all loaded directly, S - 1 of S stages ahead: every
 // wave issues the same number of loads a stage, so that it can wait for the oldest stage alone. Lane
 // group g = lane / 16 multiplies block 4 p + g of a stage in its half p. Rows past the segment repeat
 // its first row (their results are not stored). The sums meet in LDS, and a thread finishes eight
@@ -25,10 +25,20 @@ constexpr int kMsBN = 128;                         // weight rows per workgroup
 constexpr int kMsBand = 8;                         // row-blocks per band of the tile order
 constexpr int kMsPitch = kMsBN * 4 + 16;           // bytes per row of the float32 sums
 
-template <int RT, int FR>
+// Stages in LDS: as many as two workgroups of a CU have room for, or for short rows two, so that up to four
+// workgroups lie on a CU: of a few stages' time in LDS a workgroup's start and end are much, and the
+// others' loads cover them. Microseconds with two stages and with more, 32 tokens (16-bit rows: 24):
+//   4-bit rows: 1408 -> 2816  50 and 54    2048 -> 4096  88 and 89    2816 -> 2816  84 and 82    4096 -> 4096  180 and 175
+//   16-bit rows: 1408 -> 2816  31 and 36   4 tokens, 4096 -> 4096  62 and 55
+// With no more workgroups than CUs, more stages: 4-bit rows, one token, 6 of 64, 1408 -> 2816, 7.7 and 7.1.
+constexpr int kMsShort = 2048;                     // elements of the longest short row
+constexpr int kMsCus = 256;
+constexpr int ms_stages(int RT, int FR, bool few) { return few ? 2 : RT == kMx4 ? (FR == 1 ? 4 : 3) : FR == 1 ? 3 : 2; }
+
+template <int RT, int FR, int S>
 struct MsLds {
   static constexpr bool kQ = RT == kMx4;
-  static constexpr int kStages = kQ ? (FR == 1 ? 4 : 3) : FR == 1 ? 3 : 2;  // two workgroups per CU
+  static constexpr int kStages = S;
   static constexpr int kRowBytes = kQ ? 128 : 512;                   // 256 elements of a row
   static constexpr int kA = 16 * FR * kRowBytes;
   static constexpr int kAScales = kQ ? (FR == 4 ? 512 : 256) : 0;    // whole wave loads of words
@@ -42,11 +52,10 @@ struct MsLds {
   static_assert(kBytes <= 160 * 1024 && (kStages - 2) * kLoads < 64);
 };
 
-template <int RT, int DT, int FR>
+template <int RT, int DT, int FR, int S>
 __global__ __launch_bounds__(kMsThreads) void mx4_stream_kernel(Mx4Act p, int col_blocks, int tile_grid) {
-  using Lds = MsLds<RT, FR>;
+  using Lds = MsLds<RT, FR, S>;
   constexpr bool kQ = Lds::kQ;
-  constexpr int S = Lds::kStages;
   extern __shared__ __attribute__((aligned(1024))) char lds[];
   if (static_cast<int>(blockIdx.x) >= tile_grid) {
     zero_unfilled_mx4(p, blockIdx.x - tile_grid, gridDim.x - tile_grid);
@@ -260,15 +269,21 @@ __global__ __launch_bounds__(kMsThreads) void mx4_stream_kernel(Mx4Act p, int co
   }
 }
 
-template <int RT, int DT, int FR>
-static hipError_t launch(const Mx4Act& p, int col_blocks, int64_t grid, hipStream_t stream) {
+template <int RT, int DT, int FR, int S>
+static hipError_t launch_stages(const Mx4Act& p, int col_blocks, int64_t grid, hipStream_t stream) {
   static std::atomic<uint64_t> done{0};
-  auto kern = mx4_stream_kernel<RT, DT, FR>;
-  constexpr int kBytes = MsLds<RT, FR>::kBytes;
+  auto kern = mx4_stream_kernel<RT, DT, FR, S>;
+  constexpr int kBytes = MsLds<RT, FR, S>::kBytes;
   const hipError_t err = allow_lds(reinterpret_cast<const void*>(kern), kBytes, done);
   if (err != hipSuccess) return err;
   kern<<<static_cast<unsigned>(grid), kMsThreads, kBytes, stream>>>(p, col_blocks, static_cast<int>(grid) - kZeroBlocks);
   return hipGetLastError();
+}
+
+template <int RT, int DT, int FR>
+static hipError_t launch(const Mx4Act& p, int col_blocks, int64_t grid, hipStream_t stream) {
+  return p.m <= kMsShort && grid - kZeroBlocks > kMsCus ? launch_stages<RT, DT, FR, ms_stages(RT, FR, true)>(p, col_blocks, grid, stream)
+                                                        : launch_stages<RT, DT, FR, ms_stages(RT, FR, false)>(p, col_blocks, grid, stream);
 }
 
 template <int RT, int DT>

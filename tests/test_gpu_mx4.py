@@ -376,6 +376,49 @@ def test_whole_numbers_are_exact(s, e, k, n, m, dtype, rows):
     assert_bits_equal(to_host(got), oracle.from_f32(ga.astype(np.float32), dtype), "input gradient")
 
 
+@pytest.mark.parametrize("m", [1920, 2048, 2176, 2304, 4224])
+@pytest.mark.parametrize("s", [1, 9, 40, 130])
+def test_long_rows_of_few_tokens(s, m):
+    """Rows on both sides of what the streams take for short, with whole and partial last stages; 1, 3, 14
+    and 44 routes an expert. Whole numbers: exact in any order."""
+    announce("mx4 product long rows", s, m)
+    rng = np.random.default_rng(s + m)
+    e, k, n = 3, 1, 160
+    idx = W.random_idx(rng, s, e, k)
+    L, Lg = oracle.dispatch_layout(idx, e, 0), M.moe_dispatch_layout(to_dev(idx), e, 0)
+    x = rng.integers(-2, 3, (s, m)).astype(np.float32)
+    wts = rng.integers(-2, 3, (e, n, m)).astype(np.float32)
+    x[:, ::32], wts[:, :, 5::32] = 4, -6  # a scale of 1 in every block
+    xq, wq = mx4.quantize(x), mx4.quantize(wts)
+    want, _ = oracle.expert_gemm_act(L, x, wts, "f32", True)
+    for dtype in ("bf16", "f16"):
+        rounded = oracle.from_f32(want.astype(np.float32), dtype)
+        for rows in (to_dev(W.cast_input(x, dtype), dtype), pair(*xq)):
+            got = M.moe_mx4_expert_gemm(Lg, rows, pair(*wq), dtype=TORCH_DTYPE[dtype])
+            assert_bits_equal(to_host(got), rounded, dtype)
+
+
+@pytest.mark.parametrize("m", [128, 640, 1152])
+@pytest.mark.parametrize("s", [40, 600, 1600])
+def test_short_rows_of_many_workgroups(s, m):
+    """Few routes an expert (1, 15, 40) and more workgroups than CUs. Products are multiples of 1/4 whose sums
+    stay below 2^16: exact in any order."""
+    announce("mx4 product short rows", s, m)
+    rng = np.random.default_rng(s + m)
+    e, k, n = 40, 1, 1024
+    idx = W.random_idx(rng, s, e, k)
+    L, Lg = oracle.dispatch_layout(idx, e, 0), M.moe_dispatch_layout(to_dev(idx), e, 0)
+    xq = rng.integers(0, 256, (s, m // 2)).astype(np.uint8), np.full((s, m // 32), 127, np.uint8)
+    wq = rng.integers(0, 256, (e, n, m // 2)).astype(np.uint8), np.full((e, n, m // 32), 127, np.uint8)
+    x = mx4.values(*xq).astype(np.float32)
+    want, _ = oracle.expert_gemm_act(L, x, mx4.values(*wq).astype(np.float32), "f32", True)
+    for dtype in ("bf16", "f16"):
+        rounded = oracle.from_f32(want.astype(np.float32), dtype)
+        for rows in (to_dev(W.cast_input(x, dtype), dtype), pair(*xq)):
+            got = M.moe_mx4_expert_gemm(Lg, rows, pair(*wq), dtype=TORCH_DTYPE[dtype])
+            assert_bits_equal(to_host(got), rounded, dtype)
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f16"])
 def test_scales_of_every_size(dtype):
     """Weights whose blocks lie far apart, f16's range and its subnormals included: rows and gradients are
