@@ -230,28 +230,29 @@ struct Mx4Shape {
   int64_t col_blocks, tiles;
 };
 
-// Streams read weights best (5.2 TB/s where the tiles reach 4.3); the tiles multiply best, once an
+// Streams read weights best (5.5 TB/s where the tiles reach 4.3); the tiles multiply best, once an
 // expert has rows to fill them and there are enough of them for the CUs. Microseconds, random rows,
 // bf16 and 4-bit (`mean` per expert; `tiles` as counted below):
 //                                          bf16: stream of           4-bit: stream of
 //   experts, weight rows x length   mean    16     32    tiles        16     32     64    tiles  (tiles)
 //   128, 4096 x 4096                1/16    17     21     61          14     14     15     20
-//   128, 2816 x 2816                8      112    127    313         103    104    106    126
-//   128, 2816 x 2816                16     138    131    315         129    113    115    128
-//   128, 2816 x 2816                32     206    166    326         176    135    121    136
-//   128, 2816 x 2816                64            244    357                190    148    151
-//   64, 2816 x 1408                 96            107    101                 72     58     52
-//   128, 2816 x 2816                128           422    447                320    226    175
-//   128, 2816 x 2816                256           770    608                594    376    253
-//   8, 1024 x 1024                  16     7.0    8.1     16         5.8    6.4    7.2    8.2
-//   16, 1024 x 1024                 256            24     38                 18     17     20    (120)
-//   8, 1024 x 2048                  1024           61     72                 39     33     30    (144)
-//   16, 1024 x 1024                 512            40     42                 29     24     22    (176)
-//   8, 512 x 512                    4000           50     31                 40     29     20    (238)
+//   128, 4096 x 4096                16     289    265    465         276    231    233    253
+//   128, 2816 x 2816                32     212    168    260         179    137    121    141
+//   128, 2816 x 2816                64     337    255    285         287    190    151    158
+//   128, 2816 x 2816                72     375    289    291         315    213    168    162
+//   128, 2816 x 2816                128    608    446    348         520    321    226    186
+//   64, 2816 x 1408                 8       30     37     68          28     29     30     39
+//   64, 2816 x 1408                 16      37     39     69          32     30     31     40
+//   64, 2816 x 1408                 72     102     95     87          78     64     55     55
+//   8, 1024 x 1024                  16     6.9    8.0     17         5.8    6.4    7.3    8.2
+//   16, 1024 x 1024                 256     25     24     38          19     15     13     20    (120)
+//   8, 1024 x 2048                  1024    72     60     65          54     36     27     29    (144)
+//   16, 1024 x 4096                 512    154    100    117         107     66     51     45    (176)
+//   8, 512 x 512                    4000    59     50     29          42     32     24     20    (238)
 // Rows that are no multiple of 128 elements, or unaligned scales, take this file's kernel in place of a
 // stream: 16 experts, 576 x 544, mean 125 in 9.1 and 7.2 (tiles 19 and 12). It takes 32 rows at a time,
 // of f16 16: beside more, the split form does not fit the registers (25 us where 32 rows take 39).
-constexpr int kMx4Mean16 = 112, kMx4Mean4 = 72;      // mean rows from which the tiles are worth while
+constexpr int kMx4Mean = 72;                         // mean rows from which the tiles are worth while
 constexpr int64_t kMx4Tiles16 = 200, kMx4Tiles4 = 128;
 static Mx4Shape mx4_shape(const LayoutView& L, const Mx4Act& p, int dtype) {
   const bool q = p.a_scales != nullptr;
@@ -265,7 +266,7 @@ static Mx4Shape mx4_shape(const LayoutView& L, const Mx4Act& p, int dtype) {
   int64_t mean = (routes + L.e - 1) / L.e;
   if (L.capacity > 0 && mean > L.capacity) mean = L.capacity;
   const bool many = large.tiles >= (q ? kMx4Tiles4 : kMx4Tiles16);
-  if (many && mean >= (q ? kMx4Mean4 : kMx4Mean16)) return large;
+  if (many && mean >= kMx4Mean) return large;
   const uintptr_t scales = reinterpret_cast<uintptr_t>(p.w_scales) | reinterpret_cast<uintptr_t>(p.a_scales);
   if (p.m % 128 == 0 && scales % 4 == 0) {
     const int few = mean <= (q ? 8 : 12) ? 1 : q && mean > 24 ? 4 : 2;

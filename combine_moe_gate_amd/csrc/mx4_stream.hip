@@ -10,7 +10,7 @@
 // features of a row.
 //
 // Measured: one token, 8 of 128 experts, 4096 -> 2 x 2048, bf16 rows, 71 MB in 17 us; 32 tokens, 4-bit
-// rows, 2816 -> 2 x 1408, 460 MB in 84 us (5.5 TB/s) and 1408 -> 2816, 243 MB in 55 (4.4): the shorter
+// rows, 2816 -> 2 x 1408, 460 MB in 84 us (5.5 TB/s) and 1408 -> 2816, 243 MB in 51 (4.8): the shorter
 // the rows, the more of a workgroup's time is its start and end.
 //
 // Scales load as words: rows must be a multiple of 128 elements and scales 4-byte aligned.
