@@ -57,8 +57,8 @@ __device__ __forceinline__ uint32_t mx4_quantize8(const float (&v)[8], uint32_t*
   return mx4_codes8(v, *E);
 }
 
-// Eight codes as eight values of the element type (bf16: exact; f16 and float32: rounded to
-// nearest, which f16 needs below 2^-23 and above 2^13 times the code, infinite past the range).
+// Eight codes as eight values of a 16-bit element type: bf16 holds every value of a scale up to 2^125;
+// f16 those of scales from 2^-23 to 2^13, others are rounded to nearest, past its range to infinity.
 template <int DT>
 __device__ __forceinline__ chunk_t mx4_values8(uint32_t codes, float scale) {
   chunk_t o;

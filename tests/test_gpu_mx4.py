@@ -455,6 +455,36 @@ def test_scales_of_every_size(dtype):
         assert_bits_equal(to_host(got), oracle.from_f32(want.astype(np.float32), dtype), f"input gradient, s {s}")
 
 
+def test_subnormal_weights_and_rows():
+    """Values below bf16's normal range on one side and large ones on the other: their products are
+    ordinary, and whole numbers times one power of two."""
+    announce("mx4 product subnormals")
+    rng = np.random.default_rng(21)
+    e, k = 2, 1
+    for s, n, m in ((5, 64, 256), (40, 64, 160), (700, 4160, 256)):  # streams, few rows, tiles
+        idx = W.random_idx(rng, s, e, k)
+        L, Lg = oracle.dispatch_layout(idx, e, 0), M.moe_dispatch_layout(to_dev(idx), e, 0)
+        codes = rng.integers(0, 256, (e, n, m // 2)).astype(np.uint8)
+        x = rng.integers(-3, 4, (s, m)).astype(np.float32)
+        x[:, ::32] = 3
+        g = rng.integers(-3, 4, (L.rows, n)).astype(np.float32)
+        for E_, power in ((0, 120), (1, 119), (3, 110), (240, -130), (245, -133)):
+            scales = np.full((e, n, m // 32), E_, np.uint8)
+            scaled = (x * np.float32(2.0) ** power).astype(np.float32)
+            wide = mx4.values(codes, scales).astype(np.float64)
+            want, _ = oracle.expert_gemm_act(L, x, (wide * 2.0 ** power).astype(np.float32), "f32", True)
+            want = oracle.from_f32(want.astype(np.float32), "bf16")
+            got = M.moe_mx4_expert_gemm(Lg, to_dev(W.cast_input(scaled, "bf16"), "bf16"), pair(codes, scales))
+            assert_bits_equal(to_host(got), want, f"s {s}, scale {E_}")
+            if power > -128:  # 4-bit rows of halves: their scale is 2^(power - 1)
+                got = M.moe_mx4_expert_gemm(Lg, pair(*mx4.quantize(scaled)), pair(codes, scales))
+                assert_bits_equal(to_host(got), want, f"4-bit rows, s {s}, scale {E_}")
+            _, want = oracle.expert_gemm_dgrad(L, g, (wide * 2.0 ** power).astype(np.float32), "f32")
+            got = M.moe_mx4_expert_dgrad(Lg, to_dev(W.cast_input((g * np.float32(2.0) ** power).astype(np.float32), "bf16"), "bf16"),
+                                         pair(codes, scales))
+            assert_bits_equal(to_host(got), oracle.from_f32(want.astype(np.float32), "bf16"), f"input gradient, s {s}, scale {E_}")
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f16"])
 def test_large_scales_before_a_tail(dtype):
     """Rows whose last K stage is not whole, the largest scales in their first blocks but small codes under
