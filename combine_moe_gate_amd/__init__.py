@@ -141,6 +141,10 @@ _SIGNATURES = {
     "moe_mx4_expert_gemm": (ctypes.c_int, [ctypes.POINTER(LayoutStruct), _P, _P, _I, _P, _P, _I, _I, ctypes.c_int,
                                            ctypes.POINTER(Epilogue), ctypes.c_int, _P, _P, _P]),
     "moe_mx4_expert_dgrad": (ctypes.c_int, [ctypes.POINTER(LayoutStruct), _P, _P, _P, _I, _I, ctypes.c_int, _P, _P]),
+    "moe_mx4_expert_dgrad_ex": (ctypes.c_int, [ctypes.POINTER(LayoutStruct), _P, _I, _P, _P, _I, _I, ctypes.c_int,
+                                               ctypes.c_int, _P, _P]),
+    "moe_expert_act_backward_parts": (ctypes.c_int, [ctypes.POINTER(LayoutStruct), _P, _P, ctypes.c_int, _I, ctypes.c_int,
+                                                     _I, _I, _P, _I, _P, ctypes.c_int, _P, _P, _P, _P, ctypes.c_size_t, _P]),
     "moe_dispatch_layout_static_scratch": (ctypes.c_int, [_P, _I, _I, _I, _I, ctypes.POINTER(LayoutOptions), _P,
                                                           ctypes.c_size_t, ctypes.POINTER(LayoutStruct), _P]),
 }
@@ -567,7 +571,7 @@ def moe_expert_gemm_act(layout: Layout, a: torch.Tensor, weights: torch.Tensor, 
 
 def moe_expert_act_backward(layout: Layout, grad_out: torch.Tensor, preact=None, act: str = "none", gated: bool = False,
                             w=None, need_preact: bool = True, bias_dtype=None, need_w: bool = False,
-                            need_residual: bool = False, workspace=None):
+                            need_residual: bool = False, workspace=None, parts: int = 1):
     """Backward of moe_expert_gemm_act's epilogue: (grad_preact, grad_bias, grad_w,
     grad_residual), None where not asked for.
 
@@ -576,6 +580,10 @@ def moe_expert_act_backward(layout: Layout, grad_out: torch.Tensor, preact=None,
     bias_dtype (float32 or grad_out's dtype; None: not wanted); grad_w [s, k] float32 (needs
     w); grad_residual [rows, n], for a residual of buffer rows. The gradients of a and
     weights are moe_expert_act_dgrad and moe_expert_gemm_wgrad of grad_preact.
+
+    grad_preact is rounded to grad_out's dtype, or with parts=2 is [rows, 2, weight rows] bfloat16,
+    the nearest value and the nearest to what that leaves (16 bits of a float32 value together, and
+    its range), for moe_mx4_expert_dgrad.
     """
     _expect(grad_out, "grad_out", (layout.rows, None), _GEMM_DTYPES)
     n, dt = grad_out.shape[1], grad_out.dtype
@@ -586,21 +594,25 @@ def moe_expert_act_backward(layout: Layout, grad_out: torch.Tensor, preact=None,
     _expect(w, "w", (layout.s, layout.k), torch.float32)
     if need_w and w is None:
         raise ValueError("need_w: w is required")
+    if parts != 1 and parts != 2:
+        raise ValueError(f"parts must be 1 or 2, got {parts!r}")
     if preact is None and (code != 0 or gated or need_w):
         raise ValueError("preact is required (the values the forward kept)")
     _expect(preact, "preact", (layout.rows, nz), (dt, torch.float32))
     _expect(workspace, "workspace", (None,), torch.uint8)
     _same_device(layout, grad_out, preact, w, workspace)
     dev = grad_out.device
-    gz = torch.empty((layout.rows, nz), dtype=dt, device=dev) if need_preact else None
+    gz = None
+    if need_preact:
+        gz = torch.empty((layout.rows, nz) if parts == 1 else (layout.rows, 2, nz), dtype=dt if parts == 1 else torch.bfloat16, device=dev)
     gb = torch.empty((layout.e, nz), dtype=bias_dtype, device=dev) if bias_dtype is not None else None
     gw = torch.empty((layout.s, layout.k), dtype=torch.float32, device=dev) if need_w else None
     gr = torch.empty((layout.rows, n), dtype=dt, device=dev) if need_residual else None
     if workspace is None and (gb is not None or gw is not None):
         workspace = torch.empty(lib().moe_expert_act_backward_workspace_bytes(layout.byref(), n, int(bool(gated))),
                                 dtype=torch.uint8, device=dev)
-    _launch(grad_out, lib().moe_expert_act_backward_ex, layout.byref(), _ptr(grad_out), _ptr(preact),
-            _DTYPE_CODE[dt if preact is None else preact.dtype], n, _DTYPE_CODE[dt], code, int(bool(gated)), _ptr(w), _ptr(gz),
+    _launch(grad_out, lib().moe_expert_act_backward_parts, layout.byref(), _ptr(grad_out), _ptr(preact),
+            _DTYPE_CODE[dt if preact is None else preact.dtype], n, _DTYPE_CODE[dt], code, int(bool(gated)), _ptr(w), parts, _ptr(gz),
             _DTYPE_CODE[bias_dtype] if gb is not None else MOE_F32, _ptr(gb), _ptr(gw), _ptr(gr), _ptr(workspace), workspace.numel() if workspace is not None else 0)
     return gz, gb, gw, gr
 
@@ -778,19 +790,32 @@ def moe_mx4_expert_gemm(layout: Layout, a, weights, gather: bool = True, bias=No
     return result if preact is None else (result, preact)
 
 
-def moe_mx4_expert_dgrad(layout: Layout, grad_preact: torch.Tensor, weights, out=None):
+def moe_mx4_expert_dgrad(layout: Layout, grad_preact: torch.Tensor, weights, out=None, out_dtype=None):
     """Input-row gradient of moe_mx4_expert_gemm: grad_a[r] = grad_preact[r] @ W[x], W the values of
     the pair weights, for the placed rows of expert x, [rows, m] (zero rows where no route is placed).
-    grad_preact is moe_expert_act_backward's (the epilogue is the same); the token gradient of a
-    gathered forward is moe_dispatch_backward(layout, grad_a)."""
-    _expect(grad_preact, "grad_preact", (layout.rows, None), _GEMM_DTYPES)
-    nz = grad_preact.shape[1]
+    grad_preact is moe_expert_act_backward's (the epilogue is the same): [rows, weight rows], or both
+    parts of it, [rows, 2, weight rows] bfloat16. out_dtype (or out's): float32, or grad_preact's dtype
+    (of parts: any element type); grad_preact's unless given. The token gradient of a gathered forward is
+    moe_dispatch_backward(layout, grad_a): of float32 rows it rounds nothing before a token's sum."""
+    if isinstance(grad_preact, torch.Tensor) and grad_preact.dim() == 3:
+        parts = 2
+        _expect(grad_preact, "grad_preact", (layout.rows, 2, None), torch.bfloat16)
+        allowed = _ROW_DTYPES
+    else:
+        parts = 1
+        _expect(grad_preact, "grad_preact", (layout.rows, None), _GEMM_DTYPES)
+        allowed = (torch.float32, grad_preact.dtype)
+    nz = grad_preact.shape[-1]
     m = _expect_mx4(weights, "weights", (layout.e, nz, None))
-    _expect(out, "out", (layout.rows, m), grad_preact.dtype)
+    if out_dtype is None:
+        out_dtype = grad_preact.dtype if out is None else allowed
+    elif out_dtype not in allowed:
+        raise ValueError(f"out_dtype must be {' or '.join(str(d) for d in allowed)}, got {out_dtype}")
+    _expect(out, "out", (layout.rows, m), out_dtype)
     _same_device(layout, grad_preact, weights[0], weights[1], out)
-    out = out if out is not None else torch.empty((layout.rows, m), dtype=grad_preact.dtype, device=grad_preact.device)
-    _launch(grad_preact, lib().moe_mx4_expert_dgrad, layout.byref(), _ptr(grad_preact), _ptr(weights[0]), _ptr(weights[1]), m, nz,
-            _DTYPE_CODE[grad_preact.dtype], _ptr(out))
+    out = out if out is not None else torch.empty((layout.rows, m), dtype=out_dtype, device=grad_preact.device)
+    _launch(grad_preact, lib().moe_mx4_expert_dgrad_ex, layout.byref(), _ptr(grad_preact), parts, _ptr(weights[0]), _ptr(weights[1]),
+            m, nz, _DTYPE_CODE[grad_preact.dtype], _DTYPE_CODE[out.dtype], _ptr(out))
     return out
 
 

@@ -3,8 +3,8 @@
     python -m combine_moe_gate_amd._build
 
 hipcc cross-compiles for gfx950 without a GPU present. The same build compiles
-tests/c_abi_check, tests/c_abi_ops_check and tests/c_abi_mx4_check, C++ programs that drive the
-library through its C ABI alone.
+tests/c_abi_check, tests/c_abi_ops_check, tests/c_abi_mx4_check and tests/c_abi_mx4_grad_check, C++
+programs that drive the library through its C ABI alone.
 """
 from __future__ import annotations
 
@@ -50,7 +50,7 @@ def hipcc() -> str:
     return path
 
 
-C_CHECKS = [os.path.join(ROOT, "tests", name) for name in ("c_abi_check", "c_abi_ops_check", "c_abi_mx4_check")]
+C_CHECKS = [os.path.join(ROOT, "tests", name) for name in ("c_abi_check", "c_abi_ops_check", "c_abi_mx4_check", "c_abi_mx4_grad_check")]
 
 
 def build_c_checks(verbose: bool = False) -> None:

@@ -274,9 +274,11 @@ class _ExpertMx4(torch.autograd.Function):
 
     @staticmethod
     def forward(ctx, a, bias, w, residual, codes, scales, layout, act, gated, gather, residual_gather, quantize_rows,
-                preact_dtype, backward):
+                preact_dtype, grad_dtype, backward):
         a, codes, scales = a.contiguous(), codes.contiguous(), scales.contiguous()
         bias, w, residual = (None if t is None else t.contiguous() for t in (bias, w, residual))
+        if grad_dtype is not None and grad_dtype not in (a.dtype, torch.float32):
+            raise ValueError(f"grad_dtype must be float32 or {a.dtype}, got {grad_dtype}")
         bent = act != "none" or gated
         keep = backward and ((bent and any(ctx.needs_input_grad[:3])) or (w is not None and ctx.needs_input_grad[2]))
         got = moe_mx4_expert_gemm(layout, moe_mx4_quantize(a) if quantize_rows else a, (codes, scales), gather=gather,
@@ -287,6 +289,7 @@ class _ExpertMx4(torch.autograd.Function):
         ctx.save_for_backward(codes, scales, w, preact)
         ctx.layout, ctx.act, ctx.gated, ctx.bent = layout, act, gated, bent
         ctx.gather, ctx.residual_gather = gather, residual_gather
+        ctx.wide, ctx.dtype = grad_dtype is torch.float32, a.dtype
         ctx.bias_dtype = None if bias is None else bias.dtype
         return out
 
@@ -302,16 +305,17 @@ class _ExpertMx4(torch.autograd.Function):
         rows_res = need_res and not ctx.residual_gather
         if need_z or need_bias or need_w or rows_res:
             gz, g_bias, g_w, g_res = moe_expert_act_backward(
-                L, g_out, preact, ctx.act, ctx.gated, w, need_preact=need_z,
+                L, g_out, preact, ctx.act, ctx.gated, w, need_preact=need_z, parts=2 if ctx.wide else 1,
                 bias_dtype=ctx.bias_dtype if need_bias else None, need_w=need_w, need_residual=rows_res)
             g_z = gz if need_z else g_out
         if need_a:
-            g_a = moe_mx4_expert_dgrad(L, g_z, (codes, scales))
+            # a token's rows are summed before their one rounding where the caller keeps them in float32
+            g_a = moe_mx4_expert_dgrad(L, g_z, (codes, scales), out_dtype=torch.float32 if ctx.wide and ctx.gather else ctx.dtype)
             if ctx.gather:
-                g_a = moe_dispatch_backward(L, g_a)
+                g_a = moe_dispatch_backward(L, g_a).to(ctx.dtype)
         if need_res and ctx.residual_gather:
             g_res = moe_dispatch_backward(L, g_out)
-        return g_a, g_bias, g_w, g_res, None, None, None, None, None, None, None, None, None, None
+        return (g_a, g_bias, g_w, g_res) + (None,) * 11
 
 
 class LayoutRecorder:
@@ -485,14 +489,19 @@ def expert_linear(x: torch.Tensor, weights: torch.Tensor, layout: Layout, bias: 
 def expert_linear_mx4(x: torch.Tensor, weights, layout: Layout, bias: torch.Tensor | None = None, act: str = "none",
                       gated: bool = False, w: torch.Tensor | None = None, residual: torch.Tensor | None = None,
                       residual_gather: bool = False, gather: bool = True, quantize_rows: bool = False,
-                      preact_dtype: torch.dtype | None = None):
+                      preact_dtype: torch.dtype | None = None, grad_dtype: torch.dtype | None = None):
     """expert_linear on frozen 4-bit weights, the pair (codes [e, n, m / 2], scales [e, n, m / 32]) of
     moe_mx4_quantize (gated: [e, 2n, ..]): gradients reach x, bias, w and residual, for tuning what stands
     around the experts. quantize_rows: x is rounded to 4 bits before the product as well, and the gradient
-    passes through that rounding as it is. The other arguments as in expert_linear."""
+    passes through that rounding as it is.
+
+    grad_dtype: between the epilogue's backward and x's gradient, values are rounded to x's dtype (None), or
+    with float32 kept in 16 bits of significance (two bf16 parts) and summed over a token's routes in float32: x's
+    gradient is then rounded once, and values past f16's range reach it; twice the input gradient's products.
+    The other arguments as in expert_linear."""
     codes, scales = weights
     return _ExpertMx4.apply(x, bias, w, residual, codes, scales, layout, act, gated, gather, residual_gather,
-                            quantize_rows, preact_dtype, torch.is_grad_enabled())
+                            quantize_rows, preact_dtype, grad_dtype, torch.is_grad_enabled())
 
 
 def renormalize(w: torch.Tensor, layout: Layout):

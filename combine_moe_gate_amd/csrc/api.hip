@@ -794,11 +794,23 @@ moe_status_t moe_mx4_expert_gemm(const moe_layout_t* layout, const void* a, cons
 moe_status_t moe_mx4_expert_dgrad(const moe_layout_t* layout, const void* grad_preact, const void* w_codes,
                                   const uint8_t* w_scales, int32_t m, int32_t nz, moe_dtype_t dtype,
                                   void* grad_a, void* stream) {
+  return moe_mx4_expert_dgrad_ex(layout, grad_preact, 1, w_codes, w_scales, m, nz, dtype, dtype, grad_a, stream);
+}
+
+moe_status_t moe_mx4_expert_dgrad_ex(const moe_layout_t* layout, const void* grad_preact, int32_t parts,
+                                     const void* w_codes, const uint8_t* w_scales, int32_t m, int32_t nz,
+                                     moe_dtype_t dtype, moe_dtype_t grad_a_dtype, void* grad_a, void* stream) {
   moe::LayoutView v;
   MOE_TRY(view_of(layout, &v));
   if (dtype != MOE_BF16 && dtype != MOE_F16)
     return fail(MOE_ERR_UNSUPPORTED, "moe_mx4_expert_dgrad supports bf16 and f16 only (got dtype %d)",
                 static_cast<int>(dtype));
+  if (parts != 1 && parts != 2) return fail(MOE_ERR_INVALID_ARG, "parts must be 1 or 2 (got %d)", parts);
+  if (parts == 2 && dtype != MOE_BF16)
+    return fail(MOE_ERR_UNSUPPORTED, "gradients in two parts are bf16 (got dtype %d)", static_cast<int>(dtype));
+  if (parts == 1) MOE_TRY(check_wide("grad_a_dtype", grad_a_dtype, dtype));
+  if (elem_bytes(grad_a_dtype) == 0)
+    return fail(MOE_ERR_UNSUPPORTED, "grad_a_dtype must be float32, bf16 or f16 (got %d)", static_cast<int>(grad_a_dtype));
   int64_t rc_in = 0;
   MOE_TRY(check_rows(nz, dtype, &rc_in));
   MOE_TRY(check_mx4_rows("m", m));
@@ -809,11 +821,11 @@ moe_status_t moe_mx4_expert_dgrad(const moe_layout_t* layout, const void* grad_p
   MOE_TRY(check_array(w_scales, v.s > 0 ? v.e : 0, "w_scales", false));
   MOE_TRY(check_array(grad_a, v.rows, "grad_a", true));
   const size_t eb = elem_bytes(dtype), blocks = static_cast<size_t>(v.e) * nz * (m / 32);
-  const size_t a_bytes = static_cast<size_t>(v.rows) * m * eb;
-  if (overlap(grad_a, a_bytes, grad_preact, static_cast<size_t>(v.rows) * nz * eb) ||
+  const size_t a_bytes = static_cast<size_t>(v.rows) * m * elem_bytes(grad_a_dtype);
+  if (overlap(grad_a, a_bytes, grad_preact, static_cast<size_t>(v.rows) * nz * parts * eb) ||
       overlap(grad_a, a_bytes, w_codes, blocks * 16) || overlap(grad_a, a_bytes, w_scales, blocks))
     return fail(MOE_ERR_INVALID_ARG, "grad_a may not overlap grad_preact or the weights");
-  moe::Mx4Act p{};
+  moe::Mx4Dgrad p{};
   p.a = grad_preact;
   p.w = w_codes;
   p.w_scales = w_scales;
@@ -828,6 +840,8 @@ moe_status_t moe_mx4_expert_dgrad(const moe_layout_t* layout, const void* grad_p
   p.n = p.nz = m;
   p.act = MOE_ACT_NONE;
   p.rows = v.rows;
+  p.parts = parts;
+  p.out_type = static_cast<int>(grad_a_dtype);
   return hip_status(moe::launch_mx4_dgrad(v, p, static_cast<int>(dtype), static_cast<hipStream_t>(stream)),
                     "moe_mx4_expert_dgrad");
 }
@@ -859,11 +873,24 @@ moe_status_t moe_expert_act_backward_ex(const moe_layout_t* layout, const void* 
                                         const float* topk_w, void* grad_preact, moe_dtype_t bias_dtype,
                                         void* grad_bias, float* grad_topk_w, void* grad_residual,
                                         void* workspace, size_t workspace_bytes, void* stream) {
+  return moe_expert_act_backward_parts(layout, grad_out, preact, preact_dtype, n, dtype, activation, gated, topk_w, 1,
+                                       grad_preact, bias_dtype, grad_bias, grad_topk_w, grad_residual, workspace,
+                                       workspace_bytes, stream);
+}
+
+moe_status_t moe_expert_act_backward_parts(const moe_layout_t* layout, const void* grad_out,
+                                           const void* preact, moe_dtype_t preact_dtype, int32_t n,
+                                           moe_dtype_t dtype, int32_t activation, int32_t gated,
+                                           const float* topk_w, int32_t parts, void* grad_preact,
+                                           moe_dtype_t bias_dtype, void* grad_bias, float* grad_topk_w,
+                                           void* grad_residual, void* workspace, size_t workspace_bytes,
+                                           void* stream) {
   moe::LayoutView v;
   MOE_TRY(view_of(layout, &v));
   if (dtype != MOE_BF16 && dtype != MOE_F16)
     return fail(MOE_ERR_UNSUPPORTED, "moe_expert_act_backward supports bf16 and f16 only (got dtype %d)",
                 static_cast<int>(dtype));
+  if (parts != 1 && parts != 2) return fail(MOE_ERR_INVALID_ARG, "parts must be 1 or 2 (got %d)", parts);
   int64_t rc = 0;
   MOE_TRY(check_rows(n, dtype, &rc));
   MOE_TRY(check_act(activation, gated, n));
@@ -890,7 +917,7 @@ moe_status_t moe_expert_act_backward_ex(const moe_layout_t* layout, const void* 
                   plan.bytes);
   }
   const size_t eb = elem_bytes(dtype);
-  const size_t n_bytes = v.rows * n * eb, gz_bytes = static_cast<size_t>(v.rows) * nz * eb;
+  const size_t n_bytes = v.rows * n * eb, gz_bytes = static_cast<size_t>(v.rows) * nz * parts * eb;
   const size_t z_bytes = static_cast<size_t>(v.rows) * nz * elem_bytes(preact_dtype);
   if (overlap(grad_preact, gz_bytes, grad_out, n_bytes) || overlap(grad_preact, gz_bytes, preact, z_bytes) ||
       overlap(grad_residual, n_bytes, grad_out, n_bytes) || overlap(grad_residual, n_bytes, preact, z_bytes) ||
@@ -914,6 +941,7 @@ moe_status_t moe_expert_act_backward_ex(const moe_layout_t* layout, const void* 
   p.n = n;
   p.nz = nz;
   p.act = activation;
+  p.parts = parts;
   p.rows = v.rows;
   p.gated = gated != 0;
   p.bias_f32 = bias_dtype == MOE_F32;

@@ -5,8 +5,10 @@
 //     grad_z[r] = g act'(z)      (gated: g z_up act'(z_gate), and g act(z_gate))
 //     grad_b[x] = sum_r grad_z[r],   grad_w(route at r) = <grad_out[r], u(z[r])>
 // The products' own gradients are grouped GEMMs of grad_z, which is rounded to the element type
-// for them, once: what the matrix cores take (grad_b sums the unrounded values). z is read as
-// the forward kept it, rounded to the element type or in float32 (Z32): whichever the caller
+// for them, once: what the matrix cores take (grad_b sums the unrounded values). Or it goes out in
+// two bf16 parts, the nearest bf16 value and the nearest to what that leaves, 16 bits of a float32
+// value together: the matrix cores take those one after the other, with float32's range. z is read
+// as the forward kept it, rounded to the element type or in float32 (Z32): whichever the caller
 // keeps memory for.
 //
 // One pass over grad_out and z, bound by its traffic. A workgroup takes 64 rows (16 of few)
@@ -18,7 +20,7 @@
 // are in flight, since a row's loads alone would leave memory idle while it is finished.
 //
 // Measured: 49152 rows of 1408 gated features (0.69 GB) 134 us, 5.2 TB/s, with float32 z (0.97
-// GB) 190 us, 5.1 TB/s; 2000 rows of 264
+// GB) 190 us, 5.1 TB/s, and with grad_z in two parts (1.25 GB) 250 us, 5.0 TB/s; 2000 rows of 264
 // gated features with bias 9.5 us and 3 us for the sums.
 #include <type_traits>
 
@@ -67,6 +69,20 @@ __device__ __forceinline__ void act_and_slope(float z, float* f, float* d) {
   }
 }
 
+// Eight values in two bf16 parts whose sum is off by at most 2^-17 of each (above bf16's subnormals).
+// Past bf16's largest value a finite one's first part is that value; an infinity or NaN is all in it.
+__device__ __forceinline__ void bf16_parts(const float (&v)[8], chunk_t* hi, chunk_t* lo) {
+  constexpr float kMost = 3.3895313892515355e38f;  // (2 - 2^-7) 2^127
+  float h[8], l[8];
+#pragma unroll
+  for (int q = 0; q < 8; ++q) h[q] = __builtin_fabsf(v[q]) < INFINITY ? clamp_to(v[q], kMost) : v[q];
+  *hi = pack<kBF16>(h);
+  unpack<kBF16>(*hi, h);
+#pragma unroll
+  for (int q = 0; q < 8; ++q) l[q] = __builtin_fabsf(v[q]) < INFINITY ? v[q] - h[q] : 0.0f;
+  *lo = pack<kBF16>(l);
+}
+
 template <int DT, int ACT, bool GATED, bool Z32>
 __global__ __launch_bounds__(kBwdThreads) void expert_act_backward_kernel(ExpertActBackward p, int col_blocks,
                                                                           int shift, int tile_grid, float* __restrict__ bias_part,
@@ -81,8 +97,9 @@ __global__ __launch_bounds__(kBwdThreads) void expert_act_backward_kernel(Expert
     const chunk_t z = {0u, 0u, 0u, 0u};
     auto clear = [&](int r) {
       if (p.grad_preact != nullptr) {
-        chunk_t* o = reinterpret_cast<chunk_t*>(static_cast<uint16_t*>(p.grad_preact) + static_cast<size_t>(r) * p.nz);
-        for (int c = lane; c < p.nz / 8; c += kWave) o[c] = z;
+        const size_t chunks = static_cast<size_t>(p.parts) * p.nz / 8;
+        chunk_t* o = static_cast<chunk_t*>(p.grad_preact) + static_cast<size_t>(r) * chunks;
+        for (size_t c = lane; c < chunks; c += kWave) o[c] = z;
       }
       if (p.grad_residual != nullptr) {
         chunk_t* o = reinterpret_cast<chunk_t*>(static_cast<uint16_t*>(p.grad_residual) + static_cast<size_t>(r) * p.n);
@@ -170,9 +187,11 @@ __global__ __launch_bounds__(kBwdThreads) void expert_act_backward_kernel(Expert
       for (int h = 0; h < H; ++h) {
 #pragma unroll
         for (int q = 0; q < 8; ++q) acc[h][q] += d[h][q];
-        if (p.grad_preact != nullptr)
-          *reinterpret_cast<chunk_t*>(static_cast<uint16_t*>(p.grad_preact) + static_cast<size_t>(r) * p.nz + h * p.n + c) =
-              pack<DT>(d[h]);
+        if (p.grad_preact != nullptr) {
+          uint16_t* o = static_cast<uint16_t*>(p.grad_preact) + static_cast<size_t>(r) * p.nz * p.parts + h * p.n + c;
+          if (p.parts == 1) *reinterpret_cast<chunk_t*>(o) = pack<DT>(d[h]);
+          else bf16_parts(d[h], reinterpret_cast<chunk_t*>(o), reinterpret_cast<chunk_t*>(o + p.nz));
+        }
       }
       if (p.grad_residual != nullptr)
         *reinterpret_cast<chunk_t*>(static_cast<uint16_t*>(p.grad_residual) + static_cast<size_t>(r) * p.n + c) = gv[b];

@@ -5,6 +5,8 @@
 // its own, so the weights are widened on their way to LDS: to bf16, which is exact, or for f16 gradients
 // to f16, exact for scales from 2^-23 to 2^13. A tile that met others is formed again from gradients in
 // two parts (split_f16) and bf16 weights, straight from memory: far slower, and in few registers.
+// Gradient rows that come in two bf16 parts are multiplied part by part, the second's steps after the
+// first's, on the same weights: twice the steps. Results are rounded to 16 bits or stay float32.
 //
 // Tiles of up to 256 rows by 256 input features, eight waves, as in mx4_tile.hip: a step is 64 weight
 // rows. Each thread has one block of 32 weights of a step: loaded two steps ahead, widened and written
@@ -13,8 +15,8 @@
 // go to LDS directly.
 //
 // Measured, 49152 routes, 64 experts: 2816 -> 2048 561 us and 2048 -> 1408 326 us (1.01 and 0.87 PFLOP/s;
-// the product with bf16 weights takes 600 and 370). Bound by the main loop: a loop of its matrix
-// instruction alone reaches 1.3.
+// the product with bf16 weights takes 600 and 370); rows in parts, to float32, 1071 and 639. Bound by
+// the main loop: a loop of its matrix instruction alone reaches 1.3.
 #include <atomic>
 
 #include "mx4_product.h"
@@ -33,9 +35,17 @@ constexpr int kMdLds = kMdVotes + 32;
 constexpr int kMdSlabPitch = 64 * 4 + 16;          // bytes per row of a wave's 16 x 64 float32 slab
 static_assert(8 * 2 * 16 * kMdSlabPitch <= kMdVotes, "the slabs reuse the stages");
 
+// Eight results. Of 16-bit gradient rows they are float32 or of the same type; of rows in parts, of any.
+template <int DT, int PARTS>
+__device__ __forceinline__ void mx4_dgrad_store(const Mx4Dgrad& p, size_t at, const float (&v)[8]) {
+  if (p.out_type == DT) *reinterpret_cast<chunk_t*>(static_cast<uint16_t*>(p.out) + at) = pack<DT>(v);
+  else if (p.out_type == kF32) store8<DT>(p.out, at, true, v);
+  else if (PARTS == 2) *reinterpret_cast<chunk_t*>(static_cast<uint16_t*>(p.out) + at) = pack<kF16>(v);
+}
+
 // A tile of 32 FM rows; false if it is left to mx4_dgrad_split (f16 alone).
-template <int DT, int FM>
-__device__ __forceinline__ bool mx4_dgrad_body(const Mx4Act& p, const UnitTile& tc, char* lds) {
+template <int DT, int PARTS, int FM>
+__device__ __forceinline__ bool mx4_dgrad_body(const Mx4Dgrad& p, const UnitTile& tc, char* lds) {
   constexpr int FN = 4;
   // A step's products in order: (k32 half, row tile), 2 FM slots of FN MFMAs, cut into groups of up to
   // four slots whose fragments are read together; the last group lies in the second half.
@@ -48,7 +58,9 @@ __device__ __forceinline__ bool mx4_dgrad_body(const Mx4Act& p, const UnitTile& 
   const int rem = tc.rows - tc.unit0 * 32;
   const int nrows = rem < 32 * FM ? rem : 32 * FM;
   const int col0 = tc.cb * kMdBN;
-  const int K = p.m, achunks = K / 8, nk = (achunks + 7) / 8, kb = p.n / kMx4Block;
+  const int K = p.m, achunks = K / 8, kb = p.n / kMx4Block;
+  const int part_steps = (achunks + 7) / 8, nk = part_steps * PARTS;
+  auto in_part = [&](int kt) { return PARTS == 1 || kt < part_steps ? kt : kt - part_steps; };  // a step's number in its part
 
   // this thread's block of a step: weight row tid / 8, input features 32 (tid % 8) .. + 31; past the
   // last feature any block (its sums are not stored), past the last row one that is all finite
@@ -59,7 +71,7 @@ __device__ __forceinline__ bool mx4_dgrad_body(const Mx4Act& p, const UnitTile& 
   uint32_t sreg;
   uint32_t reach = 0;  // f16: the largest distance from the least scale that fits
   auto load_b = [&](int kt) __attribute__((always_inline)) {
-    const int r = kt * 64 + b_row;
+    const int r = in_part(kt) * 64 + b_row;
     const size_t at = w0 + static_cast<size_t>(r < K ? r : K - 1) * kb;
     breg = static_cast<const chunk_t*>(p.w)[at];
     sreg = p.w_scales[at];
@@ -69,7 +81,7 @@ __device__ __forceinline__ bool mx4_dgrad_body(const Mx4Act& p, const UnitTile& 
   const int turn = (b_col >> 2) | ((b_row & 1) << 1);  // part q goes out as q ^ turn
   const int b_to = b_row * 512 + (((4 * b_col) ^ kn_swizzle(b_row) ^ turn) << 4);
   auto write_b = [&](int kt) __attribute__((always_inline)) {
-    const uint32_t E = kt * 64 + b_row < K ? sreg : 127u;
+    const uint32_t E = in_part(kt) * 64 + b_row < K ? sreg : 127u;
     const float s = mx4_scale(E);
     reach = mx4_f16_reach(E) > reach ? mx4_f16_reach(E) : reach;
     chunk_t c = breg;
@@ -88,10 +100,11 @@ __device__ __forceinline__ bool mx4_dgrad_body(const Mx4Act& p, const UnitTile& 
 #pragma unroll
   for (int q = 0; q < kALoads; ++q) {
     const int r = (q * 8 + wv) * 8 + lane / 8;
-    a_row[q] = static_cast<const chunk_t*>(p.a) + static_cast<size_t>(row0 + (r < nrows ? r : 0)) * achunks;
+    a_row[q] = static_cast<const chunk_t*>(p.a) + static_cast<size_t>(row0 + (r < nrows ? r : 0)) * (achunks * PARTS);
   }
   auto issue_a = [&](int kt) __attribute__((always_inline)) {
-    const int at = kt * 8 + chunk < achunks ? kt * 8 + chunk : 0;  // past the row's end: cleared once landed
+    const int piece = in_part(kt) * 8 + chunk;
+    const int at = (piece < achunks ? piece : 0) + (PARTS == 1 || kt < part_steps ? 0 : achunks);  // past the row's end: cleared once landed
 #pragma unroll
     for (int q = 0; q < kALoads; ++q)
       if (q * 8 + wv < 4 * FM)  // uniform
@@ -143,8 +156,8 @@ __device__ __forceinline__ bool mx4_dgrad_body(const Mx4Act& p, const UnitTile& 
   auto publish = [&](int kt) __attribute__((always_inline)) {
     if (kt + 1 < nk) __builtin_amdgcn_s_waitcnt(wait_vm(2) & ~0xF00);
     else __builtin_amdgcn_s_waitcnt(wait_vm(0) & ~0xF00);
-    if ((kt + 1) * 8 > achunks) {
-      if (kt * 8 + chunk >= achunks) {
+    if ((in_part(kt) + 1) * 8 > achunks) {
+      if (in_part(kt) * 8 + chunk >= achunks) {
 #pragma unroll
         for (int q = 0; q < kALoads; ++q)
           if (q * 8 + wv < 4 * FM)
@@ -232,14 +245,13 @@ __device__ __forceinline__ bool mx4_dgrad_body(const Mx4Act& p, const UnitTile& 
         *reinterpret_cast<f32x4_t*>(slab + (lane & 15) * kMdSlabPitch + j * 64 + grp * 16) = acc[i][j];
       const float* back = reinterpret_cast<const float*>(slab + (lane >> 2) * kMdSlabPitch) + 8 * (lane & 3);
       const int row = wm * 16 * FM + i * 16 + (lane >> 2);
-      uint16_t* out = static_cast<uint16_t*>(p.out) + static_cast<size_t>(row0 + row) * p.n;
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         float v[8];
 #pragma unroll
         for (int q = 0; q < 8; ++q) v[q] = back[32 * h + q];
         const int c = col0 + wn * 64 + 32 * h + 8 * (lane & 3);
-        if (row < nrows && c < p.n) *reinterpret_cast<chunk_t*>(out + c) = pack<DT>(v);
+        if (row < nrows && c < p.n) mx4_dgrad_store<DT, PARTS>(p, static_cast<size_t>(row0 + row) * p.n + c, v);
       }
     }
   }
@@ -247,7 +259,7 @@ __device__ __forceinline__ bool mx4_dgrad_body(const Mx4Act& p, const UnitTile& 
 }
 
 // A tile whose weights f16 does not hold, 16 rows by 16 features of a wave at a time.
-__device__ __forceinline__ void mx4_dgrad_split(const Mx4Act& p, const UnitTile& tc) {
+__device__ __forceinline__ void mx4_dgrad_split(const Mx4Dgrad& p, const UnitTile& tc) {
   const int lane = lane_id(), wv = wave_in_block(), grp = lane >> 4, lrow = lane & 15;
   const int row0 = tc.offset + tc.unit0 * 32;
   const int rem = tc.rows - tc.unit0 * 32;
@@ -278,32 +290,38 @@ __device__ __forceinline__ void mx4_dgrad_split(const Mx4Act& p, const UnitTile&
       acc = mfma_16x16x32<kBF16>(w, lo, acc);
       acc = mfma_16x16x32<kBF16>(w, hi, acc);
     }
-    if (row < nrows)
-      *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + static_cast<size_t>(row0 + row) * p.n + col + 4 * grp) =
-          uint2{narrow2<kF16>(acc[0], acc[1]), narrow2<kF16>(acc[2], acc[3])};
+    const size_t at = static_cast<size_t>(row0 + row) * p.n + col + 4 * grp;
+    if (row < nrows) {
+      if (p.out_type == kF32) *reinterpret_cast<f32x4_t*>(static_cast<float*>(p.out) + at) = acc;
+      else *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + at) = uint2{narrow2<kF16>(acc[0], acc[1]), narrow2<kF16>(acc[2], acc[3])};
+    }
   }
 }
 
-template <int DT>
+template <int DT, int PARTS>
 __global__ __launch_bounds__(kMdThreads) __attribute__((amdgpu_waves_per_eu(2, 2))) void mx4_dgrad_kernel(
-    Mx4Act p, int col_blocks, int tile_grid) {
+    Mx4Dgrad p, int col_blocks, int tile_grid) {
   extern __shared__ __attribute__((aligned(1024))) char lds[];
   if (static_cast<int>(blockIdx.x) >= tile_grid) {
-    zero_unfilled(p, blockIdx.x - tile_grid, gridDim.x - tile_grid);
+    each_unfilled(p, blockIdx.x - tile_grid, gridDim.x - tile_grid, [&](int r) {
+      const size_t chunks = p.n / (p.out_type == kF32 ? 4 : 8);
+      chunk_t* o = static_cast<chunk_t*>(p.out) + static_cast<size_t>(r) * chunks;
+      for (size_t c = lane_id(); c < chunks; c += kWave) o[c] = chunk_t{0u, 0u, 0u, 0u};
+    });
     return;
   }
   const UnitTile tc = unit_tile<kMdUnits>(blockIdx.x, p.e, p.kept, p.offsets, col_blocks, kMdBand);
   if (tc.expert < 0) return;
   bool done = true;
   switch (tc.units) {
-    case 1: done = mx4_dgrad_body<DT, 1>(p, tc, lds); break;
-    case 2: done = mx4_dgrad_body<DT, 2>(p, tc, lds); break;
-    case 3: done = mx4_dgrad_body<DT, 3>(p, tc, lds); break;
-    case 4: done = mx4_dgrad_body<DT, 4>(p, tc, lds); break;
-    case 5: done = mx4_dgrad_body<DT, 5>(p, tc, lds); break;
-    case 6: done = mx4_dgrad_body<DT, 6>(p, tc, lds); break;
-    case 7: done = mx4_dgrad_body<DT, 7>(p, tc, lds); break;
-    default: done = mx4_dgrad_body<DT, 8>(p, tc, lds); break;
+    case 1: done = mx4_dgrad_body<DT, PARTS, 1>(p, tc, lds); break;
+    case 2: done = mx4_dgrad_body<DT, PARTS, 2>(p, tc, lds); break;
+    case 3: done = mx4_dgrad_body<DT, PARTS, 3>(p, tc, lds); break;
+    case 4: done = mx4_dgrad_body<DT, PARTS, 4>(p, tc, lds); break;
+    case 5: done = mx4_dgrad_body<DT, PARTS, 5>(p, tc, lds); break;
+    case 6: done = mx4_dgrad_body<DT, PARTS, 6>(p, tc, lds); break;
+    case 7: done = mx4_dgrad_body<DT, PARTS, 7>(p, tc, lds); break;
+    default: done = mx4_dgrad_body<DT, PARTS, 8>(p, tc, lds); break;
   }
   if constexpr (DT == kF16)
     if (!done) mx4_dgrad_split(p, tc);
@@ -320,10 +338,10 @@ bool mx4_dgrad_fits(const LayoutView& L, int m) {
   return mx4_dgrad_grid(L, m, &cb) <= most_workgroups(kMdThreads);
 }
 
-template <int DT>
-static hipError_t launch_dt(const LayoutView& L, const Mx4Act& p, hipStream_t stream) {
+template <int DT, int PARTS>
+static hipError_t launch_dt(const LayoutView& L, const Mx4Dgrad& p, hipStream_t stream) {
   static std::atomic<uint64_t> done{0};
-  auto kern = mx4_dgrad_kernel<DT>;
+  auto kern = mx4_dgrad_kernel<DT, PARTS>;
   const hipError_t err = allow_lds(reinterpret_cast<const void*>(kern), kMdLds, done);
   if (err != hipSuccess) return err;
   int64_t cb;
@@ -333,9 +351,10 @@ static hipError_t launch_dt(const LayoutView& L, const Mx4Act& p, hipStream_t st
   return hipGetLastError();
 }
 
-hipError_t launch_mx4_dgrad(const LayoutView& L, const Mx4Act& p, int dtype, hipStream_t stream) {
+hipError_t launch_mx4_dgrad(const LayoutView& L, const Mx4Dgrad& p, int dtype, hipStream_t stream) {
   if (p.rows == 0) return hipSuccess;
-  return dtype == kBF16 ? launch_dt<kBF16>(L, p, stream) : launch_dt<kF16>(L, p, stream);
+  if (p.parts == 2) return launch_dt<kBF16, 2>(L, p, stream);
+  return dtype == kBF16 ? launch_dt<kBF16, 1>(L, p, stream) : launch_dt<kF16, 1>(L, p, stream);
 }
 
 }  // namespace moe

@@ -83,12 +83,13 @@ struct ExpertActBackward {
   const void* grad_out;     // [rows, n]
   const void* preact;       // [rows, nz] (float32 if preact_f32), or null where nothing needs it
   const float* route_w;     // [s, k], or null
-  void* grad_preact;        // [rows, nz], or null
+  void* grad_preact;        // [rows, nz], in two parts [rows, 2, nz] bf16, or null
   void* grad_bias;          // [e, nz] (float32 if bias_f32), or null
   float* grad_w;            // [s, k], or null
   void* grad_residual;      // [rows, n], or null
   const int32_t *dst, *src, *kept, *offsets;
   int32_t s, e, k, n, nz, act;
+  int32_t parts;            // of grad_preact: 1 or 2
   int64_t rows;
   bool gated, bias_f32, preact_f32;
 };
@@ -131,8 +132,13 @@ hipError_t launch_mx4_tiles(const Mx4Act& p, int dtype, int col_blocks, int64_t 
 constexpr int kMx4StreamThreads = 256;
 hipError_t launch_mx4_stream(const Mx4Act& p, int dtype, int few, int col_blocks, int64_t grid, hipStream_t stream);
 // Its input gradient: out[r] = a[r] @ W[x] with W [e, m, n] (m weight rows, n inputs): the struct's
-// a = the gradient rows [rows, m], out [rows, n], nz = n; no epilogue.
-hipError_t launch_mx4_dgrad(const LayoutView& L, const Mx4Act& p, int dtype, hipStream_t stream);
+// a = the gradient rows [rows, m], or in two bf16 parts [rows, 2, m], out [rows, n], nz = n; no
+// epilogue.
+struct Mx4Dgrad : Mx4Act {
+  int32_t parts;            // of the gradient rows: 1, or 2 (bf16)
+  int32_t out_type;
+};
+hipError_t launch_mx4_dgrad(const LayoutView& L, const Mx4Dgrad& p, int dtype, hipStream_t stream);
 bool mx4_dgrad_fits(const LayoutView& L, int n);
 
 }  // namespace moe

@@ -447,6 +447,11 @@ moe_status_t moe_expert_gemm_act_ex(const moe_layout_t* layout, const void* a, i
  *   workspace: moe_expert_act_backward_workspace_bytes bytes, 256-byte aligned (may be NULL
  *   if grad_bias and grad_topk_w are; not kept after the call; calls that may overlap in
  *   time need one each).
+ * moe_expert_act_backward_parts with parts = 2: grad_preact is [rows, 2, nz] bf16 whatever dtype
+ * is, the bf16 value nearest to the float32 one and that nearest to what is left: their sum is off
+ * by at most 2^-17 of it, and it has float32's range (a finite value past bf16's largest has that
+ * as its first part, an infinity or NaN is all in the first). moe_mx4_expert_dgrad_ex takes it.
+ * With parts = 1 it is moe_expert_act_backward_ex.
  */
 size_t moe_expert_act_backward_workspace_bytes(const moe_layout_t* layout, int32_t n,
                                                int32_t gated);
@@ -462,6 +467,13 @@ moe_status_t moe_expert_act_backward_ex(const moe_layout_t* layout, const void* 
                                         const float* topk_w, void* grad_preact, moe_dtype_t bias_dtype,
                                         void* grad_bias, float* grad_topk_w, void* grad_residual,
                                         void* workspace, size_t workspace_bytes, void* stream);
+moe_status_t moe_expert_act_backward_parts(const moe_layout_t* layout, const void* grad_out,
+                                           const void* preact, moe_dtype_t preact_dtype, int32_t n,
+                                           moe_dtype_t dtype, int32_t activation, int32_t gated,
+                                           const float* topk_w, int32_t parts, void* grad_preact,
+                                           moe_dtype_t bias_dtype, void* grad_bias,
+                                           float* grad_topk_w, void* grad_residual, void* workspace,
+                                           size_t workspace_bytes, void* stream);
 
 /*
  * Input-row gradient of moe_expert_gemm_act, from its epilogue's grad_preact [rows, nz]:
@@ -531,10 +543,19 @@ moe_status_t moe_mx4_expert_gemm(const moe_layout_t* layout, const void* a, cons
  * bits the gradient is taken to pass unchanged. grad_preact and grad_a of dtype (bf16 or f16),
  * m a multiple of 32, nz of 8; grad_a may not overlap grad_preact or the weights. The gradient of
  * gathered token rows is moe_dispatch_backward of grad_a.
+ *
+ * moe_mx4_expert_dgrad_ex keeps more: with parts = 2, grad_preact is [rows, 2, nz], both parts of
+ * moe_expert_act_backward_parts (dtype MOE_BF16; twice the products), with 1 as above; grad_a is
+ * rounded once to grad_a_dtype, or with MOE_F32 not at all (16-bit rows: MOE_F32 or dtype; rows in
+ * parts: any type), so that moe_dispatch_backward sums a token's rows unrounded.
  */
 moe_status_t moe_mx4_expert_dgrad(const moe_layout_t* layout, const void* grad_preact,
                                   const void* w_codes, const uint8_t* w_scales, int32_t m,
                                   int32_t nz, moe_dtype_t dtype, void* grad_a, void* stream);
+moe_status_t moe_mx4_expert_dgrad_ex(const moe_layout_t* layout, const void* grad_preact,
+                                     int32_t parts, const void* w_codes, const uint8_t* w_scales,
+                                     int32_t m, int32_t nz, moe_dtype_t dtype,
+                                     moe_dtype_t grad_a_dtype, void* grad_a, void* stream);
 
 /*
  * Input-row gradient of moe_expert_gemm ([DS-8213] first commit: the backward replays the
