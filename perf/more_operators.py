@@ -365,9 +365,9 @@ def _own_block(st):
 def _own_step(st):
     import combine_moe_gate_amd.autograd as A
     c, L = st["case"], st["layout"]
-    # the gradient of the z that the forward used, in 32 bits as inside any operator here
+    # the gradient of the z that the forward used, and no rounding on its way to x: as inside any operator here
     h = A.expert_linear_mx4(st["x"], st["up"], L, bias=st["up_bias"], act=c["act"], gated=True, quantize_rows=c["quantized"],
-                            preact_dtype=torch.float32)
+                            preact_dtype=torch.float32, grad_dtype=torch.float32)
     o = A.expert_linear_mx4(h, st["down"], L, bias=st["down_bias"], gather=False, quantize_rows=c["quantized"])
     return _with_grads(st, A.combine(o, st["w"].float(), L))
 
