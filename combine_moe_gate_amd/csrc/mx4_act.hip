@@ -7,9 +7,9 @@
 //
 // 4-bit rows meet 4-bit weights in v_mfma_scale_f32_16x16x128_f8f6f4, which takes the scales. For
 // bf16 rows the codes are widened to bf16 with their scale, which is exact. For f16 rows they are
-// widened to f16 where the scales of the step in hand allow that exactly (2^-23 to 2^13, what
-// weights have in earnest); elsewhere each row value is split into two bf16 values, the upper 8
-// bits of its 11 and the rest, both products exact again.
+// widened to f16 where the scales of the step in hand allow that exactly (2^-23 to 2^13, which is what
+// weights in use have, and any over zeros); elsewhere each row value is split into two bf16 values, the
+// upper 8 bits of its 11 and the rest, both products exact again.
 //
 // Three kernels, chosen by the rows an expert has on average, the workgroups there would be and the
 // scales' alignment (mx4_shape() below): the tiles of mx4_tile.hip, the streams of mx4_stream.hip, and
@@ -122,6 +122,12 @@ __global__ __launch_bounds__(kMxFewThreads, kOcc) void mx4_few_kernel(Mx4Act p, 
 #pragma unroll
         for (int j = 0; j < FB; ++j) fits = fits && mx4_fits_f16(sb[d][j]);
         split = !__all(fits);
+        if (split) {  // uniform
+          fits = true;
+#pragma unroll
+          for (int j = 0; j < FB; ++j) fits = fits && (mx4_fits_f16(sb[d][j]) || mx4_zeros(fb[d][j]));
+          split = !__all(fits);
+        }
       }
       if (RT == kBF16 || !split) {
 #pragma unroll

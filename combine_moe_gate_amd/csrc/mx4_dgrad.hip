@@ -3,8 +3,9 @@
 // For each placed row r of expert x: out[r] = a[r] @ W[x], a the 16-bit gradient rows [rows, nz], W
 // [nz, m] the values the codes stand for. The sum runs along the weights' rows, each with scales of
 // its own, so the weights are widened on their way to LDS: to bf16, which is exact, or for f16 gradients
-// to f16, exact for scales from 2^-23 to 2^13. A tile that met others is formed again from gradients in
-// two parts (split_f16) and bf16 weights, straight from memory: far slower, and in few registers.
+// to f16, exact for scales from 2^-23 to 2^13. A tile that met others, over values that are not zeros, is
+// formed again from gradients in two parts (split_f16) and bf16 weights, straight from memory: slower, and
+// in few registers.
 // Gradient rows that come in two bf16 parts are multiplied part by part, the second's steps after the
 // first's, on the same weights: twice the steps. Results are rounded to 16 bits or stay float32.
 //
@@ -219,18 +220,29 @@ __device__ __forceinline__ bool mx4_dgrad_body(const Mx4Dgrad& p, const UnitTile
     }
   }
 
-  int* votes = reinterpret_cast<int*>(lds + kMdVotes);
-  if (DT == kF16) {
-    const bool misfit = __any(reach > kMx4F16Reach);
-    if (lane == 0) votes[wv] = misfit;
+  if constexpr (DT == kF16) {
+    int* votes = reinterpret_cast<int*>(lds + kMdVotes);
+    auto vote = [&](bool mine) {
+      if (lane == 0) votes[wv] = mine;
+      __syncthreads();
+      int any = 0;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) any |= votes[i];
+      return __builtin_amdgcn_readfirstlane(any) != 0;
+    };
+    if (vote(__any(reach > kMx4F16Reach))) {
+      // the sums are right if only zeros lie under the scales that do not fit: a thread a weight row looks at
+      // the tile's blocks. 65536 routes, 128 experts, 4096 -> 4096: 2.03 ms without zeros, 2.03 with a block of
+      // them in 256 weight rows, 2.21 with a quarter of the rows zero; with the codes looked at in the loop 2.46.
+      const int first = col0 / kMx4Block, count = kb - first < kMdBN / kMx4Block ? kb - first : kMdBN / kMx4Block;
+      bool bad = false;
+      for (int r = tid; r < K; r += kMdThreads)
+        bad = bad || mx4_misfits_f16(static_cast<const chunk_t*>(p.w), p.w_scales, (static_cast<size_t>(tc.expert) * K + r) * kb + first, count);
+      __syncthreads();  // every wave has read the votes
+      if (vote(__any(bad))) return false;
+    }
   }
   __syncthreads();
-  if constexpr (DT == kF16) {
-    int any = 0;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) any |= votes[i];
-    if (__builtin_amdgcn_readfirstlane(any)) return false;
-  }
 
   // each 16-row tile's sums through one of the wave's two slabs: lane l holds row l % 16, features
   // 16 j + 4 (l / 16) .. + 3 of its 64; it takes back row l / 4, features 8 (l % 4) .. + 7 of each 32
@@ -258,7 +270,8 @@ __device__ __forceinline__ bool mx4_dgrad_body(const Mx4Dgrad& p, const UnitTile
   return true;
 }
 
-// A tile whose weights f16 does not hold, 16 rows by 16 features of a wave at a time.
+// A tile whose weights f16 does not hold, 16 rows by 16 features of a wave at a time: 56 ms where the loop takes
+// 2.03, were all tiles such.
 __device__ __forceinline__ void mx4_dgrad_split(const Mx4Dgrad& p, const UnitTile& tc) {
   const int lane = lane_id(), wv = wave_in_block(), grp = lane >> 4, lrow = lane & 15;
   const int row0 = tc.offset + tc.unit0 * 32;

@@ -24,6 +24,32 @@ __device__ __forceinline__ f32x4_t mfma_16x16x32(const chunk_t& a, const chunk_t
 constexpr uint32_t kMx4F16Reach = 36u;
 __device__ __forceinline__ uint32_t mx4_f16_reach(uint32_t E) { return E - 104u; }
 __device__ __forceinline__ bool mx4_fits_f16(uint32_t E) { return mx4_f16_reach(E) <= kMx4F16Reach; }
+// Zeros are f16 values under any scale (the quantiser gives a block of them 0; under 255 they are widened to
+// NaN, which f16 holds too). The scales alone are looked at first: codes matter only where they do not fit.
+__device__ __forceinline__ bool mx4_zeros(const chunk_t& codes) { return ((codes.x | codes.y | codes.z | codes.w) & 0x77777777u) == 0u; }
+
+// Whether blocks `first` .. + count - 1 hold values that f16 does not.
+__device__ __forceinline__ bool mx4_misfits_f16(const chunk_t* codes, const uint8_t* scales, size_t first, int count) {
+  typedef uint64_t __attribute__((aligned(1), may_alias)) bytes8_t;
+  bool bad = false;
+  for (int at = 0; at < count; at += 32) {
+    uint64_t E[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      E[i] = 0x7f7f7f7f7f7f7f7full;
+      if (at + 8 * i + 8 <= count) {
+        E[i] = *reinterpret_cast<const bytes8_t*>(scales + first + at + 8 * i);
+      } else {
+        for (int b = 0; at + 8 * i + b < count; ++b)
+          E[i] = (E[i] & ~(255ull << (8 * b))) | static_cast<uint64_t>(scales[first + at + 8 * i + b]) << (8 * b);
+      }
+    }
+#pragma unroll
+    for (int b = 0; b < 32; ++b)
+      if (!mx4_fits_f16(static_cast<uint32_t>(E[b / 8] >> (8 * (b % 8))) & 255u)) bad = bad || !mx4_zeros(codes[first + at + b]);
+  }
+  return bad;
+}
 
 // Eight f16 values as the sums of two bf16 values each: the upper 8 of the 11 significant bits, and
 // the other 3. An infinity or NaN is all in the first.

@@ -215,7 +215,11 @@ __global__ __launch_bounds__(kMsThreads) void mx4_stream_kernel(Mx4Act p, int co
           for (int q = 0; q < 4; ++q)
             a[i][q] = *reinterpret_cast<const chunk_t*>(st + (16 * i + lrow) * 512 + (((4 * (4 * h + grp) + q) ^ a_swz) << 4));
         bool split = false;
-        if constexpr (RT == kF16) split = !__all(mx4_fits_f16(sb[0] & 255u) && mx4_fits_f16(sb[1] & 255u));
+        if constexpr (RT == kF16) {
+          const bool fit0 = mx4_fits_f16(sb[0] & 255u), fit1 = mx4_fits_f16(sb[1] & 255u);
+          split = !__all(fit0 && fit1);
+          if (split) split = !__all((fit0 || mx4_zeros(codes[0])) && (fit1 || mx4_zeros(codes[1])));  // uniform
+        }
         constexpr int kWide = RT == kF16 ? kF16 : kBF16;
         if (!split) {
 #pragma unroll

@@ -439,14 +439,29 @@ __device__ __forceinline__ bool mx4_tile_body(const Mx4Act& p, const UnitTile& t
   float* row_weight = reinterpret_cast<float*>(lds + Lds::kRows + Lds::kBM * 4);
   f32x4_t acc[FM][FN];
   const bool misfit = mx4_tile_products<RT, FM>(p, tc, lds, acc);
-  if constexpr (RT == kF16) {  // no weights in earnest ask for this: what it costs them is the vote
+  if constexpr (RT == kF16) {  // weights in use have zeros at most under such scales: what it costs others is the vote
     int* votes = reinterpret_cast<int*>(lds + Lds::kVotes);
-    if (lane == 0) votes[wv] = misfit;
-    __syncthreads();
-    int any = 0;
+    auto vote = [&](bool mine) {
+      if (lane == 0) votes[wv] = mine;
+      __syncthreads();
+      int any = 0;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) any |= votes[i];
-    if (__builtin_amdgcn_readfirstlane(any)) return false;
+      for (int i = 0; i < 8; ++i) any |= votes[i];
+      return __builtin_amdgcn_readfirstlane(any) != 0;
+    };
+    if (vote(misfit)) {
+      // the sums are right if only zeros lie under the scales that do not fit. Two threads a weight row look, half
+      // a row each: of the same product 1.96 ms with a block of zeros in each tile, 1.99 with a quarter of the
+      // weight rows zero. Looking at the codes within the loop would take registers from it: 2.00 with or without.
+      const int kb = p.m / kMx4Block, half = (kb + 1) / 2, from = (threadIdx.x % 2) * half;
+      const int R = threadIdx.x / 2;  // staged row, as the tile stages them: gated, 32 gate rows and their up rows
+      const int f = p.gated ? col0 + R / 64 * 32 + R % 32 : col0 + R;
+      const int row = (f < p.n ? f : p.n - 1) + (p.gated && R % 64 >= 32 ? p.n : 0);
+      const bool bad = mx4_misfits_f16(static_cast<const chunk_t*>(p.w), p.w_scales,
+                                       (static_cast<size_t>(x) * p.nz + row) * kb + from, kb - from < half ? kb - from : half);
+      __syncthreads();  // every wave has read the votes
+      if (vote(__any(bad))) return false;
+    }
   }
 
   // epilogue: each 16-row tile's sums through one of the wave's two slabs. Lane l holds token
@@ -498,10 +513,10 @@ __device__ __forceinline__ bool mx4_tile_body(const Mx4Act& p, const UnitTile& t
 }
 
 // A tile of f16 rows whose weights f16 does not hold: each row value in two parts (split_f16) times the
-// weights in bf16, 16 rows by 64 weight rows of a wave at a time, straight from memory. Several times
-// slower than the tile's own loop, in few registers: a second loop of that kind, next to the first,
-// would take registers from it (8192 rows of 4096: 2.5 ms where 2.0 are). Only weights with scales below
-// 2^-23 or above 2^13 come here.
+// weights in bf16, 16 rows by 64 weight rows of a wave at a time, straight from memory, in few registers. Seven
+// times slower than the tile's own loop (8192 tokens, 8 of 128 experts, 4096 -> 2 x 2048: 13.2 ms where that takes
+// 1.92): a second loop of that kind, next to the first, would take registers from it (2.5 ms where 2.0 are).
+// Only tiles with values, other than zeros, under scales below 2^-23 or above 2^13 come here.
 template <int DT>
 __device__ __forceinline__ void mx4_tile_split(const Mx4Act& p, const UnitTile& tc, char* lds) {
   using Lds = MtLds<kF16>;
