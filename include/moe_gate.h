@@ -490,8 +490,8 @@ moe_status_t moe_expert_act_dgrad(const moe_layout_t* layout, const void* grad_p
 /*
  * Microscaled 4-bit floating point. A row is cut into blocks of 32 values. A block has a scale
  * byte E, standing for 2^(E - 127), 255 for "not a number"; a value has four bits: a sign (8)
- * and one of 0, 0.5, 1, 1.5, 2, 3, 4, 6 (0 to 7). It stands for their product as a float32: a
- * power of two past float32's range (E = 254 with codes above 1) is infinite.
+ * and one of 0, 0.5, 1, 1.5, 2, 3, 4, 6 (0 to 7). It stands for their product as a float32; past
+ * that type's range it is infinite: 4 and 6 under E = 253, 2 to 6 under E = 254.
  *   codes  [rows, m / 2] bytes, two values to a byte, the first in the low half; 16-byte aligned
  *   scales [rows, m / 32] bytes, any alignment
  * m is a multiple of 32 (MOE_ERR_MISALIGNED otherwise).
