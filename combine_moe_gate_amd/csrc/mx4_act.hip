@@ -256,10 +256,26 @@ struct Mx4Shape {
 //   16, 1024 x 4096                 512    154    100    117         107     66     51     45    (176)
 //   8, 512 x 512                    4000    59     50     29          42     32     24     20    (238)
 // Rows that are no multiple of 128 elements, or unaligned scales, take this file's kernel in place of a
-// stream: 16 experts, 576 x 544, mean 125 in 9.1 and 7.2 (tiles 19 and 12). It takes 32 rows at a time,
-// of f16 16: beside more, the split form does not fit the registers (25 us where 32 rows take 39).
+// stream (16 experts, 576 x 544, mean 125 in 9.1 and 7.2, tiles 19 and 12). It takes 32 rows at a time, of f16
+// 16: beside more, the split form does not fit the registers (25 us where 32 rows take 39). As an expert's rows
+// pass that its time doubles, and the tiles' grows little; of short rows its start costs less. this / tiles:
+//   experts, weight rows x length   mean        bf16         f16        4-bit
+//   128, 2880 x 2880                0.75    107 / 167    103 / 180    96 / 94
+//   128, 2880 x 2880                8       204 / 263    199 / 280   186 / 164
+//   128, 2880 x 2880                16      243 / 265    280 / 281   207 / 166
+//   128, 2880 x 2880                24      285 / 270    368 / 285   227 / 170
+//   128, 2880 x 2880                32      388 / 279    432 / 291   297 / 174
+//   64, 2880 x 1440                 16       66 / 71      86 / 79     56 / 41
+//   64, 2880 x 1440                 24       79 / 74     111 / 80     61 / 41
+//   128, 1088 x 544                 16       26 / 38      40 / 41     21 / 24
+//   128, 1088 x 544                 24       29 / 38      52 / 42     24 / 24
+//   128, 1088 x 544                 32       38 / 41      63 / 44     32 / 26
+//   60, 1408 x 288                  24       13 / 19      24 / 21     12 / 14
+// With streams 2816 x 2816 of these takes 51, 112, 130, 133 and 163 in bf16: rows of any length, or scales at any
+// address, cost up to twice that.
 constexpr int kMx4Mean = 72;                         // mean rows from which the tiles are worth while
 constexpr int64_t kMx4Tiles16 = 200, kMx4Tiles4 = 128;
+constexpr int kMx4Long = 1024;                       // elements of a row that is not short
 static Mx4Shape mx4_shape(const LayoutView& L, const Mx4Act& p, int dtype) {
   const bool q = p.a_scales != nullptr;
   auto shape = [&](Mx4Form form, int few, int height, int cols) {
@@ -278,7 +294,8 @@ static Mx4Shape mx4_shape(const LayoutView& L, const Mx4Act& p, int dtype) {
     const int few = mean <= (q ? 8 : 12) ? 1 : q && mean > 24 ? 4 : 2;
     return shape(Mx4Form::stream, few, 16 * few, 128);
   }
-  if (many && (q || mean > 32)) return large;
+  const bool longer = p.m >= kMx4Long;
+  if (many && mean > (q ? (longer ? 0 : 24) : dtype == kF16 ? 16 : longer ? 20 : 32)) return large;
   const int few = !q && dtype == kF16 ? 1 : 2;
   // 64 weight rows, so that a 4-bit block of 32 gated results lies in one workgroup
   return shape(Mx4Form::few, few, 16 * few, 64);
