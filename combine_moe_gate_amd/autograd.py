@@ -493,7 +493,10 @@ def expert_linear_mx4(x: torch.Tensor, weights, layout: Layout, bias: torch.Tens
     """expert_linear on frozen 4-bit weights, the pair (codes [e, n, m / 2], scales [e, n, m / 32]) of
     moe_mx4_quantize (gated: [e, 2n, ..]): gradients reach x, bias, w and residual, for tuning what stands
     around the experts. quantize_rows: x is rounded to 4 bits before the product as well, and the gradient
-    passes through that rounding as it is.
+    passes through that rounding as it is. Between two projections rows are in x's dtype, since a gradient
+    passes there: with quantize_rows a hidden row is rounded to 16 bits and then to 4, where serving with
+    moe_mx4_expert_gemm(quantize_out=True) rounds the float32 row to 4 once. The two may differ by a code
+    where the 16-bit value lies on a border between two.
 
     grad_dtype: between the epilogue's backward and x's gradient, values are rounded to x's dtype (None), or
     with float32 kept in 16 bits of significance (two bf16 parts) and summed over a token's routes in float32: x's

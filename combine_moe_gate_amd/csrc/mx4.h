@@ -16,6 +16,8 @@
 
 namespace moe {
 
+typedef float f32x4_t __attribute__((ext_vector_type(4)));
+
 constexpr int kMx4 = 3;       // beside the element types: rows of 4-bit values
 constexpr int kMx4Block = 32;
 

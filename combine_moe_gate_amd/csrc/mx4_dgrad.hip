@@ -17,7 +17,7 @@
 //
 // Measured, 49152 routes, 64 experts: 2816 -> 2048 561 us and 2048 -> 1408 326 us (1.01 and 0.87 PFLOP/s;
 // the product with bf16 weights takes 600 and 370); rows in parts, to float32, 1071 and 639. Bound by
-// the main loop: a loop of its matrix instruction alone reaches 1.3.
+// the main loop, matrix units busy 38 to 44%: its matrix instruction alone reaches 1.95.
 #include <atomic>
 
 #include "mx4_product.h"

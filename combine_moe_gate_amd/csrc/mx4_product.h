@@ -7,8 +7,6 @@
 
 namespace moe {
 
-typedef float f32x4_t __attribute__((ext_vector_type(4)));
-
 template <int DT>
 __device__ __forceinline__ f32x4_t mfma_16x16x32(const chunk_t& a, const chunk_t& b, f32x4_t c) {
   if constexpr (DT == kBF16)

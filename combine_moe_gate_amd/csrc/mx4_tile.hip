@@ -20,10 +20,10 @@
 // the matrix instructions take them: a lane's word holds both halves' scales of a row and of the row 16
 // further on, its next MFMA tile, and an instruction names the byte.
 //
-// Measured, 8192 tokens, 8 of 128 experts, 4096 -> 2 x 2048 gated: 4-bit rows 746 us (2.9 PFLOP/s; a
-// loop of the scaled instruction alone reaches 4.5, this one's without its loads and epilogue 4.2);
-// without the loop's loads 130 us less, without the epilogue 58. bf16 rows 1.95 ms (1.13 PFLOP/s,
-// where a loop of their instruction alone reaches 1.3).
+// Measured, 8192 tokens, 8 of 128 experts, 4096 -> 2 x 2048 gated: 4-bit rows 746 us (2.9 PFLOP/s, matrix
+// units busy 32%; the loop without its loads and epilogue 4.2, the scaled instruction alone on random codes
+// 6.9); without the loop's loads 130 us less, without the epilogue 58. bf16 rows 1.94 ms (1.13 PFLOP/s, busy
+// 48%, where their instruction alone reaches 1.95 and a large library product 1.5).
 #include <atomic>
 
 #include "mx4_product.h"
