@@ -257,21 +257,22 @@ struct Mx4Shape {
 //   8, 512 x 512                    4000    59     50     29          42     32     24     20    (238)
 // Rows that are no multiple of 128 elements, or unaligned scales, take this file's kernel in place of a
 // stream (16 experts, 576 x 544, mean 125 in 9.1 and 7.2, tiles 19 and 12). It takes 32 rows at a time, of f16
-// 16: beside more, the split form does not fit the registers (25 us where 32 rows take 39). As an expert's rows
-// pass that its time doubles, and the tiles' grows little; of short rows its start costs less. this / tiles:
-//   experts, weight rows x length   mean        bf16         f16        4-bit
-//   128, 2880 x 2880                0.75    107 / 167    103 / 180    96 / 94
-//   128, 2880 x 2880                8       204 / 263    199 / 280   186 / 164
-//   128, 2880 x 2880                16      243 / 265    280 / 281   207 / 166
-//   128, 2880 x 2880                24      285 / 270    368 / 285   227 / 170
-//   128, 2880 x 2880                32      388 / 279    432 / 291   297 / 174
-//   64, 2880 x 1440                 16       66 / 71      86 / 79     56 / 41
-//   64, 2880 x 1440                 24       79 / 74     111 / 80     61 / 41
-//   128, 1088 x 544                 16       26 / 38      40 / 41     21 / 24
-//   128, 1088 x 544                 24       29 / 38      52 / 42     24 / 24
-//   128, 1088 x 544                 32       38 / 41      63 / 44     32 / 26
-//   60, 1408 x 288                  24       13 / 19      24 / 21     12 / 14
-// With streams 2816 x 2816 of these takes 51, 112, 130, 133 and 163 in bf16: rows of any length, or scales at any
+// rows 16 where experts have few: beside 32, the split form leaves registers for one K step in flight, not
+// two. As an expert's rows pass that its time doubles, and the tiles' grows little; of short rows its start costs
+// less. With 16 rows / with 32 / the tiles:
+//   experts, weight rows x length   mean          bf16               f16               4-bit
+//   128, 2880 x 2880                1        121 / 128 / 174    125 / 140 / 185    117 / 113 / 105
+//   128, 2880 x 2880                8        197 / 205 / 263    199 / 216 / 280    195 / 187 / 164
+//   128, 2880 x 2880                16       304 / 243 / 265    280 / 236 / 281    292 / 207 / 166
+//   128, 2880 x 2880                24       421 / 285 / 270    374 / 265 / 285    403 / 228 / 170
+//   128, 2880 x 2880                32       459 / 390 / 279    432 / 351 / 291    445 / 294 / 174
+//   64, 2880 x 1440                 16        72 / 69 / 71       82 / 75 / 79       69 / 56 / 41
+//   64, 2880 x 1440                 24        94 / 76 / 74      109 / 81 / 80       89 / 60 / 41
+//   128, 1088 x 544                 8         21 / 23 / 37       29 / 32 / 41       19 / 20 / 23
+//   128, 1088 x 544                 24        38 / 29 / 38       52 / 37 / 42       30 / 24 / 24
+//   128, 1088 x 544                 32        45 / 39 / 41       63 / 49 / 44       36 / 33 / 26
+//   60, 1408 x 288                  24        17 / 13 / 19       23 / 16 / 21       13 / 11 / 14
+// With streams 2816 x 2816 of these takes 73, 112, 130, 133 and 163 in bf16: rows of any length, or scales at any
 // address, cost up to twice that.
 constexpr int kMx4Mean = 72;                         // mean rows from which the tiles are worth while
 constexpr int64_t kMx4Tiles16 = 200, kMx4Tiles4 = 128;
@@ -295,8 +296,8 @@ static Mx4Shape mx4_shape(const LayoutView& L, const Mx4Act& p, int dtype) {
     return shape(Mx4Form::stream, few, 16 * few, 128);
   }
   const bool longer = p.m >= kMx4Long;
-  if (many && mean > (q ? (longer ? 0 : 24) : dtype == kF16 ? 16 : longer ? 20 : 32)) return large;
-  const int few = !q && dtype == kF16 ? 1 : 2;
+  if (many && mean > (q ? (longer ? 0 : 24) : longer ? 20 : 32)) return large;
+  const int few = !q && dtype == kF16 && mean <= 12 ? 1 : 2;
   // 64 weight rows, so that a 4-bit block of 32 gated results lies in one workgroup
   return shape(Mx4Form::few, few, 16 * few, 64);
 }
@@ -328,8 +329,9 @@ hipError_t launch_mx4_act(const LayoutView& L, const Mx4Act& p, int dtype, hipSt
   if (p.a_scales != nullptr)
     return dtype == kBF16 ? launch_few<kMx4, kBF16, 2, 2, 3>(p, col_blocks, grid, stream)
                           : launch_few<kMx4, kF16, 2, 2, 3>(p, col_blocks, grid, stream);
-  return dtype == kBF16 ? launch_few<kBF16, kBF16, 2, 1, 3>(p, col_blocks, grid, stream)
-                        : launch_few<kF16, kF16, 1, 2, 2>(p, col_blocks, grid, stream);
+  if (dtype == kBF16) return launch_few<kBF16, kBF16, 2, 1, 3>(p, col_blocks, grid, stream);
+  return a.few == 1 ? launch_few<kF16, kF16, 1, 2, 2>(p, col_blocks, grid, stream)
+                    : launch_few<kF16, kF16, 2, 1, 2>(p, col_blocks, grid, stream);
 }
 
 }  // namespace moe
